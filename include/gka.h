@@ -290,6 +290,131 @@ int gka_solver_study(const void *q, const void *k, const float *beta, const floa
                      int H, int T, int D, gka_dtype dt, float a, int r, int chunk, int solver,
                      float *resid, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Gated linear recurrence: the layer's value state read by the query itself,
+ * without the ridge solve (ai.info page, Methodology: the same gated fading
+ * recurrence and chunk-wise form; the linear-attention layers the paper compares
+ * against are of this kind).  Per (batch, head), with a scale c:
+ *     M_t = beta_t M_{t-1} + g_t v_t k_t^T,   o_t = c M_t q_t,
+ * M_{-1} the initial state (zero where it is NULL).  q and k are used as given.
+ * The sequence may have any length T >= 0; beta_t = 0 starts a new document.
+ *   q, k, v     [B, H, T, D] in `dt`, finite (a chunk's outputs are sums that also
+ *               run over its later tokens with weight zero)
+ *   beta        [B, H, T] fp32 in [0, 1];  gate nullable fp32 [B, H, T] in [0, 1]
+ *   o           [B, H, T, D] in `dt` (written; no input's memory)
+ *   initial_state, final_state   nullable fp32 [B, H, D, D] (M maps keys to
+ *               values); final_state (written) is the state after the last token
+ *               and may be initial_state itself; T = 0 copies the one to the other
+ *   workspace   at least gka_linear_forward_workspace_bytes(), 256-byte aligned
+ *               (0 bytes for some sizes: then NULL will do)
+ * B*H is at most 65535.  The fp32 state is carried in fp32; with bf16 inputs and
+ * D = 128 the products run on the tensor cores.
+ */
+size_t gka_linear_forward_workspace_bytes(int B, int H, int T, int D, gka_dtype dt);
+int gka_linear_forward(const void *q, const void *k, const void *v, const float *beta,
+                       const float *gate, void *o, int B, int H, int T, int D, gka_dtype dt,
+                       float scale, const float *initial_state, float *final_state,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of the recurrence, in place on the fp32 state [B, H, D, D]:
+ *   M <- beta M + g v k^T,  o = c M q.   q, k, v, o [B, H, D]; beta, gate [B, H].
+ */
+int gka_linear_decode_step(float *state, const void *q, const void *k, const void *v,
+                           const float *beta, const float *gate, void *o, int B, int H, int D,
+                           gka_dtype dt, float scale, void *stream);
+
+/*
+ * Gradients of gka_linear_forward (exact, of every input).  With R_t = dL/dM_t,
+ *   R_t = beta_{t+1} R_{t+1} + c dout_t q_t^T   (R_{T-1} also gets dfinal_state),
+ *   dq_t = c M_t^T dout_t,  dk_t = g_t R_t^T v_t,  dv_t = g_t R_t k_t,
+ *   dgate_t = v_t^T R_t k_t,  dbeta_t = <R_t, M_{t-1}>,  dinitial_state = beta_0 R_0.
+ *   dout          [B, H, T, D] in `dt`, finite
+ *   initial_state, dfinal_state   nullable fp32 [B, H, D, D]
+ *   dq, dk, dv    [B, H, T, D] in `dt`; dbeta [B, H, T] fp32 (written)
+ *   dgate         [B, H, T] fp32 (written); non-NULL exactly when gate is
+ *   dinitial_state  nullable fp32 [B, H, D, D] (written); may be dfinal_state itself
+ *   workspace     at least gka_linear_backward_workspace_bytes(), 256-byte aligned
+ * Decays below 2^-60 (a reset's 0 among them) count as 2^-60: dbeta stays exact
+ * there, and every other gradient is off by less than 2^-60 of what was written.
+ */
+size_t gka_linear_backward_workspace_bytes(int B, int H, int T, int D, gka_dtype dt);
+int gka_linear_backward(const void *q, const void *k, const void *v, const float *beta,
+                        const float *gate, const void *dout, const float *initial_state,
+                        const float *dfinal_state, void *dq, void *dk, void *dv, float *dbeta,
+                        float *dgate, float *dinitial_state, int B, int H, int T, int D,
+                        gka_dtype dt, float scale, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* Rows [B, T, heads, D] (or scalars [B, T, heads]) at element strides: a view of a
+ * projection's output.  Rows themselves are contiguous; their pointer and the
+ * strides in bytes are multiples of 16 (scalars: no condition). */
+typedef struct {
+    const void *ptr;
+    long long stride_b, stride_t, stride_h;
+} gka_strided;
+
+/*
+ * Before the layer (pith.science page, Fig. 2: the block l2-normalises q and k):
+ * token-major projections to the layer's inputs.
+ *   q_out = q (|q|^2 + eps)^-1/2,  k_out = k (|k|^2 + eps)^-1/2,  v_out = v,
+ *   beta = sigmoid(beta_logit + beta_bias_h),  gate = sigmoid(gate_logit + gate_bias_h)
+ *   q             [B, T, H, D];  k, v [B, T, Hk, D] with Hk dividing H: key/value
+ *                 head h serves the H / Hk heads of its group
+ *   beta_logit    [B, T, H] in `dt`;  gate_logit nullable (struct pointer NULL)
+ *   beta_bias, gate_bias   nullable fp32 [H]
+ *   lengths       nullable int32 [B]: tokens t >= lengths[b] are padding, whose
+ *                 memory is not read; they get zero rows, beta = 1 and gate = 0, so
+ *                 that they write nothing and the state passes them unchanged
+ *   q_out, k_out, v_out   [B, H, T, D] in `dt` (written);  beta [B, H, T] fp32 (written)
+ *   gate          [B, H, T] fp32 (written); non-NULL exactly when gate_logit or
+ *                 lengths is (1 where only lengths is)
+ */
+int gka_block_in_forward(const gka_strided *q, const gka_strided *k, const gka_strided *v,
+                         const gka_strided *beta_logit, const gka_strided *gate_logit,
+                         const float *beta_bias, const float *gate_bias, const int *lengths,
+                         void *q_out, void *k_out, void *v_out, float *beta, float *gate, int B,
+                         int T, int H, int Hk, int D, gka_dtype dt, float eps, void *stream);
+
+/*
+ * Gradients of gka_block_in_forward from dq_out, dk_out, dv_out [B, H, T, D] and
+ * dbeta, dgate [B, H, T] (dgate and dgate_logit non-NULL exactly when gate_logit is):
+ *   dq [B, T, H, D], dk, dv [B, T, Hk, D] (summed over each group), dbeta_logit,
+ *   dgate_logit [B, T, H], all dense in `dt` (written; zero at padding, where nothing
+ *   is read); dbeta_bias, dgate_bias nullable fp32 [H] (written).
+ */
+size_t gka_block_in_backward_workspace_bytes(int B, int T, int H, int Hk, int D, gka_dtype dt);
+int gka_block_in_backward(const gka_strided *q, const gka_strided *k,
+                          const gka_strided *beta_logit, const gka_strided *gate_logit,
+                          const float *beta_bias, const float *gate_bias, const int *lengths,
+                          const void *dq_out, const void *dk_out, const void *dv_out,
+                          const float *dbeta, const float *dgate, void *dq, void *dk, void *dv,
+                          void *dbeta_logit, void *dgate_logit, float *dbeta_bias,
+                          float *dgate_bias, int B, int T, int H, int Hk, int D, gka_dtype dt,
+                          float eps, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * After the layer: residual, RMS norm, gate and the way back to token-major rows.
+ *   u = o + skip_h v,   y = u (|u|^2 / D + eps)^-1/2 * w * silu(z)
+ *   o, v   [B, H, T, D] in `dt`; v nullable, and skip (fp32 [H]) non-NULL exactly when v is
+ *   z      [B, T, H, D] at strides; nullable (no gate)
+ *   w      fp32 [D];   y [B, T, H, D] dense in `dt` (written)
+ */
+int gka_block_out_forward(const void *o, const void *v, const gka_strided *z, const float *w,
+                          const float *skip, void *y, int B, int T, int H, int D, gka_dtype dt,
+                          float eps, void *stream);
+
+/*
+ * Gradients of gka_block_out_forward from dy [B, T, H, D] (dense): d_o [B, H, T, D],
+ * dw fp32 [D]; with v: dv [B, H, T, D] and dskip fp32 [H]; with z: dz [B, T, H, D]
+ * dense (each non-NULL exactly when its input is).
+ */
+size_t gka_block_out_backward_workspace_bytes(int B, int T, int H, int D, gka_dtype dt);
+int gka_block_out_backward(const void *o, const void *v, const gka_strided *z, const float *w,
+                           const float *skip, const void *dy, void *d_o, void *dv, void *dz,
+                           float *dw, float *dskip, int B, int T, int H, int D, gka_dtype dt,
+                           float eps, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Synchronises `stream`, then returns GKA_ERR_DEVICE_TIMEOUT if any kernel of
  * this library on the current device gave up a bounded wait since the last
  * call (and clears the flag), GKA_ERR_CUDA if the stream reports an error,
@@ -334,6 +459,9 @@ enum {
     GKA_KERNEL_BWD_ROWS = 10,     /* backward: chunk rows against H_s, M_s and the adjoints */
     GKA_KERNEL_BWD_GRADS = 11,    /* backward: dk, dv, dbeta, dgate of each chunk */
     GKA_KERNEL_SOLVER_STUDY = 12, /* solver study: residual histories */
+    GKA_KERNEL_LINEAR = 13,       /* gated linear recurrence, forward and single step */
+    GKA_KERNEL_LINEAR_GRAD = 14,  /* gated linear recurrence, gradients */
+    GKA_KERNEL_BLOCK_ROWS = 15,   /* row operations before and after the layer */
     GKA_KERNEL_COUNT = 16
 };
 

@@ -20,6 +20,7 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-shared",
     "--expt-relaxed-constexpr",
     "-Xptxas", "-warn-spills",
+    "--threads", "0",   # the translation units in parallel
 ]
 
 

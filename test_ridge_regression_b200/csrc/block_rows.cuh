@@ -1,0 +1,483 @@
+// The row operations on either side of the layer inside its block: unit rows of
+// q and k, sigmoid gates and the head-major layout before it; residual, RMS
+// norm, SiLU gate and the token-major layout after it; and their gradients.
+//
+// Method: "Gated KalmaNet" (arXiv 2511.21016), pith.science page, Fig. 2 (the
+// block normalises q and k by their l2 norm before the layer).  Per row x of D
+// elements, with r = (|x|^2 + eps)^-1/2:
+//   y = r x,              dx = r (dy - y (y . dy))
+// and per row u = o + skip_h v of the output, r = (|u|^2 / D + eps)^-1/2, n = r u:
+//   y = n w silu(z),      dn = dy w silu(z),  du = r (dn - n (n . dn) / D),
+//   dz = dy n w silu'(z), dw = sum dy n silu(z),  dskip_h = sum du . v,  dv = skip_h du.
+//
+// Every kernel reads each row once and writes each result once: memory traffic
+// bounds them.  A row is spread over D * sizeof(T) / 16 neighbouring lanes, 16
+// bytes a lane, so a warp's loads and stores are whole rows (64 to 512 bytes
+// each) whichever of the two layouts a side has, and a row's sum is a few
+// shuffles.  Threads walk the head-major side in order (t fastest).  All sums
+// are fp32; the gradients of what is shared by many rows (biases, w, skip) are
+// summed per block and then over the blocks in a fixed order, so results do not
+// depend on scheduling.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+
+namespace gka {
+
+constexpr int kRowThreads = 256;
+
+// [B, T, heads, D] rows (or [B, T, heads] scalars) with element strides.
+struct StridedRows {
+    const void *ptr;
+    long long sb, st, sh;
+};
+
+// 16 bytes of a row as floats and back, rounded once to nearest.
+template <typename T>
+struct Vec16;
+template <>
+struct Vec16<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void load(const float *p, float *x) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    }
+    static __device__ __forceinline__ void store(float *p, const float *x) {
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+};
+template <>
+struct Vec16<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float *x) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *x) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// Sum over the LPR neighbouring lanes of a row.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+__device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-x)); }
+
+// ---------------------------------------------------------------------------
+// Before the layer
+// ---------------------------------------------------------------------------
+struct BlockInArgs {
+    StridedRows q, k, v, beta_logit, gate_logit;   // gate_logit.ptr nullable
+    const float *beta_bias, *gate_bias;            // [H], nullable
+    const int *lengths;                            // [B], nullable
+    int B, T, H, Hk;
+    float eps;
+    unsigned row_blocks;   // blocks of the row part; the rest do the gates
+};
+
+// Row index -> (b, slot, t), slots 0..H-1 queries, then Hk keys, then Hk values,
+// t fastest.
+struct SlotRow {
+    int b, slot, t;
+};
+__device__ __forceinline__ SlotRow slot_row(size_t r, int T, int slots) {
+    SlotRow s;
+    const size_t bs = r / (unsigned)T;
+    s.t = (int)(r - bs * (unsigned)T);
+    s.b = (int)(bs / (unsigned)slots);
+    s.slot = (int)(bs - (size_t)s.b * (unsigned)slots);
+    return s;
+}
+
+// grid: row_blocks blocks of rows (RPT rows a lane group), then ceil(B*H*T / 256)
+// blocks of gates.
+template <typename T, int D, int RPT>
+__global__ void __launch_bounds__(kRowThreads)
+k_block_in(const BlockInArgs a, T *__restrict__ qo, T *__restrict__ ko, T *__restrict__ vo,
+           float *__restrict__ beta, float *__restrict__ gate) {
+    using V = Vec16<T>;
+    constexpr int LPR = D / V::N, GROUPS = kRowThreads / LPR;
+    const int slots = a.H + 2 * a.Hk;
+    if (blockIdx.x >= a.row_blocks) {
+        // gates: beta = sigmoid(logit + bias), padding keeps the state (beta 1, gate 0)
+        const size_t n = (size_t)a.B * a.H * a.T;
+        const size_t i = (size_t)(blockIdx.x - a.row_blocks) * kRowThreads + threadIdx.x;
+        if (i >= n) return;
+        const size_t bh = i / (unsigned)a.T;
+        const int t = (int)(i - bh * (unsigned)a.T), b = (int)(bh / (unsigned)a.H);
+        const int h = (int)(bh - (size_t)b * (unsigned)a.H);
+        const bool ok = !a.lengths || t < a.lengths[b];
+        const T *bl = static_cast<const T *>(a.beta_logit.ptr) + b * a.beta_logit.sb +
+                      t * a.beta_logit.st + h * a.beta_logit.sh;
+        beta[i] = ok ? sigmoid_f(load_f(bl) + (a.beta_bias ? a.beta_bias[h] : 0.f)) : 1.f;
+        if (gate) {
+            float g = 1.f;
+            if (a.gate_logit.ptr) {
+                const T *gl = static_cast<const T *>(a.gate_logit.ptr) + b * a.gate_logit.sb +
+                              t * a.gate_logit.st + h * a.gate_logit.sh;
+                g = sigmoid_f(load_f(gl) + (a.gate_bias ? a.gate_bias[h] : 0.f));
+            }
+            gate[i] = ok ? g : 0.f;
+        }
+        return;
+    }
+    const size_t rows = (size_t)a.B * slots * a.T;
+    const int lane = threadIdx.x % LPR, rep = a.H / a.Hk;
+    const size_t r0 = (size_t)blockIdx.x * (GROUPS * RPT) + threadIdx.x / LPR;
+    float x[RPT][V::N];
+    // every load of the group's rows goes out before the first sum
+#pragma unroll
+    for (int j = 0; j < RPT; ++j) {
+        const size_t r = r0 + (size_t)j * GROUPS;
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) x[j][i] = 0.f;
+        if (r >= rows) continue;
+        const SlotRow s = slot_row(r, a.T, slots);
+        if (a.lengths && s.t >= a.lengths[s.b]) continue;
+        const StridedRows &in = s.slot < a.H ? a.q : s.slot < a.H + a.Hk ? a.k : a.v;
+        const int h = s.slot < a.H ? s.slot : (s.slot - a.H) % a.Hk;
+        V::load(static_cast<const T *>(in.ptr) + s.b * in.sb + s.t * in.st + h * in.sh +
+                    lane * V::N, x[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < RPT; ++j) {
+        const size_t r = r0 + (size_t)j * GROUPS;
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) ss = fmaf(x[j][i], x[j][i], ss);
+        ss = row_sum<LPR>(ss);
+        if (r >= rows) continue;
+        const SlotRow s = slot_row(r, a.T, slots);
+        if (s.slot < a.H + a.Hk) {
+            const float rn = rsqrtf(ss + a.eps);
+#pragma unroll
+            for (int i = 0; i < V::N; ++i) x[j][i] *= rn;
+        }
+        const bool is_q = s.slot < a.H;
+        T *out = is_q ? qo : s.slot < a.H + a.Hk ? ko : vo;
+        const int h0 = is_q ? s.slot : ((s.slot - a.H) % a.Hk) * rep, nh = is_q ? 1 : rep;
+        for (int h = h0; h < h0 + nh; ++h)
+            V::store(out + (((size_t)s.b * a.H + h) * a.T + s.t) * D + lane * V::N, x[j]);
+    }
+}
+
+struct BlockInGrad {
+    const void *dq, *dk, *dv;        // [B, H, T, D]
+    const float *dbeta, *dgate;      // [B, H, T]; dgate nullable
+    void *xq, *xk, *xv;              // gradients of the raw rows, dense [B, T, heads, D]
+    void *xbeta, *xgate;             // gradients of the logits, dense [B, T, H]
+    float *part;                     // [2][H][gblk] sums of the logits' gradients
+    int gblk;                        // gate blocks per head
+};
+
+// grid: row_blocks blocks of rows, then H * gblk blocks of gates (each a run of
+// the B*T tokens of one head).
+template <typename T, int D, int RPT>
+__global__ void __launch_bounds__(kRowThreads)
+k_block_in_grad(const BlockInArgs a, const BlockInGrad g) {
+    using V = Vec16<T>;
+    constexpr int LPR = D / V::N, GROUPS = kRowThreads / LPR;
+    const int slots = a.H + 2 * a.Hk, lane = threadIdx.x % LPR;
+    if (blockIdx.x >= a.row_blocks) {
+        const unsigned id = blockIdx.x - a.row_blocks;
+        const int h = (int)(id / (unsigned)g.gblk), part = (int)(id % (unsigned)g.gblk);
+        const size_t n = (size_t)a.B * a.T;
+        const size_t e0 = n * part / g.gblk, e1 = n * (part + 1) / g.gblk;
+        const float bb = a.beta_bias ? a.beta_bias[h] : 0.f;
+        const float gb = a.gate_bias ? a.gate_bias[h] : 0.f;
+        float sb = 0.f, sg = 0.f;
+        for (size_t e = e0 + threadIdx.x; e < e1; e += kRowThreads) {
+            const size_t b = e / (unsigned)a.T, t = e - b * (unsigned)a.T;
+            const bool ok = !a.lengths || (int)t < a.lengths[b];
+            const size_t src = (b * a.H + h) * a.T + t, dst = e * a.H + h;
+            float d = 0.f, dg = 0.f;
+            if (ok) {
+                // sigma'(x) = sigma(x) sigma(-x): no difference from 1 is formed
+                const float x = bb + load_f(static_cast<const T *>(a.beta_logit.ptr) +
+                                            b * a.beta_logit.sb + t * a.beta_logit.st +
+                                            h * a.beta_logit.sh);
+                d = g.dbeta[src] * sigmoid_f(x) * sigmoid_f(-x);
+                if (g.xgate) {
+                    const float y = gb + load_f(static_cast<const T *>(a.gate_logit.ptr) +
+                                                b * a.gate_logit.sb + t * a.gate_logit.st +
+                                                h * a.gate_logit.sh);
+                    dg = g.dgate[src] * sigmoid_f(y) * sigmoid_f(-y);
+                }
+            }
+            store_f(static_cast<T *>(g.xbeta) + dst, d);
+            if (g.xgate) store_f(static_cast<T *>(g.xgate) + dst, dg);
+            sb += d;
+            sg += dg;
+        }
+        __shared__ float red[2][kRowThreads / 32];
+        sb = warp_sum(sb);
+        sg = warp_sum(sg);
+        if ((threadIdx.x & 31) == 0) {
+            red[0][threadIdx.x >> 5] = sb;
+            red[1][threadIdx.x >> 5] = sg;
+        }
+        __syncthreads();
+        if (threadIdx.x < 2) {
+            float s = 0.f;
+            for (int w = 0; w < kRowThreads / 32; ++w) s += red[threadIdx.x][w];
+            g.part[((size_t)threadIdx.x * a.H + h) * g.gblk + part] = s;
+        }
+        return;
+    }
+    const size_t rows = (size_t)a.B * slots * a.T;
+    const int rep = a.H / a.Hk;
+    const size_t r0 = (size_t)blockIdx.x * (GROUPS * RPT) + threadIdx.x / LPR;
+    float x[RPT][V::N], dy[RPT][V::N];
+#pragma unroll
+    for (int j = 0; j < RPT; ++j) {
+        const size_t r = r0 + (size_t)j * GROUPS;
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) x[j][i] = dy[j][i] = 0.f;
+        if (r >= rows) continue;
+        const SlotRow s = slot_row(r, a.T, slots);
+        if (a.lengths && s.t >= a.lengths[s.b]) continue;
+        const bool is_q = s.slot < a.H, unit = s.slot < a.H + a.Hk;
+        const int h = is_q ? s.slot : (s.slot - a.H) % a.Hk;
+        if (unit) {
+            const StridedRows &in = is_q ? a.q : a.k;
+            V::load(static_cast<const T *>(in.ptr) + s.b * in.sb + s.t * in.st + h * in.sh +
+                        lane * V::N, x[j]);
+        }
+        // a shared key or value head collects the gradients of its group
+        const T *up = static_cast<const T *>(is_q ? g.dq : unit ? g.dk : g.dv);
+        const int h0 = is_q ? h : h * rep, nh = is_q ? 1 : rep;
+        for (int hh = h0; hh < h0 + nh; ++hh) {
+            float d[V::N];
+            V::load(up + (((size_t)s.b * a.H + hh) * a.T + s.t) * D + lane * V::N, d);
+#pragma unroll
+            for (int i = 0; i < V::N; ++i) dy[j][i] += d[i];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < RPT; ++j) {
+        const size_t r = r0 + (size_t)j * GROUPS;
+        float ss = 0.f, xd = 0.f;
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) {
+            ss = fmaf(x[j][i], x[j][i], ss);
+            xd = fmaf(x[j][i], dy[j][i], xd);
+        }
+        ss = row_sum<LPR>(ss);
+        xd = row_sum<LPR>(xd);
+        if (r >= rows) continue;
+        const SlotRow s = slot_row(r, a.T, slots);
+        const bool is_q = s.slot < a.H, unit = s.slot < a.H + a.Hk;
+        if (unit) {
+            const float rn = rsqrtf(ss + a.eps), c = rn * rn * xd;   // r (dy - r x (r x . dy))
+#pragma unroll
+            for (int i = 0; i < V::N; ++i) dy[j][i] = rn * (dy[j][i] - c * x[j][i]);
+        }
+        const int heads = is_q ? a.H : a.Hk, h = is_q ? s.slot : (s.slot - a.H) % a.Hk;
+        T *out = static_cast<T *>(is_q ? g.xq : unit ? g.xk : g.xv);
+        V::store(out + (((size_t)s.b * a.T + s.t) * heads + h) * D + lane * V::N, dy[j]);
+    }
+}
+
+// out[i] = sum of part[i][0..n), one block per output, in a fixed order.  The first
+// n0 outputs go to out0, the others to out1 (either nullable).
+__global__ void __launch_bounds__(128)
+k_block_sums(const float *__restrict__ part, int n, int n0, float *__restrict__ out0,
+             float *__restrict__ out1) {
+    __shared__ float red[4];
+    float s = 0.f;
+    for (int i = threadIdx.x; i < n; i += 128) s += part[(size_t)blockIdx.x * n + i];
+    s = warp_sum(s);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = red[0] + red[1] + red[2] + red[3];
+        const int i = blockIdx.x;
+        if (i < n0) {
+            if (out0) out0[i] = s;
+        } else if (out1) {
+            out1[i - n0] = s;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// After the layer
+// ---------------------------------------------------------------------------
+struct BlockOutArgs {
+    const void *o, *v;         // [B, H, T, D]; v nullable
+    StridedRows z;             // [B, T, H, D], ptr nullable
+    const float *w, *skip;     // [D]; [H], non-null exactly when v is
+    int B, T, H;
+    float eps;
+};
+
+template <typename T, int D, int RPT>
+__global__ void __launch_bounds__(kRowThreads)
+k_block_out(const BlockOutArgs a, T *__restrict__ y) {
+    using V = Vec16<T>;
+    constexpr int LPR = D / V::N, GROUPS = kRowThreads / LPR;
+    const size_t rows = (size_t)a.B * a.H * a.T;
+    const int lane = threadIdx.x % LPR;
+    const size_t r0 = (size_t)blockIdx.x * (GROUPS * RPT) + threadIdx.x / LPR;
+    float w[V::N];
+#pragma unroll
+    for (int i = 0; i < V::N; ++i) w[i] = a.w[lane * V::N + i];
+    float u[RPT][V::N], z[RPT][V::N];
+#pragma unroll
+    for (int j = 0; j < RPT; ++j) {
+        const size_t r = r0 + (size_t)j * GROUPS;
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) u[j][i] = z[j][i] = 0.f;
+        if (r >= rows) continue;
+        V::load(static_cast<const T *>(a.o) + r * D + lane * V::N, u[j]);
+        const SlotRow s = slot_row(r, a.T, a.H);
+        if (a.z.ptr)
+            V::load(static_cast<const T *>(a.z.ptr) + s.b * a.z.sb + s.t * a.z.st + s.slot * a.z.sh +
+                        lane * V::N, z[j]);
+        if (a.v) {
+            float v[V::N];
+            V::load(static_cast<const T *>(a.v) + r * D + lane * V::N, v);
+            const float sk = a.skip[s.slot];
+#pragma unroll
+            for (int i = 0; i < V::N; ++i) u[j][i] = fmaf(sk, v[i], u[j][i]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < RPT; ++j) {
+        const size_t r = r0 + (size_t)j * GROUPS;
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) ss = fmaf(u[j][i], u[j][i], ss);
+        ss = row_sum<LPR>(ss);
+        if (r >= rows) continue;
+        const SlotRow s = slot_row(r, a.T, a.H);
+        const float rn = rsqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) {
+            u[j][i] *= rn * w[i];
+            if (a.z.ptr) u[j][i] *= z[j][i] * sigmoid_f(z[j][i]);
+        }
+        V::store(y + (((size_t)s.b * a.T + s.t) * a.H + s.slot) * D + lane * V::N, u[j]);
+    }
+}
+
+struct BlockOutGrad {
+    const void *dy;            // [B, T, H, D]
+    void *d_o, *dv;            // [B, H, T, D]; dv with a.v
+    void *dz;                  // [B, T, H, D], with a.z
+    float *wpart;              // [D][H * blk] sums of dw
+    float *spart;              // [H][blk] sums of dskip (with a.v)
+    int blk;                   // blocks per head
+};
+
+// grid (blk, H): block (i, h) walks a run of head h's B*T rows, so that dw and
+// dskip_h stay in registers to its end.
+template <typename T, int D>
+__global__ void __launch_bounds__(kRowThreads)
+k_block_out_grad(const BlockOutArgs a, const BlockOutGrad g) {
+    using V = Vec16<T>;
+    constexpr int LPR = D / V::N, GROUPS = kRowThreads / LPR;
+    const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR, h = blockIdx.y;
+    const size_t n = (size_t)a.B * a.T;
+    const size_t e0 = n * blockIdx.x / g.blk, e1 = n * (blockIdx.x + 1) / g.blk;
+    const float sk = a.v ? a.skip[h] : 0.f;
+    float w[V::N], dw[V::N], ds = 0.f;
+#pragma unroll
+    for (int i = 0; i < V::N; ++i) {
+        w[i] = a.w[lane * V::N + i];
+        dw[i] = 0.f;
+    }
+    // every lane of a warp runs the same number of rounds: the row sums are shuffles
+    // over the whole warp
+    const size_t rounds = (e1 - e0 + GROUPS - 1) / GROUPS;
+    for (size_t k = 0; k < rounds; ++k) {
+        const size_t e = e0 + k * GROUPS + grp;
+        const bool in = e < e1;
+        const size_t ec = in ? e : e0;
+        const size_t b = ec / (unsigned)a.T, t = ec - b * (unsigned)a.T;
+        const size_t hm = ((b * a.H + h) * a.T + t) * D + lane * V::N;
+        const size_t tm = (ec * a.H + h) * D + lane * V::N;
+        float u[V::N], v[V::N], z[V::N], dy[V::N];
+        V::load(static_cast<const T *>(a.o) + hm, u);
+        V::load(static_cast<const T *>(g.dy) + tm, dy);
+        if (a.v) {
+            V::load(static_cast<const T *>(a.v) + hm, v);
+#pragma unroll
+            for (int i = 0; i < V::N; ++i) u[i] = fmaf(sk, v[i], u[i]);
+        }
+        if (a.z.ptr)
+            V::load(static_cast<const T *>(a.z.ptr) + b * a.z.sb + t * a.z.st + h * a.z.sh +
+                        lane * V::N, z);
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) ss = fmaf(u[i], u[i], ss);
+        const float rn = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) {
+            u[i] *= rn;   // n
+            if (a.z.ptr) {
+                const float sg = sigmoid_f(z[i]);
+                // d silu(z) / dz = s (1 + z (1 - s)), with 1 - s = sigmoid(-z)
+                const float dsil = sg * fmaf(z[i], sigmoid_f(-z[i]), 1.f);
+                const float dyi = dy[i];
+                dy[i] = dyi * (z[i] * sg);
+                z[i] = dyi * u[i] * w[i] * dsil;
+            }
+            if (in) dw[i] = fmaf(dy[i], u[i], dw[i]);
+            dy[i] *= w[i];   // dn
+            dot = fmaf(dy[i], u[i], dot);
+        }
+        dot = row_sum<LPR>(dot) * (1.f / D);
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) dy[i] = rn * (dy[i] - u[i] * dot);   // du
+        if (!in) continue;
+        V::store(static_cast<T *>(g.d_o) + hm, dy);
+        if (a.z.ptr) V::store(static_cast<T *>(g.dz) + tm, z);
+        if (a.v) {
+#pragma unroll
+            for (int i = 0; i < V::N; ++i) {
+                ds = fmaf(dy[i], v[i], ds);
+                dy[i] *= sk;
+            }
+            V::store(static_cast<T *>(g.dv) + hm, dy);
+        }
+    }
+    __shared__ float red[GROUPS][D];
+    __shared__ float reds[kRowThreads / 32];
+#pragma unroll
+    for (int i = 0; i < V::N; ++i) red[grp][lane * V::N + i] = dw[i];
+    ds = warp_sum(ds);
+    if ((threadIdx.x & 31) == 0) reds[threadIdx.x >> 5] = ds;
+    __syncthreads();
+    if (threadIdx.x < D) {
+        float s = 0.f;
+        for (int i = 0; i < GROUPS; ++i) s += red[i][threadIdx.x];
+        g.wpart[((size_t)threadIdx.x * a.H + h) * g.blk + blockIdx.x] = s;
+    }
+    if (threadIdx.x == 0 && a.v) {
+        float s = 0.f;
+        for (int i = 0; i < kRowThreads / 32; ++i) s += reds[i];
+        g.spart[(size_t)h * g.blk + blockIdx.x] = s;
+    }
+}
+
+}  // namespace gka

@@ -21,6 +21,7 @@
 #include "chunk_simt.cuh"
 #include "common.cuh"
 #include "decode.cuh"
+#include "host.cuh"
 #include "seg_tc.cuh"
 #include "solve_tc.cuh"
 #include "state_tc.cuh"
@@ -59,41 +60,31 @@ static cudaEvent_t prof_event() {
     return e;
 }
 
-struct ProfScope {
-    int kernel;
-    cudaStream_t s;
-    cudaEvent_t start = nullptr;
-    ProfScope(int k, cudaStream_t st) : kernel(k), s(st) {
-        if (!g_prof_on) return;
-        std::lock_guard<std::mutex> g(g_prof_mu);
-        start = prof_event();
-        if (start) cudaEventRecord(start, s);
-    }
-    ~ProfScope() {
-        if (!start) return;
-        std::lock_guard<std::mutex> g(g_prof_mu);
-        cudaEvent_t stop = prof_event();
-        if (!stop) return;
-        cudaEventRecord(stop, s);
-        g_prof_pending.push_back({kernel, start, stop});
-    }
-};
+ProfScope::ProfScope(int k, cudaStream_t st) : kernel(k), s(st) {
+    if (!g_prof_on) return;
+    std::lock_guard<std::mutex> g(g_prof_mu);
+    start = prof_event();
+    if (start) cudaEventRecord(start, s);
+}
+ProfScope::~ProfScope() {
+    if (!start) return;
+    std::lock_guard<std::mutex> g(g_prof_mu);
+    cudaEvent_t stop = prof_event();
+    if (!stop) return;
+    cudaEventRecord(stop, s);
+    g_prof_pending.push_back({kernel, start, stop});
+}
 
-static int cuda_fail(cudaError_t e) {
+int cuda_fail(cudaError_t e) {
     g_last_cuda_error.store((int)e);
     return GKA_ERR_CUDA;
 }
 
-static int check_launch() {
+int check_launch() {
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? GKA_OK : cuda_fail(e);
 }
 
-static bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-static size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-static bool supported_d(int D) { return D == 32 || D == 64 || D == 128; }
 static bool supported_c(int C) { return C == 16 || C == 32 || C == 64 || C == 128; }
 
 // bf16 inputs, head dimension 128 and chunks of 64 or 128 tokens run the
@@ -154,18 +145,14 @@ static int layout(int B, int H, int T, int D, int C, gka_dtype dt, gka_workspace
     return GKA_OK;
 }
 
-// Opts a kernel into `bytes` of dynamic shared memory (beyond the 48 KiB
-// default, which also counts the kernel's static shared memory).  Remembered
-// per (kernel, device) so the attribute call happens once.
 static std::mutex g_smem_mu;
 static std::map<std::pair<const void *, int>, size_t> g_smem_set;
 
-template <typename K>
-static cudaError_t set_smem(K kernel, size_t bytes) {
+cudaError_t set_smem_bytes(const void *kernel, size_t bytes) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const auto key = std::make_pair(reinterpret_cast<const void *>(kernel), dev);
+    const auto key = std::make_pair(kernel, dev);
     std::lock_guard<std::mutex> g(g_smem_mu);
     auto it = g_smem_set.find(key);
     if (it != g_smem_set.end() && it->second >= bytes) return cudaSuccess;
@@ -213,8 +200,7 @@ static int forward_simt(const Tin *q, const Tin *k, const Tin *v, const float *b
     return check_launch();
 }
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no -lcuda).
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -243,8 +229,6 @@ static int rows128_map(CUtensorMap *m, const void *base, uint64_t rows, CUtensor
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? GKA_OK : cuda_fail(cudaErrorInvalidValue);
 }
-
-static int timeout_flag_ptr(int **ptr);
 
 // The tensor-core forward workspace's per-token decay planes (4 x B*H*T floats: l2, b,
 // beta, beta^2) for chunk C.
@@ -762,7 +746,7 @@ static int study_simt(const Tin *q, const Tin *k, const float *beta, const float
     }
 }
 
-static int timeout_flag_ptr(int **ptr) {
+int timeout_flag_ptr(int **ptr) {
     cudaError_t e = cudaGetSymbolAddress((void **)ptr, g_timeout_flag);
     return e == cudaSuccess ? GKA_OK : cuda_fail(e);
 }
@@ -1212,7 +1196,7 @@ const char *gka_status_string(int status) {
     }
 }
 
-int gka_version(void) { return 110; }
+int gka_version(void) { return 120; }
 
 int gka_profiler_enable(int on) {
     std::lock_guard<std::mutex> g(g_prof_mu);

@@ -1,0 +1,529 @@
+// C ABI of the gated linear recurrence and of the block's row operations:
+// argument checks, workspace layout, launches.  The contract of every entry
+// point is in include/gka.h.
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "../../include/gka.h"
+#include "block_rows.cuh"
+#include "host.cuh"
+#include "linear_simt.cuh"
+
+namespace gka {
+
+constexpr int kSms = 148;   // SMs of the one GPU this library is built for
+
+static bool valid_dtype(gka_dtype dt) { return dt == GKA_F32 || dt == GKA_BF16; }
+
+// ---------------------------------------------------------------------------
+// Gated linear recurrence
+// ---------------------------------------------------------------------------
+struct LinLayout {
+    int N, S, ZS;                              // chunks, segments, column splits
+    size_t agg, segdec;                        // segment aggregates, decays (S > 1)
+    size_t states, zeta, eta, fdot;            // backward
+    size_t total;
+};
+
+// Segments per sequence: enough CTAs for `per_sm` on every SM, whole chunks each.
+static int lin_segments(int ctas, int N, int per_sm) {
+    const int S = ctas > 0 ? kSms * per_sm / ctas : 1;
+    return std::max(1, std::min(S, N));
+}
+
+static int lin_layout(int B, int H, int T, int D, gka_dtype dt, bool bwd, LinLayout *L) {
+    if (B < 0 || H < 0 || T < 0 || !valid_dtype(dt)) return GKA_ERR_INVALID_ARG;
+    if (!supported_d(D)) return GKA_ERR_UNSUPPORTED;
+    if ((size_t)B * H > 65535) return GKA_ERR_UNSUPPORTED;   // grid limit
+    const size_t BH = (size_t)B * H, st = sizeof(float) * (size_t)D * D;
+    L->ZS = D / kLinZN;
+    L->N = (int)(((long long)T + kLinC - 1) / kLinC);
+    L->S = lin_segments((int)BH * L->ZS, L->N, 3);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = round256(off + bytes);
+        return at;
+    };
+    L->agg = take(L->S > 1 ? BH * L->S * st : 0);
+    L->segdec = take(L->S > 1 ? BH * L->S * sizeof(float) : 0);
+    L->states = L->zeta = L->eta = L->fdot = off;
+    if (bwd) {
+        L->states = take(BH * L->N * st);
+        L->zeta = take(L->ZS * BH * T * sizeof(float));
+        L->eta = take(L->ZS * BH * T * sizeof(float));
+        L->fdot = take(L->ZS * BH * L->N * sizeof(float));
+    }
+    L->total = off;
+    return GKA_OK;
+}
+
+template <typename T, int D, bool REV, bool OUT>
+static int lin_launch(const LinPass &p, int ZS, int prof, cudaStream_t s) {
+    cudaError_t e;
+    auto kern = k_linear_pass<T, D, REV, OUT>;
+    if ((e = set_smem(kern, LinSmem<D>::bytes)) != cudaSuccess) return cuda_fail(e);
+    ProfScope ps(prof, s);
+    kern<<<dim3(ZS, p.BH, p.S), kLinThreads, LinSmem<D>::bytes, s>>>(p);
+    return check_launch();
+}
+
+// Segment starts for a pass (p.S > 1): aggregates, then their scan from `init`.
+template <typename T, int D, bool REV>
+static int lin_starts(LinPass &p, const LinLayout &L, char *ws, const float *init, int prof,
+                      cudaStream_t s) {
+    if (L.S == 1) {
+        p.start = init;
+        return GKA_OK;
+    }
+    p.agg = reinterpret_cast<float *>(ws + L.agg);
+    p.segdec = reinterpret_cast<float *>(ws + L.segdec);
+    if (int rc = lin_launch<T, D, REV, false>(p, L.ZS, prof, s)) return rc;
+    ProfScope ps(prof, s);
+    k_linear_scan<<<dim3((D * D + 1023) / 1024, p.BH), 256, 0, s>>>(p.agg, p.segdec, init, L.S,
+                                                                  D * D, REV);
+    p.start = p.agg;
+    return check_launch();
+}
+
+struct LinCall {
+    const void *q, *k, *v, *d_o;
+    const float *beta, *gate, *init, *dlast;
+    void *o, *dq, *dk, *dv;
+    float *last, *dbeta, *dgate, *dinit;
+    int BH, T;
+    float scale;
+    char *ws;
+    cudaStream_t s;
+};
+
+template <typename T, int D>
+static int lin_forward(const LinCall &c, const LinLayout &L) {
+    LinPass p = {};
+    p.x = c.q; p.y = c.k; p.z = c.v;
+    p.out = c.o;
+    p.beta = c.beta; p.gate = c.gate;
+    p.scale = c.scale;
+    p.log_min = kLogBetaMin;
+    p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S;
+    p.zy = 1;
+    if (int rc = lin_starts<T, D, false>(p, L, c.ws, c.init, GKA_KERNEL_LINEAR, c.s)) return rc;
+    p.last = c.last;
+    return lin_launch<T, D, false, true>(p, L.ZS, GKA_KERNEL_LINEAR, c.s);
+}
+
+template <typename T, int D>
+static int lin_backward(const LinCall &c, const LinLayout &L) {
+    constexpr int kProf = GKA_KERNEL_LINEAR_GRAD;
+    float *states = reinterpret_cast<float *>(c.ws + L.states);
+    float *zeta = reinterpret_cast<float *>(c.ws + L.zeta);
+    float *eta = reinterpret_cast<float *>(c.ws + L.eta);
+    float *fdot = reinterpret_cast<float *>(c.ws + L.fdot);
+    LinPass p = {};
+    p.beta = c.beta; p.gate = c.gate;
+    p.scale = c.scale;
+    p.log_min = kLinLogMinBwd;
+    p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S;
+    // dq, forwards in time; M before every chunk stays for F
+    LinPass f = p;
+    f.x = c.d_o; f.y = c.v; f.z = c.k;
+    f.zy = 0;
+    if (int rc = lin_starts<T, D, false>(f, L, c.ws, c.init, kProf, c.s)) return rc;
+    f.out = c.dq;
+    f.xd = c.q;
+    f.dot = zeta;
+    f.states = states;
+    if (int rc = lin_launch<T, D, false, true>(f, L.ZS, kProf, c.s)) return rc;
+    // dv and dk, backwards in time
+    LinPass r = p;
+    r.x = c.k; r.y = c.q; r.z = c.d_o;
+    r.zy = 1;
+    if (int rc = lin_starts<T, D, true>(r, L, c.ws, c.dlast, kProf, c.s)) return rc;
+    r.out = c.dv;
+    r.xd = c.v;
+    r.dot = eta;
+    r.states_in = states;
+    r.fdot = fdot;
+    r.last = c.dinit;
+    if (int rc = lin_launch<T, D, true, true>(r, L.ZS, kProf, c.s)) return rc;
+    LinPass d = p;
+    d.x = c.v; d.y = c.d_o; d.z = c.q;
+    d.zy = 0;
+    d.start = r.start;
+    d.out = c.dk;
+    if (int rc = lin_launch<T, D, true, true>(d, L.ZS, kProf, c.s)) return rc;
+    LinPairs w = {};
+    w.q = c.q; w.k = c.k; w.v = c.v; w.d_o = c.d_o;
+    w.beta = c.beta; w.gate = c.gate;
+    w.zeta = zeta; w.eta = eta; w.fdot = fdot;
+    w.dbeta = c.dbeta; w.dgate = c.dgate;
+    w.scale = c.scale;
+    w.BH = c.BH; w.T = c.T; w.N = L.N; w.ZS = L.ZS;
+    cudaError_t e;
+    auto kern = k_linear_pairs<T, D>;
+    if ((e = set_smem(kern, lin_pairs_smem<D>())) != cudaSuccess) return cuda_fail(e);
+    ProfScope ps(kProf, c.s);
+    kern<<<dim3(L.N, c.BH), kLinThreads, lin_pairs_smem<D>(), c.s>>>(w);
+    return check_launch();
+}
+
+// f(type tag, size tag) for the call's type and head size.
+template <typename F>
+static int by_type(gka_dtype dt, int D, F f) {
+    auto by_size = [&](auto tag) {
+        switch (D) {
+            case 32: return f(tag, std::integral_constant<int, 32>());
+            case 64: return f(tag, std::integral_constant<int, 64>());
+            default: return f(tag, std::integral_constant<int, 128>());
+        }
+    };
+    return dt == GKA_BF16 ? by_size(__nv_bfloat16()) : by_size(float());
+}
+
+// ---------------------------------------------------------------------------
+// Block rows
+// ---------------------------------------------------------------------------
+static int strided(const gka_strided *r, bool rows, int es, StridedRows *out) {
+    *out = StridedRows{r->ptr, r->stride_b, r->stride_t, r->stride_h};
+    if (!r->ptr) return GKA_ERR_INVALID_ARG;
+    if (rows) {
+        if (!aligned16(r->ptr)) return GKA_ERR_MISALIGNED;
+        if ((r->stride_b * es) % 16 || (r->stride_t * es) % 16 || (r->stride_h * es) % 16)
+            return GKA_ERR_MISALIGNED;
+    }
+    return GKA_OK;
+}
+
+static int rows_ok(int B, int T, int H, int Hk, int D, gka_dtype dt, float eps) {
+    if (B < 0 || T < 0 || H < 0 || Hk < 0 || !valid_dtype(dt)) return GKA_ERR_INVALID_ARG;
+    if (!(eps >= 0.f) || !isfinite(eps)) return GKA_ERR_INVALID_ARG;
+    if (H > 0 && (Hk == 0 || H % Hk)) return GKA_ERR_INVALID_ARG;
+    if (!supported_d(D)) return GKA_ERR_UNSUPPORTED;
+    if (H > 65535) return GKA_ERR_UNSUPPORTED;
+    // blocks of 32 to 256 rows each, in one grid dimension
+    if ((double)B * T * ((double)H + 2.0 * Hk) > 3e10) return GKA_ERR_UNSUPPORTED;
+    return GKA_OK;
+}
+
+static int gate_blocks(int B, int T) {
+    return (int)std::max<size_t>(1, std::min<size_t>(64, ((size_t)B * T + 1023) / 1024));
+}
+
+// Blocks per head of the output norm's gradient: at most eight a SM in all, at
+// least four rounds of rows each.
+static int out_blocks(int B, int T, int H, int D, gka_dtype dt) {
+    const size_t groups = kRowThreads / (D * (dt == GKA_BF16 ? 2 : 4) / 16);
+    const size_t rounds = ((size_t)B * T + groups * 4 - 1) / (groups * 4);
+    const size_t most = std::max(1, kSms * 8 / std::max(1, H));
+    return (int)std::max<size_t>(1, std::min(rounds, most));
+}
+
+template <typename T, int D>
+static size_t row_blocks(size_t rows, int rpt) {
+    const size_t per = (size_t)kRowThreads / (D / Vec16<T>::N) * rpt;
+    return (rows + per - 1) / per;
+}
+
+}  // namespace gka
+
+using namespace gka;
+
+extern "C" {
+
+size_t gka_linear_forward_workspace_bytes(int B, int H, int T, int D, gka_dtype dt) {
+    LinLayout L;
+    return lin_layout(B, H, T, D, dt, false, &L) == GKA_OK ? L.total : 0;
+}
+
+size_t gka_linear_backward_workspace_bytes(int B, int H, int T, int D, gka_dtype dt) {
+    LinLayout L;
+    return lin_layout(B, H, T, D, dt, true, &L) == GKA_OK ? L.total : 0;
+}
+
+// A state that no token touches: dst = src, or zero.
+static int pass_state(float *dst, const float *src, size_t floats, cudaStream_t s) {
+    if (!dst || dst == src) return GKA_OK;
+    const cudaError_t e =
+        src ? cudaMemcpyAsync(dst, src, floats * sizeof(float), cudaMemcpyDeviceToDevice, s)
+            : cudaMemsetAsync(dst, 0, floats * sizeof(float), s);
+    return e == cudaSuccess ? GKA_OK : cuda_fail(e);
+}
+
+int gka_linear_forward(const void *q, const void *k, const void *v, const float *beta,
+                       const float *gate, void *o, int B, int H, int T, int D, gka_dtype dt,
+                       float scale, const float *initial_state, float *final_state,
+                       void *workspace, size_t workspace_bytes, void *stream) {
+    LinLayout L;
+    if (int rc = lin_layout(B, H, T, D, dt, false, &L)) return rc;
+    if (!isfinite(scale)) return GKA_ERR_INVALID_ARG;
+    const size_t BH = (size_t)B * H;
+    if (BH == 0) return GKA_OK;
+    const void *ptrs[] = {q, k, v, beta, gate, o, initial_state, final_state};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return GKA_ERR_MISALIGNED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0) return pass_state(final_state, initial_state, BH * D * D, s);
+    if (!q || !k || !v || !beta || !o) return GKA_ERR_INVALID_ARG;
+    if (L.total > 0 && !workspace) return GKA_ERR_INVALID_ARG;
+    if ((uintptr_t)workspace & 255u) return GKA_ERR_MISALIGNED;
+    if (workspace_bytes < L.total) return GKA_ERR_WORKSPACE_TOO_SMALL;
+    LinCall c = {};
+    c.q = q; c.k = k; c.v = v; c.beta = beta; c.gate = gate; c.o = o;
+    c.init = initial_state; c.last = final_state;
+    c.BH = (int)BH; c.T = T; c.scale = scale;
+    c.ws = static_cast<char *>(workspace);
+    c.s = s;
+    return by_type(dt, D, [&](auto tag, auto d) {
+        return lin_forward<decltype(tag), decltype(d)::value>(c, L);
+    });
+}
+
+int gka_linear_backward(const void *q, const void *k, const void *v, const float *beta,
+                        const float *gate, const void *dout, const float *initial_state,
+                        const float *dfinal_state, void *dq, void *dk, void *dv, float *dbeta,
+                        float *dgate, float *dinitial_state, int B, int H, int T, int D,
+                        gka_dtype dt, float scale, void *workspace, size_t workspace_bytes,
+                        void *stream) {
+    LinLayout L;
+    if (int rc = lin_layout(B, H, T, D, dt, true, &L)) return rc;
+    if (!isfinite(scale)) return GKA_ERR_INVALID_ARG;
+    if ((dgate != nullptr) != (gate != nullptr)) return GKA_ERR_INVALID_ARG;
+    const size_t BH = (size_t)B * H;
+    if (BH == 0) return GKA_OK;
+    const void *ptrs[] = {q, k, v, beta, gate, dout, initial_state, dfinal_state, dq, dk, dv, dbeta,
+                          dgate, dinitial_state};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return GKA_ERR_MISALIGNED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0) return pass_state(dinitial_state, dfinal_state, BH * D * D, s);
+    if (!q || !k || !v || !beta || !dout || !dq || !dk || !dv || !dbeta || !workspace)
+        return GKA_ERR_INVALID_ARG;
+    if ((uintptr_t)workspace & 255u) return GKA_ERR_MISALIGNED;
+    if (workspace_bytes < L.total) return GKA_ERR_WORKSPACE_TOO_SMALL;
+    LinCall c = {};
+    c.q = q; c.k = k; c.v = v; c.beta = beta; c.gate = gate; c.d_o = dout;
+    c.init = initial_state; c.dlast = dfinal_state;
+    c.dq = dq; c.dk = dk; c.dv = dv; c.dbeta = dbeta; c.dgate = dgate; c.dinit = dinitial_state;
+    c.BH = (int)BH; c.T = T; c.scale = scale;
+    c.ws = static_cast<char *>(workspace);
+    c.s = s;
+    return by_type(dt, D, [&](auto tag, auto d) {
+        return lin_backward<decltype(tag), decltype(d)::value>(c, L);
+    });
+}
+
+int gka_linear_decode_step(float *state, const void *q, const void *k, const void *v,
+                           const float *beta, const float *gate, void *o, int B, int H, int D,
+                           gka_dtype dt, float scale, void *stream) {
+    if (B < 0 || H < 0 || !valid_dtype(dt) || !isfinite(scale)) return GKA_ERR_INVALID_ARG;
+    if (!supported_d(D)) return GKA_ERR_UNSUPPORTED;
+    const size_t BH = (size_t)B * H;
+    if (BH == 0) return GKA_OK;
+    if (BH > 0x7fffffffu / 8) return GKA_ERR_UNSUPPORTED;   // eight parts a head in one grid dimension
+    if (!state || !q || !k || !v || !beta || !o) return GKA_ERR_INVALID_ARG;
+    const void *ptrs[] = {state, q, k, v, beta, gate, o};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return GKA_ERR_MISALIGNED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return by_type(dt, D, [&](auto tag, auto d) {
+        using T = decltype(tag);
+        constexpr int DD = decltype(d)::value;
+        constexpr int rows = kStepThreads / (DD / 4) * kStepRows;
+        constexpr int parts = (DD + rows - 1) / rows;
+        ProfScope ps(GKA_KERNEL_LINEAR, s);
+        k_linear_step<T, DD><<<(unsigned)(BH * parts), kStepThreads, 0, s>>>(
+            state, static_cast<const T *>(q), static_cast<const T *>(k), static_cast<const T *>(v),
+            beta, gate, static_cast<T *>(o), scale, parts);
+        return check_launch();
+    });
+}
+
+int gka_block_in_forward(const gka_strided *q, const gka_strided *k, const gka_strided *v,
+                         const gka_strided *beta_logit, const gka_strided *gate_logit,
+                         const float *beta_bias, const float *gate_bias, const int *lengths,
+                         void *q_out, void *k_out, void *v_out, float *beta, float *gate, int B,
+                         int T, int H, int Hk, int D, gka_dtype dt, float eps, void *stream) {
+    if (int rc = rows_ok(B, T, H, Hk, D, dt, eps)) return rc;
+    const size_t n = (size_t)B * H * T;
+    if (n == 0) return GKA_OK;   // before any pointer is looked at: empty buffers may be NULL
+    if (!gate && (gate_logit || lengths)) return GKA_ERR_INVALID_ARG;
+    if (gate && !gate_logit && !lengths) return GKA_ERR_INVALID_ARG;
+    if (!q || !k || !v || !beta_logit || !q_out || !k_out || !v_out || !beta)
+        return GKA_ERR_INVALID_ARG;
+    const int es = dt == GKA_BF16 ? 2 : 4;
+    BlockInArgs a = {};
+    if (int rc = strided(q, true, es, &a.q)) return rc;
+    if (int rc = strided(k, true, es, &a.k)) return rc;
+    if (int rc = strided(v, true, es, &a.v)) return rc;
+    if (int rc = strided(beta_logit, false, es, &a.beta_logit)) return rc;
+    if (gate_logit)
+        if (int rc = strided(gate_logit, false, es, &a.gate_logit)) return rc;
+    const void *ptrs[] = {q_out, k_out, v_out, beta, gate};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return GKA_ERR_MISALIGNED;
+    a.beta_bias = beta_bias; a.gate_bias = gate_bias; a.lengths = lengths;
+    a.B = B; a.T = T; a.H = H; a.Hk = Hk; a.eps = eps;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return by_type(dt, D, [&](auto tag, auto d) {
+        using Tin = decltype(tag);
+        constexpr int DD = decltype(d)::value, RPT = 4;
+        a.row_blocks = (unsigned)row_blocks<Tin, DD>((size_t)B * T * (H + 2 * Hk), RPT);
+        const size_t gates = (n + kRowThreads - 1) / kRowThreads;
+        ProfScope ps(GKA_KERNEL_BLOCK_ROWS, s);
+        k_block_in<Tin, DD, RPT><<<(unsigned)(a.row_blocks + gates), kRowThreads, 0, s>>>(
+            a, static_cast<Tin *>(q_out), static_cast<Tin *>(k_out), static_cast<Tin *>(v_out), beta,
+            gate);
+        return check_launch();
+    });
+}
+
+size_t gka_block_in_backward_workspace_bytes(int B, int T, int H, int Hk, int D, gka_dtype dt) {
+    if (rows_ok(B, T, H, Hk, D, dt, 0.f)) return 0;
+    return round256(sizeof(float) * 2 * (size_t)H * gate_blocks(B, T));
+}
+
+int gka_block_in_backward(const gka_strided *q, const gka_strided *k,
+                          const gka_strided *beta_logit, const gka_strided *gate_logit,
+                          const float *beta_bias, const float *gate_bias, const int *lengths,
+                          const void *dq_out, const void *dk_out, const void *dv_out,
+                          const float *dbeta, const float *dgate, void *dq, void *dk, void *dv,
+                          void *dbeta_logit, void *dgate_logit, float *dbeta_bias,
+                          float *dgate_bias, int B, int T, int H, int Hk, int D, gka_dtype dt,
+                          float eps, void *workspace, size_t workspace_bytes, void *stream) {
+    if (int rc = rows_ok(B, T, H, Hk, D, dt, eps)) return rc;
+    if (dgate_bias && !gate_logit) return GKA_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t n = (size_t)B * H * T;
+    if (n == 0) {
+        // no token: the shared gradients are empty sums
+        if (int rc = pass_state(dbeta_bias, nullptr, H, s)) return rc;
+        return pass_state(dgate_bias, nullptr, H, s);
+    }
+    if ((gate_logit != nullptr) != (dgate != nullptr) ||
+        (gate_logit != nullptr) != (dgate_logit != nullptr))
+        return GKA_ERR_INVALID_ARG;
+    if (!q || !k || !beta_logit || !dq_out || !dk_out || !dv_out || !dbeta || !dq || !dk || !dv ||
+        !dbeta_logit || !workspace)
+        return GKA_ERR_INVALID_ARG;
+    const int es = dt == GKA_BF16 ? 2 : 4;
+    BlockInArgs a = {};
+    if (int rc = strided(q, true, es, &a.q)) return rc;
+    if (int rc = strided(k, true, es, &a.k)) return rc;
+    if (int rc = strided(beta_logit, false, es, &a.beta_logit)) return rc;
+    if (gate_logit)
+        if (int rc = strided(gate_logit, false, es, &a.gate_logit)) return rc;
+    const void *ptrs[] = {dq_out, dk_out, dv_out, dbeta, dgate, dq, dk, dv, dbeta_logit, dgate_logit};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return GKA_ERR_MISALIGNED;
+    if ((uintptr_t)workspace & 255u) return GKA_ERR_MISALIGNED;
+    BlockInGrad g = {};
+    g.gblk = gate_blocks(B, T);
+    if (workspace_bytes < round256(sizeof(float) * 2 * (size_t)H * g.gblk))
+        return GKA_ERR_WORKSPACE_TOO_SMALL;
+    g.dq = dq_out; g.dk = dk_out; g.dv = dv_out; g.dbeta = dbeta; g.dgate = dgate;
+    g.xq = dq; g.xk = dk; g.xv = dv; g.xbeta = dbeta_logit; g.xgate = dgate_logit;
+    g.part = static_cast<float *>(workspace);
+    a.beta_bias = beta_bias; a.gate_bias = gate_bias; a.lengths = lengths;
+    a.B = B; a.T = T; a.H = H; a.Hk = Hk; a.eps = eps;
+    return by_type(dt, D, [&](auto tag, auto d) {
+        using Tin = decltype(tag);
+        constexpr int DD = decltype(d)::value, RPT = 2;
+        a.row_blocks = (unsigned)row_blocks<Tin, DD>((size_t)B * T * (H + 2 * Hk), RPT);
+        {
+            ProfScope ps(GKA_KERNEL_BLOCK_ROWS, s);
+            k_block_in_grad<Tin, DD, RPT>
+                <<<a.row_blocks + (unsigned)H * g.gblk, kRowThreads, 0, s>>>(a, g);
+        }
+        if (int rc = check_launch()) return rc;
+        if (!dbeta_bias && !dgate_bias) return (int)GKA_OK;
+        ProfScope ps(GKA_KERNEL_BLOCK_ROWS, s);
+        k_block_sums<<<dgate_bias ? 2 * H : H, 128, 0, s>>>(g.part, g.gblk, H, dbeta_bias, dgate_bias);
+        return check_launch();
+    });
+}
+
+int gka_block_out_forward(const void *o, const void *v, const gka_strided *z, const float *w,
+                          const float *skip, void *y, int B, int T, int H, int D, gka_dtype dt,
+                          float eps, void *stream) {
+    if (int rc = rows_ok(B, T, H, H, D, dt, eps)) return rc;
+    const size_t n = (size_t)B * H * T;
+    if (n == 0) return GKA_OK;
+    if ((v != nullptr) != (skip != nullptr)) return GKA_ERR_INVALID_ARG;
+    if (!o || !w || !y) return GKA_ERR_INVALID_ARG;
+    BlockOutArgs a = {};
+    if (z)
+        if (int rc = strided(z, true, dt == GKA_BF16 ? 2 : 4, &a.z)) return rc;
+    const void *ptrs[] = {o, v, w, y};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return GKA_ERR_MISALIGNED;
+    a.o = o; a.v = v; a.w = w; a.skip = skip;
+    a.B = B; a.T = T; a.H = H; a.eps = eps;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return by_type(dt, D, [&](auto tag, auto d) {
+        using Tin = decltype(tag);
+        constexpr int DD = decltype(d)::value, RPT = 2;
+        ProfScope ps(GKA_KERNEL_BLOCK_ROWS, s);
+        k_block_out<Tin, DD, RPT><<<(unsigned)row_blocks<Tin, DD>(n, RPT), kRowThreads, 0, s>>>(
+            a, static_cast<Tin *>(y));
+        return check_launch();
+    });
+}
+
+size_t gka_block_out_backward_workspace_bytes(int B, int T, int H, int D, gka_dtype dt) {
+    if (rows_ok(B, T, H, H, D, dt, 0.f)) return 0;
+    const size_t blk = out_blocks(B, T, H, D, dt);
+    return round256(sizeof(float) * D * H * blk) + round256(sizeof(float) * H * blk);
+}
+
+int gka_block_out_backward(const void *o, const void *v, const gka_strided *z, const float *w,
+                           const float *skip, const void *dy, void *d_o, void *dv, void *dz,
+                           float *dw, float *dskip, int B, int T, int H, int D, gka_dtype dt,
+                           float eps, void *workspace, size_t workspace_bytes, void *stream) {
+    if (int rc = rows_ok(B, T, H, H, D, dt, eps)) return rc;
+    if (!dw) return GKA_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t n = (size_t)B * H * T;
+    if (n == 0) {
+        if (int rc = pass_state(dw, nullptr, D, s)) return rc;
+        return pass_state(dskip, nullptr, H, s);
+    }
+    if ((v != nullptr) != (skip != nullptr) || (v != nullptr) != (dv != nullptr) ||
+        (v != nullptr) != (dskip != nullptr) || (z != nullptr) != (dz != nullptr))
+        return GKA_ERR_INVALID_ARG;
+    if (!o || !w || !dy || !d_o || !workspace) return GKA_ERR_INVALID_ARG;
+    BlockOutArgs a = {};
+    if (z)
+        if (int rc = strided(z, true, dt == GKA_BF16 ? 2 : 4, &a.z)) return rc;
+    const void *ptrs[] = {o, v, w, dy, d_o, dv, dz};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return GKA_ERR_MISALIGNED;
+    if ((uintptr_t)workspace & 255u) return GKA_ERR_MISALIGNED;
+    if (workspace_bytes < gka_block_out_backward_workspace_bytes(B, T, H, D, dt))
+        return GKA_ERR_WORKSPACE_TOO_SMALL;
+    a.o = o; a.v = v; a.w = w; a.skip = skip;
+    a.B = B; a.T = T; a.H = H; a.eps = eps;
+    BlockOutGrad g = {};
+    g.blk = out_blocks(B, T, H, D, dt);
+    g.dy = dy; g.d_o = d_o; g.dv = dv; g.dz = dz;
+    g.wpart = static_cast<float *>(workspace);
+    g.spart = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                        round256(sizeof(float) * (size_t)D * H * g.blk));
+    return by_type(dt, D, [&](auto tag, auto d) {
+        using Tin = decltype(tag);
+        {
+            ProfScope ps(GKA_KERNEL_BLOCK_ROWS, s);
+            k_block_out_grad<Tin, decltype(d)::value>
+                <<<dim3(g.blk, H), kRowThreads, 0, s>>>(a, g);
+        }
+        if (int rc = check_launch()) return rc;
+        ProfScope ps(GKA_KERNEL_BLOCK_ROWS, s);
+        k_block_sums<<<D, 128, 0, s>>>(g.wpart, H * g.blk, D, dw, nullptr);
+        if (v) k_block_sums<<<H, 128, 0, s>>>(g.spart, g.blk, H, dskip, nullptr);
+        return check_launch();
+    });
+}
+
+}  // extern "C"

@@ -30,12 +30,18 @@ class GkaError(RuntimeError):
 
 KERNEL_NAMES = ["chunk_delta", "state_scan", "chunk_norm", "chunk_solve", "decode_step",
                 "chunk_solve_tc", "state_pass_tc", "bwd_solve", "bwd_delta", "adjoint_scan",
-                "bwd_rows", "bwd_grads", "solver_study"]
+                "bwd_rows", "bwd_grads", "solver_study", "linear", "linear_grad", "block_rows"]
 _KERNEL_COUNT = 16
 
 
 class KernelTimes(ctypes.Structure):
     _fields_ = [("ms", ctypes.c_double * _KERNEL_COUNT), ("launches", ctypes.c_int * _KERNEL_COUNT)]
+
+
+class Strided(ctypes.Structure):
+    """gka_strided: rows [B, T, heads, D] (or scalars [B, T, heads]) at element strides."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_longlong),
+                ("stride_t", ctypes.c_longlong), ("stride_h", ctypes.c_longlong)]
 
 
 class WorkspaceLayout(ctypes.Structure):
@@ -84,6 +90,29 @@ def _lib():
         lib.gka_solver_study_workspace_bytes.restype = sz
         lib.gka_solver_study.argtypes = [vp, vp, vp, vp, i, i, i, i, i, f, i, i, i, vp, vp, sz, vp]
         lib.gka_solver_study.restype = i
+        for n in ("forward", "backward"):
+            fn = getattr(lib, f"gka_linear_{n}_workspace_bytes")
+            fn.argtypes, fn.restype = [i] * 5, sz
+        lib.gka_linear_forward.argtypes = [vp] * 6 + [i] * 5 + [f, vp, vp, vp, sz, vp]
+        lib.gka_linear_forward.restype = i
+        lib.gka_linear_backward.argtypes = [vp] * 14 + [i] * 5 + [f, vp, sz, vp]
+        lib.gka_linear_backward.restype = i
+        lib.gka_linear_decode_step.argtypes = [vp] * 7 + [i] * 4 + [f, vp]
+        lib.gka_linear_decode_step.restype = i
+        rows = ctypes.POINTER(Strided)
+        lib.gka_block_in_forward.argtypes = [rows] * 5 + [vp] * 8 + [i] * 6 + [f, vp]
+        lib.gka_block_in_forward.restype = i
+        lib.gka_block_in_backward_workspace_bytes.argtypes = [i] * 6
+        lib.gka_block_in_backward_workspace_bytes.restype = sz
+        lib.gka_block_in_backward.argtypes = [rows] * 4 + [vp] * 15 + [i] * 6 + [f, vp, sz, vp]
+        lib.gka_block_in_backward.restype = i
+        lib.gka_block_out_forward.argtypes = [vp, vp, rows, vp, vp, vp] + [i] * 5 + [f, vp]
+        lib.gka_block_out_forward.restype = i
+        lib.gka_block_out_backward_workspace_bytes.argtypes = [i] * 5
+        lib.gka_block_out_backward_workspace_bytes.restype = sz
+        lib.gka_block_out_backward.argtypes = ([vp, vp, rows] + [vp] * 8 + [i] * 5 +
+                                               [f, vp, sz, vp])
+        lib.gka_block_out_backward.restype = i
         lib.gka_selftest_timeout.argtypes = [vp]
         lib.gka_selftest_timeout.restype = i
         lib.gka_device_status.argtypes = [vp]
@@ -336,6 +365,306 @@ def gka_backward(q, k, v, beta, dout, a: float, r: int, chunk: int = 32, *, gate
                              _ptr(workspace), workspace.numel() * workspace.element_size(),
                              _stream(stream))
     _check("gka_backward", rc)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# The gated linear recurrence and the block's row operations.  These calls run on
+# the device that holds their tensors, whichever is current, on `stream` or that
+# device's current stream.  Outputs and workspaces that a call allocates belong to
+# the stream that is current at the call, as torch's allocator has it: with a
+# `stream` of one's own, pass them, or call under `torch.cuda.stream(stream)`.
+# ---------------------------------------------------------------------------
+def _same_device(*ts):
+    """The one CUDA device of the tensors given (None: not given)."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors must be on one device")
+    return dev
+
+
+def _dense(*ts):
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("tensors must be contiguous CUDA tensors")
+
+
+def _need(name, t, shape, dtype):
+    if t is not None and (t.shape != shape or t.dtype != dtype):
+        raise ValueError(f"{name} must be {str(dtype)[6:]} {list(shape)}")
+
+
+def _apart(*outs):
+    """No two of a call's outputs (and the inputs given with them) share memory."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                   for t in outs if t is not None and t.numel())
+    for (_, e), (b, _) in zip(spans, spans[1:]):
+        if b < e:
+            raise ValueError("outputs must not share memory with each other or with inputs")
+
+
+def _invoke(fn, dev, stream, *args):
+    """Calls a C entry point whose last argument is the stream, on device ``dev``."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError("stream must belong to the tensors' device")
+    call = getattr(_lib(), fn)
+    if torch.cuda.current_device() == dev.index:
+        rc = call(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = call(*args, stream.cuda_stream)
+    _check(fn, rc)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(n, workspace, dev):
+    if workspace is None:
+        return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def linear_workspace_bytes(B, H, T, D, dtype=torch.bfloat16, *, backward=False) -> int:
+    """Workspace bytes of gka_linear_forward (or gka_linear_backward); may be 0."""
+    fn = "gka_linear_backward_workspace_bytes" if backward else "gka_linear_forward_workspace_bytes"
+    return int(getattr(_lib(), fn)(B, H, T, D, _DT[dtype]))
+
+
+def _linear_inputs(q, k, v, beta, gate, shape):
+    if k.shape != q.shape or v.shape != q.shape or beta.shape != shape:
+        raise ValueError("shape mismatch")
+    dt = _dtype(q)
+    if k.dtype != q.dtype or v.dtype != q.dtype or beta.dtype != torch.float32:
+        raise TypeError("q, k, v must share a dtype; beta must be float32")
+    _need("gate", gate, shape, torch.float32)
+    return dt
+
+
+def gka_linear_forward(q, k, v, beta, *, gate=None, scale=1.0, initial_state=None,
+                       final_state=None, o=None, workspace=None, stream=None):
+    """Gated linear recurrence M_t = beta_t M_{t-1} + g_t v_t k_t^T, o_t = scale M_t q_t
+    (see include/gka.h).  q, k, v: [B, H, T, D] fp32 or bf16 CUDA tensors, any T; beta
+    (and the optional gate): [B, H, T] fp32; initial_state, final_state (written; may be
+    initial_state): fp32 [B, H, D, D].  Returns o (shape and dtype of v)."""
+    dev = _same_device(q, k, v, beta, gate, initial_state, final_state, o, workspace)
+    _dense(q, k, v, beta, gate, initial_state, final_state, o)
+    B, H, T, D = q.shape
+    dt = _linear_inputs(q, k, v, beta, gate, (B, H, T))
+    _need("initial_state", initial_state, (B, H, D, D), torch.float32)
+    _need("final_state", final_state, (B, H, D, D), torch.float32)
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _need("o", o, q.shape, q.dtype)
+        _apart(o, final_state)
+        for t in (q, k, v, beta, gate, initial_state, workspace):
+            _apart(o, t)
+    n = _lib().gka_linear_forward_workspace_bytes(B, H, T, D, dt)
+    workspace = _scratch(n, workspace, dev)
+    _invoke("gka_linear_forward", dev, stream, _p(q), _p(k), _p(v), _p(beta), _p(gate), _p(o), B, H,
+            T, D, dt, scale, _p(initial_state), _p(final_state), _p(workspace), _nbytes(workspace))
+    return o
+
+
+def gka_linear_decode_step(state, q, k, v, beta, *, gate=None, scale=1.0, o=None, stream=None):
+    """One token of the gated linear recurrence, in place on state [B, H, D, D] fp32;
+    q, k, v: [B, H, D]; beta (and the optional gate): [B, H] fp32.  Returns o [B, H, D]."""
+    dev = _same_device(state, q, k, v, beta, gate, o)
+    _dense(state, q, k, v, beta, gate, o)
+    B, H, D = q.shape
+    dt = _linear_inputs(q, k, v, beta, gate, (B, H))
+    if state.dtype != torch.float32 or state.shape != (B, H, D, D):
+        raise ValueError("state must be float32 [B, H, D, D]")
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _need("o", o, q.shape, q.dtype)
+        for t in (state, q, k, v, beta, gate):
+            _apart(o, t)
+    _invoke("gka_linear_decode_step", dev, stream, _p(state), _p(q), _p(k), _p(v), _p(beta),
+            _p(gate), _p(o), B, H, D, dt, scale)
+    return o
+
+
+def gka_linear_backward(q, k, v, beta, dout, *, gate=None, scale=1.0, initial_state=None,
+                        dfinal_state=None, workspace=None, stream=None):
+    """Gradients of gka_linear_forward (see include/gka.h).  dout: [B, H, T, D] in the
+    inputs' dtype; dfinal_state: optional gradient of the final state, fp32 [B, H, D, D].
+    Returns a dict with dq, dk, dv (dtype of q), dbeta, with a gate dgate (fp32), and with
+    an initial_state dstate (its gradient, fp32)."""
+    dev = _same_device(q, k, v, beta, gate, dout, initial_state, dfinal_state, workspace)
+    _dense(q, k, v, beta, gate, dout, initial_state, dfinal_state)
+    B, H, T, D = q.shape
+    dt = _linear_inputs(q, k, v, beta, gate, (B, H, T))
+    _need("dout", dout, q.shape, q.dtype)
+    _need("initial_state", initial_state, (B, H, D, D), torch.float32)
+    _need("dfinal_state", dfinal_state, (B, H, D, D), torch.float32)
+    out = {n: torch.empty_like(q) for n in ("dq", "dk", "dv")}
+    out["dbeta"] = torch.empty_like(beta)
+    if gate is not None:
+        out["dgate"] = torch.empty_like(gate)
+    if initial_state is not None:
+        out["dstate"] = torch.empty_like(initial_state)
+    n = _lib().gka_linear_backward_workspace_bytes(B, H, T, D, dt)
+    workspace = _scratch(n, workspace, dev)
+    _invoke("gka_linear_backward", dev, stream, _p(q), _p(k), _p(v), _p(beta), _p(gate), _p(dout),
+            _p(initial_state), _p(dfinal_state), _p(out["dq"]), _p(out["dk"]), _p(out["dv"]),
+            _p(out["dbeta"]), _p(out.get("dgate")), _p(out.get("dstate")), B, H, T, D, dt, scale,
+            _p(workspace), _nbytes(workspace))
+    return out
+
+
+def _strided(name, t, dtype, shape):
+    """gka_strided of a [B, T, heads(, D)] tensor with contiguous rows (None: NULL)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {str(dtype)[6:]} {list(shape)}")
+    if t.dim() == 4 and t.stride(3) != 1 and t.numel():
+        raise ValueError(f"{name} must have contiguous rows")
+    # the stride of an axis of one is never used, whatever torch reports for it
+    sb, st, sh = (t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))
+    return ctypes.byref(Strided(t.data_ptr(), sb, st, sh))
+
+
+def _block_in_args(q, k, beta_logit, gate_logit, beta_bias, gate_bias, lengths):
+    B, T, H, D = q.shape
+    Hk = k.shape[2]
+    dt = _dtype(q)
+    _need("beta_bias", beta_bias, (H,), torch.float32)
+    _need("gate_bias", gate_bias, (H,), torch.float32)
+    _need("lengths", lengths, (B,), torch.int32)
+    if gate_bias is not None and gate_logit is None:
+        raise ValueError("gate_bias needs gate_logit")
+    _dense(beta_bias, gate_bias, lengths)
+    return B, T, H, Hk, D, dt, (
+        _strided("q", q, q.dtype, (B, T, H, D)), _strided("k", k, q.dtype, (B, T, Hk, D)),
+        _strided("beta_logit", beta_logit, q.dtype, (B, T, H)),
+        _strided("gate_logit", gate_logit, q.dtype, (B, T, H)))
+
+
+def gka_block_in(q, k, v, beta_logit, *, gate_logit=None, beta_bias=None, gate_bias=None,
+                 lengths=None, eps=1e-6, stream=None):
+    """Before the layer (see include/gka.h): unit rows of q and k, sigmoid gates, head-major
+    layout.  q: [B, T, H, D], k, v: [B, T, Hk, D] (Hk divides H) fp32 or bf16 CUDA tensors
+    at any strides with contiguous rows; beta_logit, gate_logit: [B, T, H] in the same
+    dtype; beta_bias, gate_bias: [H] fp32; lengths: [B] int32, tokens past it are padding.
+    Returns (q, k, v [B, H, T, D], beta [B, H, T] fp32, gate or None): the inputs of
+    gka_forward_gated and gka_linear_forward."""
+    dev = _same_device(q, k, v, beta_logit, gate_logit, beta_bias, gate_bias, lengths)
+    B, T, H, Hk, D, dt, (sq, sk, sb, sg) = _block_in_args(q, k, beta_logit, gate_logit, beta_bias,
+                                                          gate_bias, lengths)
+    sv = _strided("v", v, q.dtype, (B, T, Hk, D))
+    qo, ko, vo = (torch.empty(B, H, T, D, dtype=q.dtype, device=dev) for _ in range(3))
+    beta = torch.empty(B, H, T, device=dev, dtype=torch.float32)
+    gate = torch.empty_like(beta) if gate_logit is not None or lengths is not None else None
+    _invoke("gka_block_in_forward", dev, stream, sq, sk, sv, sb, sg, _p(beta_bias), _p(gate_bias),
+            _p(lengths), _p(qo), _p(ko), _p(vo), _p(beta), _p(gate), B, T, H, Hk, D, dt, eps)
+    return qo, ko, vo, beta, gate
+
+
+def gka_block_in_backward(q, k, beta_logit, dq, dk, dv, dbeta, *, gate_logit=None, dgate=None,
+                          beta_bias=None, gate_bias=None, lengths=None, eps=1e-6, workspace=None,
+                          stream=None):
+    """Gradients of gka_block_in from those of its outputs: dq, dk, dv [B, H, T, D] in the
+    inputs' dtype, dbeta (and dgate exactly with gate_logit) [B, H, T] fp32.  Returns a dict
+    with dq [B, T, H, D], dk, dv [B, T, Hk, D], dbeta_logit (dgate_logit) [B, T, H], and for
+    each bias given dbeta_bias (dgate_bias) [H] fp32."""
+    dev = _same_device(q, k, beta_logit, gate_logit, dq, dk, dv, dbeta, dgate, beta_bias, gate_bias,
+                       lengths, workspace)
+    B, T, H, Hk, D, dt, (sq, sk, sb, sg) = _block_in_args(q, k, beta_logit, gate_logit, beta_bias,
+                                                          gate_bias, lengths)
+    _dense(dq, dk, dv, dbeta, dgate)
+    for n, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+        _need(n, t, (B, H, T, D), q.dtype)
+    _need("dbeta", dbeta, (B, H, T), torch.float32)
+    _need("dgate", dgate, (B, H, T), torch.float32)
+    if (gate_logit is None) != (dgate is None):
+        raise ValueError("dgate is needed exactly with gate_logit")
+    out = {"dq": torch.empty(B, T, H, D, dtype=q.dtype, device=dev),
+           "dk": torch.empty(B, T, Hk, D, dtype=q.dtype, device=dev),
+           "dv": torch.empty(B, T, Hk, D, dtype=q.dtype, device=dev),
+           "dbeta_logit": torch.empty(B, T, H, dtype=q.dtype, device=dev)}
+    if gate_logit is not None:
+        out["dgate_logit"] = torch.empty(B, T, H, dtype=q.dtype, device=dev)
+    for n, t in (("dbeta_bias", beta_bias), ("dgate_bias", gate_bias)):
+        if t is not None:
+            out[n] = torch.empty_like(t)
+    n = _lib().gka_block_in_backward_workspace_bytes(B, T, H, Hk, D, dt)
+    workspace = _scratch(n, workspace, dev)
+    _invoke("gka_block_in_backward", dev, stream, sq, sk, sb, sg, _p(beta_bias), _p(gate_bias),
+            _p(lengths), _p(dq), _p(dk), _p(dv), _p(dbeta), _p(dgate), _p(out["dq"]), _p(out["dk"]),
+            _p(out["dv"]), _p(out["dbeta_logit"]), _p(out.get("dgate_logit")),
+            _p(out.get("dbeta_bias")), _p(out.get("dgate_bias")), B, T, H, Hk, D, dt, eps,
+            _p(workspace), _nbytes(workspace))
+    return out
+
+
+def _block_out_args(o, w, z, v, skip):
+    B, H, T, D = o.shape
+    dt = _dtype(o)
+    _dense(o, w, v, skip)
+    _need("w", w, (D,), torch.float32)
+    _need("v", v, o.shape, o.dtype)
+    _need("skip", skip, (H,), torch.float32)
+    if (v is None) != (skip is None):
+        raise ValueError("v and skip come together")
+    return B, H, T, D, dt, _strided("z", z, o.dtype, (B, T, H, D))
+
+
+def gka_block_out(o, w, *, z=None, v=None, skip=None, eps=1e-6, y=None, stream=None):
+    """After the layer (see include/gka.h): y = rmsnorm(o + skip_h v) w silu(z), token-major.
+    o (and the layer's v): [B, H, T, D] fp32 or bf16; w: [D] fp32; skip: [H] fp32, with v;
+    z: [B, T, H, D] at any strides with contiguous rows.  Returns y [B, T, H, D]."""
+    dev = _same_device(o, w, z, v, skip, y)
+    B, H, T, D, dt, sz = _block_out_args(o, w, z, v, skip)
+    if y is None:
+        y = torch.empty(B, T, H, D, dtype=o.dtype, device=dev)
+    else:
+        _dense(y)
+        _need("y", y, (B, T, H, D), o.dtype)
+        for t in (o, w, v, skip):
+            _apart(y, t)
+    _invoke("gka_block_out_forward", dev, stream, _p(o), _p(v), sz, _p(w), _p(skip), _p(y), B, T, H,
+            D, dt, eps)
+    return y
+
+
+def gka_block_out_backward(o, w, dy, *, z=None, v=None, skip=None, eps=1e-6, workspace=None,
+                           stream=None):
+    """Gradients of gka_block_out from dy [B, T, H, D].  Returns a dict with do [B, H, T, D],
+    dw [D] fp32; with z: dz [B, T, H, D]; with v and skip: dv [B, H, T, D], dskip [H] fp32."""
+    dev = _same_device(o, w, dy, z, v, skip, workspace)
+    B, H, T, D, dt, sz = _block_out_args(o, w, z, v, skip)
+    _dense(dy)
+    _need("dy", dy, (B, T, H, D), o.dtype)
+    out = {"do": torch.empty_like(o), "dw": torch.empty_like(w)}
+    if z is not None:
+        out["dz"] = torch.empty(B, T, H, D, dtype=o.dtype, device=dev)
+    if v is not None:
+        out["dv"], out["dskip"] = torch.empty_like(v), torch.empty_like(skip)
+    n = _lib().gka_block_out_backward_workspace_bytes(B, T, H, D, dt)
+    workspace = _scratch(n, workspace, dev)
+    _invoke("gka_block_out_backward", dev, stream, _p(o), _p(v), sz, _p(w), _p(skip), _p(dy),
+            _p(out["do"]), _p(out.get("dv")), _p(out.get("dz")), _p(out["dw"]), _p(out.get("dskip")),
+            B, T, H, D, dt, eps, _p(workspace), _nbytes(workspace))
     return out
 
 
