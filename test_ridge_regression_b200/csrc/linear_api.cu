@@ -11,6 +11,7 @@
 #include "block_rows.cuh"
 #include "host.cuh"
 #include "linear_simt.cuh"
+#include "linear_tc.cuh"
 
 namespace gka {
 
@@ -22,7 +23,9 @@ static bool valid_dtype(gka_dtype dt) { return dt == GKA_F32 || dt == GKA_BF16; 
 // Gated linear recurrence
 // ---------------------------------------------------------------------------
 struct LinLayout {
+    bool tc;                                   // tensor-core path
     int N, S, ZS;                              // chunks, segments, column splits
+    int dots, fdots;                           // planes of the dbeta terms' partial sums
     size_t agg, segdec;                        // segment aggregates, decays (S > 1)
     size_t states, zeta, eta, fdot;            // backward
     size_t total;
@@ -39,9 +42,13 @@ static int lin_layout(int B, int H, int T, int D, gka_dtype dt, bool bwd, LinLay
     if (!supported_d(D)) return GKA_ERR_UNSUPPORTED;
     if ((size_t)B * H > 65535) return GKA_ERR_UNSUPPORTED;   // grid limit
     const size_t BH = (size_t)B * H, st = sizeof(float) * (size_t)D * D;
-    L->ZS = D / kLinZN;
-    L->N = (int)(((long long)T + kLinC - 1) / kLinC);
-    L->S = lin_segments((int)BH * L->ZS, L->N, 3);
+    L->tc = dt == GKA_BF16 && D == 128;
+    const int C = L->tc ? kLtC : kLinC;
+    L->ZS = D / (L->tc ? kLtZN : kLinZN);
+    L->N = (int)(((long long)T + C - 1) / C);
+    L->S = lin_segments((int)BH * L->ZS, L->N, L->tc ? 1 : 3);
+    L->dots = L->tc ? kLtDots : L->ZS;
+    L->fdots = L->tc ? kLtFdots : L->ZS;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -53,9 +60,9 @@ static int lin_layout(int B, int H, int T, int D, gka_dtype dt, bool bwd, LinLay
     L->states = L->zeta = L->eta = L->fdot = off;
     if (bwd) {
         L->states = take(BH * L->N * st);
-        L->zeta = take(L->ZS * BH * T * sizeof(float));
-        L->eta = take(L->ZS * BH * T * sizeof(float));
-        L->fdot = take(L->ZS * BH * L->N * sizeof(float));
+        L->zeta = take(L->dots * BH * T * sizeof(float));
+        L->eta = take(L->dots * BH * T * sizeof(float));
+        L->fdot = take(L->fdots * BH * L->N * sizeof(float));
     }
     L->total = off;
     return GKA_OK;
@@ -170,6 +177,131 @@ static int lin_backward(const LinCall &c, const LinLayout &L) {
     return check_launch();
 }
 
+// ---------------------------------------------------------------------------
+// The same calls on the tensor cores
+// ---------------------------------------------------------------------------
+// [B*H][T][128] bf16 in boxes of 64 columns x 128 tokens of one head, 128-byte
+// swizzle; tokens past T read as zeros.
+static int head_map(CUtensorMap *m, const void *base, int T, int BH) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return cuda_fail(cudaErrorNotSupported);
+    cuuint64_t dims[3] = {128, (cuuint64_t)T, (cuuint64_t)BH};
+    cuuint64_t strides[2] = {256, (cuuint64_t)T * 256};
+    cuuint32_t box[3] = {64, kLtC, 1}, es[3] = {1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
+                           strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GKA_OK : cuda_fail(cudaErrorInvalidValue);
+}
+
+template <bool REV, bool OUT>
+static int lin_tc_launch(const LinTcArgs &a, int passes, int prof, cudaStream_t s) {
+    cudaError_t e;
+    int *flag = nullptr;
+    if (int rc = timeout_flag_ptr(&flag)) return rc;
+    auto kern = k_linear_tc<REV, OUT>;
+    if ((e = set_smem(kern, LtSmem::bytes)) != cudaSuccess) return cuda_fail(e);
+    const LinPass &p = a.pass[0].p;
+    ProfScope ps(prof, s);
+    kern<<<dim3(2 * passes, p.BH, p.S), kLtThreads, LtSmem::bytes, s>>>(a, flag);
+    return check_launch();
+}
+
+template <bool REV>
+static int lin_tc_starts(LinTcArgs &a, const LinLayout &L, char *ws, const float *init, int prof,
+                         cudaStream_t s) {
+    LinPass &p = a.pass[0].p;
+    if (L.S == 1) {
+        p.start = init;
+        return GKA_OK;
+    }
+    p.agg = reinterpret_cast<float *>(ws + L.agg);
+    p.segdec = reinterpret_cast<float *>(ws + L.segdec);
+    if (int rc = lin_tc_launch<REV, false>(a, 1, prof, s)) return rc;
+    ProfScope ps(prof, s);
+    k_linear_scan<<<dim3(16, p.BH), 256, 0, s>>>(p.agg, p.segdec, init, L.S, 128 * 128, REV);
+    p.start = p.agg;
+    return check_launch();
+}
+
+static int lin_tc_forward(const LinCall &c, const LinLayout &L) {
+    LinTcArgs a = {};
+    if (int rc = head_map(&a.pass[0].x, c.q, c.T, c.BH)) return rc;
+    if (int rc = head_map(&a.pass[0].y, c.k, c.T, c.BH)) return rc;
+    if (int rc = head_map(&a.pass[0].z, c.v, c.T, c.BH)) return rc;
+    LinPass &p = a.pass[0].p;
+    p.out = c.o;
+    p.beta = c.beta; p.gate = c.gate;
+    p.scale = c.scale;
+    p.log_min = kLogBetaMin;
+    p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S;
+    p.zy = 1;
+    if (int rc = lin_tc_starts<false>(a, L, c.ws, c.init, GKA_KERNEL_LINEAR, c.s)) return rc;
+    p.last = c.last;
+    return lin_tc_launch<false, true>(a, 1, GKA_KERNEL_LINEAR, c.s);
+}
+
+static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
+    constexpr int kProf = GKA_KERNEL_LINEAR_GRAD;
+    CUtensorMap q, k, v, d_o;
+    if (int rc = head_map(&q, c.q, c.T, c.BH)) return rc;
+    if (int rc = head_map(&k, c.k, c.T, c.BH)) return rc;
+    if (int rc = head_map(&v, c.v, c.T, c.BH)) return rc;
+    if (int rc = head_map(&d_o, c.d_o, c.T, c.BH)) return rc;
+    LinPass p = {};
+    p.beta = c.beta; p.gate = c.gate;
+    p.scale = c.scale;
+    p.log_min = kLinLogMinBwd;
+    p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S;
+    LinPairsTc w = {};
+    w.p.zeta = reinterpret_cast<float *>(c.ws + L.zeta);
+    w.p.eta = reinterpret_cast<float *>(c.ws + L.eta);
+    w.p.fdot = reinterpret_cast<float *>(c.ws + L.fdot);
+    // dq, forwards in time; M before every chunk stays for F
+    LinTcArgs f = {};
+    f.pass[0].x = d_o; f.pass[0].y = v; f.pass[0].z = k;
+    f.pass[0].p = p;
+    if (int rc = lin_tc_starts<false>(f, L, c.ws, c.init, kProf, c.s)) return rc;
+    LinPass &pf = f.pass[0].p;
+    pf.out = c.dq;
+    pf.xd = c.q;
+    pf.dot = const_cast<float *>(w.p.zeta);
+    pf.states = reinterpret_cast<float *>(c.ws + L.states);
+    if (int rc = lin_tc_launch<false, true>(f, 1, kProf, c.s)) return rc;
+    // dv and dk, backwards in time, in one launch
+    LinTcArgs r = {};
+    r.pass[0].x = k; r.pass[0].y = q; r.pass[0].z = d_o;
+    r.pass[0].p = p;
+    r.pass[0].p.zy = 1;
+    if (int rc = lin_tc_starts<true>(r, L, c.ws, c.dlast, kProf, c.s)) return rc;
+    LinPass &pv = r.pass[0].p, &pk = r.pass[1].p;
+    r.pass[1].x = v; r.pass[1].y = d_o; r.pass[1].z = q;
+    pk = p;
+    pk.start = pv.start;
+    pk.out = c.dk;
+    pv.out = c.dv;
+    pv.xd = c.v;
+    pv.dot = const_cast<float *>(w.p.eta);
+    pv.states_in = pf.states;
+    pv.fdot = const_cast<float *>(w.p.fdot);
+    pv.last = c.dinit;
+    if (int rc = lin_tc_launch<true, true>(r, 2, kProf, c.s)) return rc;
+    w.q = q; w.k = k; w.v = v; w.d_o = d_o;
+    w.p.beta = c.beta; w.p.gate = c.gate;
+    w.p.dbeta = c.dbeta; w.p.dgate = c.dgate;
+    w.p.scale = c.scale;
+    w.p.BH = c.BH; w.p.T = c.T; w.p.N = L.N; w.p.ZS = L.dots;
+    w.FS = L.fdots;
+    cudaError_t e;
+    int *flag = nullptr;
+    if (int rc = timeout_flag_ptr(&flag)) return rc;
+    if ((e = set_smem(k_linear_pairs_tc, LpSmem::bytes)) != cudaSuccess) return cuda_fail(e);
+    ProfScope ps(kProf, c.s);
+    k_linear_pairs_tc<<<dim3(L.N, c.BH), kLpThreads, LpSmem::bytes, c.s>>>(w, flag);
+    return check_launch();
+}
+
 // f(type tag, size tag) for the call's type and head size.
 template <typename F>
 static int by_type(gka_dtype dt, int D, F f) {
@@ -276,6 +408,7 @@ int gka_linear_forward(const void *q, const void *k, const void *v, const float 
     c.BH = (int)BH; c.T = T; c.scale = scale;
     c.ws = static_cast<char *>(workspace);
     c.s = s;
+    if (L.tc) return lin_tc_forward(c, L);
     return by_type(dt, D, [&](auto tag, auto d) {
         return lin_forward<decltype(tag), decltype(d)::value>(c, L);
     });
@@ -310,6 +443,7 @@ int gka_linear_backward(const void *q, const void *k, const void *v, const float
     c.BH = (int)BH; c.T = T; c.scale = scale;
     c.ws = static_cast<char *>(workspace);
     c.s = s;
+    if (L.tc) return lin_tc_backward(c, L);
     return by_type(dt, D, [&](auto tag, auto d) {
         return lin_backward<decltype(tag), decltype(d)::value>(c, L);
     });

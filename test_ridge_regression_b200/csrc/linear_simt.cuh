@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(kLinThreads) k_linear_pass(const LinPass p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int zsp = blockIdx.x, z0 = zsp * ZN, bh = blockIdx.y, seg = blockIdx.z;
     const int n0 = lin_seg(seg, p.S, p.N), n1 = lin_seg(seg + 1, p.S, p.N);
+    if (!OUT && seg == (REV ? 0 : p.S - 1)) return;   // never carried on
     const T *X = static_cast<const T *>(p.x) + (size_t)bh * p.T * D;
     const T *Y = static_cast<const T *>(p.y) + (size_t)bh * p.T * D;
     const T *Z = static_cast<const T *>(p.z) + (size_t)bh * p.T * D;
@@ -347,7 +348,7 @@ k_linear_scan(float *__restrict__ agg, const float *__restrict__ segdec,
         float bv[kB];
 #pragma unroll
         for (int j = 0; j < kB; ++j)
-            if (s0 + j < S) {
+            if (s0 + j < S - 1) {   // the last one's aggregate is not carried on
                 const int s = rev ? S - 1 - s0 - j : s0 + j;
                 av[j] = *reinterpret_cast<const float4 *>(base + (size_t)s * D2);
                 bv[j] = segdec[(size_t)bh * S + s];
@@ -357,7 +358,8 @@ k_linear_scan(float *__restrict__ agg, const float *__restrict__ segdec,
             if (s0 + j < S) {
                 const int s = rev ? S - 1 - s0 - j : s0 + j;
                 *reinterpret_cast<float4 *>(base + (size_t)s * D2) = run;
-                run = make_float4(fmaf(bv[j], run.x, av[j].x), fmaf(bv[j], run.y, av[j].y),
+                if (s0 + j < S - 1)
+                    run = make_float4(fmaf(bv[j], run.x, av[j].x), fmaf(bv[j], run.y, av[j].y),
                                   fmaf(bv[j], run.z, av[j].z), fmaf(bv[j], run.w, av[j].w));
             }
     }
