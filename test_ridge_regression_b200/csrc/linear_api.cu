@@ -230,8 +230,8 @@ static int lin_tc_forward(const LinCall &c, const LinLayout &L) {
     if (int rc = head_map(&a.pass[0].x, c.q, c.T, c.BH)) return rc;
     if (int rc = head_map(&a.pass[0].y, c.k, c.T, c.BH)) return rc;
     if (int rc = head_map(&a.pass[0].z, c.v, c.T, c.BH)) return rc;
+    if (int rc = head_map(&a.pass[0].out, c.o, c.T, c.BH)) return rc;
     LinPass &p = a.pass[0].p;
-    p.out = c.o;
     p.beta = c.beta; p.gate = c.gate;
     p.scale = c.scale;
     p.log_min = kLogBetaMin;
@@ -264,7 +264,7 @@ static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
     f.pass[0].p = p;
     if (int rc = lin_tc_starts<false>(f, L, c.ws, c.init, kProf, c.s)) return rc;
     LinPass &pf = f.pass[0].p;
-    pf.out = c.dq;
+    if (int rc = head_map(&f.pass[0].out, c.dq, c.T, c.BH)) return rc;
     pf.xd = c.q;
     pf.dot = const_cast<float *>(w.p.zeta);
     pf.states = reinterpret_cast<float *>(c.ws + L.states);
@@ -277,14 +277,15 @@ static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
     if (int rc = lin_tc_starts<true>(r, L, c.ws, c.dlast, kProf, c.s)) return rc;
     LinPass &pv = r.pass[0].p, &pk = r.pass[1].p;
     r.pass[1].x = v; r.pass[1].y = d_o; r.pass[1].z = q;
+    if (int rc = head_map(&r.pass[0].out, c.dv, c.T, c.BH)) return rc;
+    if (int rc = head_map(&r.pass[1].out, c.dk, c.T, c.BH)) return rc;
     pk = p;
     pk.start = pv.start;
-    pk.out = c.dk;
-    pv.out = c.dv;
+    // dk's state has dq's orientation: F there reads what dq's pass wrote, as it wrote it
+    pk.states_in = pf.states;
+    pk.fdot = const_cast<float *>(w.p.fdot);
     pv.xd = c.v;
     pv.dot = const_cast<float *>(w.p.eta);
-    pv.states_in = pf.states;
-    pv.fdot = const_cast<float *>(w.p.fdot);
     pv.last = c.dinit;
     if (int rc = lin_tc_launch<true, true>(r, 2, kProf, c.s)) return rc;
     w.q = q; w.k = k; w.v = v; w.d_o = d_o;

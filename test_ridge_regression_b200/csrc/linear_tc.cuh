@@ -30,10 +30,15 @@
 // diagonal blocks evaluate exponentials, blocks beyond the diagonal are zero.
 //
 // Chunk n's steps, by role (-> barrier -> waiting role):
-//   math: parts(n) -> MMA DS(n);  S operand(n) -> MMA OS(n);  P(n) -> weights ->
-//         MMA OI(n);  S += DS(n);  OS, OI -> out rows
+//   math: S operand(n) -> MMA OS(n);  parts(n) -> MMA DS(n);  P(n) -> weights ->
+//         MMA OI(n);  S += DS(n);  OS, OI -> rows staged in shared memory -> TMA store
 //   issuer: between them loads x(n + 1) once P(n) and OS(n) are done, y and z of
 //         n + 2 once chunk n is, and issues P(n + 1) while OI(n) runs
+// Shared memory's bandwidth is what the products compete for with the warps, so the
+// parts of one operand are columns of one product (N = 192 for DS, 128 for OS: the
+// other operand is read once) and their sums are taken in registers; rows leave
+// through shared memory and TMA, since a thread's 32 bytes of a row, stored from
+// registers, cost a pass of the memory pipe per row.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -65,13 +70,15 @@ struct LtSmem {
     // table floats: a, u, g, lrel, ta, c[3] of 128 tokens each, then b
     static constexpr uint32_t TABF = 8 * kLtC + 4;
     static constexpr uint32_t BARS = TAB + 2 * 4 * TABF;
-    static constexpr uint32_t TBASE = BARS + 8 * 16;      // TMEM base, abort flag
+    static constexpr uint32_t TBASE = BARS + 8 * 22;      // TMEM base, abort flag
     static constexpr uint32_t END = TBASE + 16;
     static constexpr size_t bytes = END + 1024;
 };
 
 struct LinTcPass {
-    CUtensorMap x, y, z;          // [B*H][T][128] bf16, box 64 x 128 x 1, 128B swizzle, zero fill
+    // [B*H][T][128] bf16, boxes of 64 columns x 128 tokens of a head, 128B swizzle; tokens
+    // past T read as zeros and are not written
+    CUtensorMap x, y, z, out;
     LinPass p;
 };
 struct LinTcArgs {
@@ -79,11 +86,20 @@ struct LinTcArgs {
 };
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2,
-                                            uint64_t *bar) {
+                                            uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int c0, int c1, int c2,
+                                             const void *src) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+            reinterpret_cast<uint64_t>(map)),
+        "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
         : "memory");
 }
 
@@ -98,62 +114,134 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-// Bounded wait that also gives up once another role has (`abort` set).
-__device__ __forceinline__ bool lt_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+// Bounded wait that also gives up once another role has (the word at shared address
+// `abort` set).  Barriers here are shared addresses: a register each, made where used.
+__device__ __forceinline__ bool lt_wait(uint32_t bar, uint32_t parity, uint32_t abort) {
+#pragma unroll 1
     for (uint32_t i = 0; i < kLtProbes; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 255) == 255 && *abort) break;
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((i & 255) == 255) {
+            uint32_t a;
+            asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(a) : "r"(abort) : "memory");
+            if (a) break;
+        }
     }
-    *abort = 1;
+    asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
     return false;
+}
+// After a time-out: a bounded wait for work in flight.
+__device__ __noinline__ void lt_drain(uint32_t bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kLtProbes; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return;
+    }
+}
+__device__ __forceinline__ void lt_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void lt_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void lt_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void lt_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
+
+// A sum of log decays as an unevaluated pair of floats (about 45 bits): differences of
+// cumulative logs keep fp32 precision after a reset, at a fraction of the latency that
+// doubles have on the one warp that forms the tables (1200 against 5400 cycles a chunk).
+struct Log2Sum {
+    float hi, lo;
+};
+__device__ __forceinline__ Log2Sum operator+(Log2Sum a, Log2Sum b) {
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
+    const float h = s + e;
+    return {h, e - (h - s)};
+}
+// 2^(a - b)
+__device__ __forceinline__ float exp2_diff(Log2Sum a, Log2Sum b) {
+    return exp2f((a.hi - b.hi) + (a.lo - b.lo));
+}
+__device__ __forceinline__ Log2Sum shfl(Log2Sum x, int src) {
+    return {__shfl_sync(0xffffffffu, x.hi, src), __shfl_sync(0xffffffffu, x.lo, src)};
 }
 
 // Decay tables of one chunk by one warp; lane l holds tokens 4l..4l+3, whose beta and
 // gate are bv and gv (1 and 0 past the sequence's end).  Returns the chunk's log2 decay.
 template <bool REV>
-__device__ __forceinline__ double lt_tables(float *tab, const float *bv, const float *gv, float scale,
-                                            float log2_min) {
+__device__ __forceinline__ float lt_tables(float *tab, const float *bv, const float *gv, float scale,
+                                           float log2_min) {
     const int lane = threadIdx.x & 31, blk = lane >> 3;
     float *ta_a = tab, *ta_u = tab + kLtC, *ta_g = tab + 2 * kLtC, *ta_l = tab + 3 * kLtC,
           *ta_t = tab + 4 * kLtC, *ta_c = tab + 5 * kLtC;
-    double l[4], run = 0.0;
+    const Log2Sum zero = {0.f, 0.f};
+    Log2Sum l[4], run = zero;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-        run += (double)fmaxf(log2f(bv[p]), log2_min);
+        run = run + Log2Sum{fmaxf(log2f(bv[p]), log2_min), 0.f};
         l[p] = run;
     }
-    double incl = run;
+    Log2Sum incl = run;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        const Log2Sum y = {__shfl_up_sync(0xffffffffu, incl.hi, o), __shfl_up_sync(0xffffffffu, incl.lo, o)};
+        if (lane >= o) incl = incl + y;
     }
-    const double excl = incl - run, lC = __shfl_sync(0xffffffffu, incl, 31);
-    double edge[5];   // cumulative log at the start of block 0..3 and at the end
-    edge[0] = 0.0;
+    Log2Sum excl = {__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+    if (lane == 0) excl = zero;
+    Log2Sum edge[4];   // cumulative log at the end of block 0..3
 #pragma unroll
-    for (int b = 1; b < 5; ++b) edge[b] = __shfl_sync(0xffffffffu, incl, 8 * b - 1);
-    const double start = blk == 0 ? 0.0 : blk == 1 ? edge[1] : blk == 2 ? edge[2] : edge[3];
-    const double stop = blk == 0 ? edge[1] : blk == 1 ? edge[2] : blk == 2 ? edge[3] : edge[4];
+    for (int b = 0; b < 4; ++b) edge[b] = shfl(incl, 8 * b + 7);
+    const Log2Sum start = blk == 0 ? zero : blk == 1 ? edge[0] : blk == 2 ? edge[1] : edge[2];
+    const Log2Sum stop = blk == 0 ? edge[0] : blk == 1 ? edge[1] : blk == 2 ? edge[2] : edge[3];
+    float va[4], vu[4], vl[4], vt[4], vc[3][4];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-        const int t = 4 * lane + p;
-        const double lt = excl + l[p];
-        ta_a[t] = REV ? exp2f((float)(lC - lt)) : scale * exp2f((float)lt);
-        ta_u[t] = REV ? scale * exp2f((float)lt) : gv[p] * exp2f((float)(lC - lt));
-        ta_g[t] = gv[p];
-        ta_l[t] = (float)(lt - start);
-        ta_t[t] = REV ? scale * exp2f((float)(stop - lt)) : exp2f((float)(lt - start));
+        const Log2Sum lt = excl + l[p];
+        va[p] = REV ? exp2_diff(edge[3], lt) : scale * exp2_diff(lt, zero);
+        vu[p] = REV ? scale * exp2_diff(lt, zero) : gv[p] * exp2_diff(edge[3], lt);
+        vl[p] = (lt.hi - start.hi) + (lt.lo - start.lo);
+        vt[p] = REV ? scale * exp2_diff(stop, lt) : exp2f(vl[p]);
+        // forward: c[b] serves block row b + 1, the blocks before it; backward: block row
+        // b, the blocks after it (other entries are not read)
 #pragma unroll
-        for (int b = 0; b < 3; ++b) {
-            // forward: c[b] serves block row b + 1, the blocks before it; backward: block
-            // row b, the blocks after it
-            if (REV ? blk > b : blk <= b)
-                ta_c[b * kLtC + t] = REV ? exp2f((float)(lt - edge[b + 1]))
-                                         : gv[p] * exp2f((float)(edge[b + 1] - lt));
-        }
+        for (int b = 0; b < 3; ++b)
+            vc[b][p] = REV ? exp2_diff(lt, edge[b]) : gv[p] * exp2_diff(edge[b], lt);
     }
-    if (lane == 0) tab[8 * kLtC] = exp2f((float)lC);
+    auto put = [&](float *dst, const float *v) {
+        *reinterpret_cast<float4 *>(dst + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+    };
+    put(ta_a, va);
+    put(ta_u, vu);
+    put(ta_g, gv);
+    put(ta_l, vl);
+    put(ta_t, vt);
+#pragma unroll
+    for (int b = 0; b < 3; ++b)
+        if (REV ? blk > b : blk <= b) put(ta_c + b * kLtC, vc[b]);
+    const float lC = edge[3].hi + edge[3].lo;
+    if (lane == 0) tab[8 * kLtC] = exp2f(lC);
     return lC;
 }
 
@@ -166,12 +254,13 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smem_align1024(smraw);
     const uint32_t sb = smem_u32(sm);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);
-    uint64_t *b_yz = bars, *b_w = bars + 2, *b_tfree = bars + 4, *b_x = bars + 6, *b_p = bars + 7,
-             *b_parts = bars + 8, *b_s = bars + 9, *b_pb = bars + 10, *b_ds = bars + 11, *b_o = bars + 12,
-             *b_xfree = bars + 13, *b_fin = bars + 14;
+    const uint32_t bars = sb + L::BARS;
+    const uint32_t b_x = bars, b_p = bars + 8, b_parts = bars + 16, b_s = bars + 24, b_pb = bars + 32,
+                   b_ds = bars + 40, b_o = bars + 48, b_xfree = bars + 56, b_out = bars + 64,
+                   b_ofree = bars + 72, b_fin = bars + 80;
+    const uint32_t b_yz = bars + 88, b_w = bars + 104, b_tfree = bars + 120, b_quart = bars + 136;
+    const uint32_t abort = sb + L::TBASE + 4;
     uint32_t *tbase = reinterpret_cast<uint32_t *>(sm + L::TBASE);
-    volatile int *abort = reinterpret_cast<volatile int *>(sm + L::TBASE + 4);
     float *s_tab = reinterpret_cast<float *>(sm + L::TAB);
     const LinTcPass &A = args.pass[blockIdx.x >> 1];
     const LinPass &p = A.p;
@@ -184,35 +273,38 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
 
     if (tid == kLtMath) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&b_yz[i], 1);
-            mbar_init(&b_w[i], 32);
-            mbar_init(&b_tfree[i], 16);
+            lt_init(b_yz + 8 * i, 1);
+            lt_init(b_w + 8 * i, 32);
+            lt_init(b_tfree + 8 * i, 16);
         }
-        mbar_init(b_x, 1);
-        mbar_init(b_p, 1);
-        mbar_init(b_parts, 16);
-        mbar_init(b_s, 16);
-        mbar_init(b_pb, 16);
-        mbar_init(b_ds, 1);
-        mbar_init(b_o, 1);
-        mbar_init(b_xfree, 1);
-        mbar_init(b_fin, 1);
-        *abort = 0;
+        lt_init(b_x, 1);
+        lt_init(b_p, 1);
+        lt_init(b_parts, 16);
+        lt_init(b_s, 16);
+        lt_init(b_pb, 16);
+        lt_init(b_ds, 1);
+        lt_init(b_o, 1);
+        lt_init(b_xfree, 1);
+        lt_init(b_out, 16);
+        lt_init(b_ofree, 1);
+        for (int i = 0; i < 4; ++i) lt_init(b_quart + 8 * i, 4);
+        lt_init(b_fin, 1);
+        asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(0u) : "memory");
         fence_mbar_init();
     }
     __syncthreads();
     int loads_x = 0, loads_yz[2] = {0, 0};   // issuer: loads begun per barrier
     auto load_yz = [&](int it) {
         const int st = it & 1, t0 = chunk(it) * C;
-        mbar_arrive_expect_tx(&b_yz[st], L::TILE + L::HALF);
-        tma_load_3d(sm + L::Y + st * L::TILE, &A.y, 0, t0, bh, &b_yz[st]);
-        tma_load_3d(sm + L::Y + st * L::TILE + L::HALF, &A.y, 64, t0, bh, &b_yz[st]);
-        tma_load_3d(sm + L::Z + st * L::HALF, &A.z, zh * kLtZN, t0, bh, &b_yz[st]);
+        lt_expect(b_yz + 8 * st, L::TILE + L::HALF);
+        tma_load_3d(sm + L::Y + st * L::TILE, &A.y, 0, t0, bh, b_yz + 8 * st);
+        tma_load_3d(sm + L::Y + st * L::TILE + L::HALF, &A.y, 64, t0, bh, b_yz + 8 * st);
+        tma_load_3d(sm + L::Z + st * L::HALF, &A.z, zh * kLtZN, t0, bh, b_yz + 8 * st);
         ++loads_yz[st];
     };
     auto load_x = [&](int it) {
         const int t0 = chunk(it) * C;
-        mbar_arrive_expect_tx(b_x, L::TILE);
+        lt_expect(b_x, L::TILE);
         tma_load_3d(sm + L::X, &A.x, 0, t0, bh, b_x);
         tma_load_3d(sm + L::X + L::HALF, &A.x, 64, t0, bh, b_x);
         ++loads_x;
@@ -230,53 +322,58 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tbase;
-    constexpr uint32_t kP = 0, kOI = 128, kOS = 192, kDS = 256, kPB = 320;   // TMEM columns
+    // TMEM columns; the bf16 weighted scores take the place of the scores
+    constexpr uint32_t kP = 0, kPB = 0, kOI = 128, kOS = 192, kDS = 320;
 
     if (warp == 16) {
         if (lane == 0) {
             constexpr uint32_t ID_P = tc::idesc_bf16(128, 128, false, false);
             constexpr uint32_t ID_O = tc::idesc_bf16(128, 64, false, true);
-            constexpr uint32_t ID_D = tc::idesc_bf16(128, 64, true, true);
-            auto kmaj = [&](uint32_t base, int kk) {
-                return tc::sdesc(sb + base + (kk >> 2) * L::HALF + (kk & 3) * 32, 16, 1024);
+            constexpr uint32_t ID_S = tc::idesc_bf16(128, 128, false, true);
+            constexpr uint32_t ID_D = tc::idesc_bf16(128, 192, true, true);
+            // first descriptors of an operand, opaque so that the eight K steps' are not kept
+            // in registers across the loop, and the step to the kk-th
+            auto first = [&](uint32_t base, uint32_t lbo) {
+                uint64_t d = tc::sdesc(sb + base, lbo, 1024);
+                asm volatile("" : "+l"(d));
+                return d;
             };
-            auto mnmaj = [&](uint32_t base, int kk) {
-                return tc::sdesc(sb + base + kk * 2048, L::HALF, 1024);
-            };
+            auto kmaj = [](int kk) { return (uint64_t)(((kk >> 2) * L::HALF + (kk & 3) * 32) >> 4); };
+            auto mnmaj = [](int kk) { return (uint64_t)((kk * 2048) >> 4); };
             auto issue_p = [&](int it) {
-                if (!lt_wait(b_x, it & 1, abort) || !lt_wait(&b_yz[it & 1], (it >> 1) & 1, abort))
+                if (!lt_wait(b_x, it & 1, abort) || !lt_wait(b_yz + 8 * (it & 1), (it >> 1) & 1, abort))
                     return false;
+                const uint64_t x = first(L::X, 16), y = first(L::Y + (it & 1) * L::TILE, 16);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    tc::mma_f16(tmem + kP, kmaj(L::X, kk), kmaj(L::Y + (it & 1) * L::TILE, kk), ID_P,
-                                kk > 0);
-                tc::commit(b_p);
+                    tc::mma_f16(tmem + kP, x + kmaj(kk), y + kmaj(kk), ID_P, kk > 0);
+                lt_commit(b_p);
                 return true;
             };
             bool ok = !OUT || issue_p(0);
             for (int it = 0; ok && it < NL; ++it) {
                 const int st = it & 1, ph = it & 1;
-                ok = lt_wait(b_parts, ph, abort);
-                if (!ok) break;
-                tc::fence_after_sync();
-#pragma unroll
-                for (int q = 0; q < 3; ++q)
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        tc::mma_f16(tmem + kDS, mnmaj(L::Y + st * L::TILE, kk),
-                                    mnmaj(L::PARTS + q * L::HALF, kk), ID_D, (q | kk) != 0);
-                tc::commit(b_ds);
                 if (OUT) {
                     ok = lt_wait(b_s, ph, abort);
                     if (!ok) break;
                     tc::fence_after_sync();
+                    const uint64_t x = first(L::X, 16), s = first(L::SOP, L::HALF);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
+                    for (int kk = 0; kk < 8; ++kk)
+                        tc::mma_f16(tmem + kOS, x + kmaj(kk), s + mnmaj(kk), ID_S, kk > 0);
+                    lt_commit(b_xfree);
+                }
+                ok = lt_wait(b_parts, ph, abort);
+                if (!ok) break;
+                tc::fence_after_sync();
+                {
+                    const uint64_t y = first(L::Y + st * L::TILE, L::HALF), u = first(L::PARTS, L::HALF);
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            tc::mma_f16(tmem + kOS, kmaj(L::X, kk), mnmaj(L::SOP + q * L::HALF, kk), ID_O,
-                                        (q | kk) != 0);
-                    tc::commit(b_xfree);
+                    for (int kk = 0; kk < 8; ++kk)
+                        tc::mma_f16(tmem + kDS, y + mnmaj(kk), u + mnmaj(kk), ID_D, kk > 0);
+                }
+                lt_commit(b_ds);
+                if (OUT) {
                     if (it + 1 < NL) {
                         ok = lt_wait(b_xfree, ph, abort);
                         if (!ok) break;
@@ -285,11 +382,11 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                     ok = lt_wait(b_pb, ph, abort);
                     if (!ok) break;
                     tc::fence_after_sync();
+                    const uint64_t z = first(L::Z + st * L::HALF, L::HALF);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_ta(tmem + kOI, tmem + kPB + kk * 8, mnmaj(L::Z + st * L::HALF, kk), ID_O,
-                                    kk > 0);
-                    tc::commit(b_o);
+                        mma_bf16_ta(tmem + kOI, tmem + kPB + kk * 8, z + mnmaj(kk), ID_O, kk > 0);
+                    lt_commit(b_o);
                     if (it + 1 < NL) ok = issue_p(it + 1);
                     if (ok && it + 2 < NL) {
                         ok = lt_wait(b_o, ph, abort);
@@ -303,11 +400,11 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             if (!ok) {
                 // a wait gave up: flag it, then drain this thread's products and copies
                 atomicExch(timeout_flag, 1);
-                tc::commit(b_fin);
-                mbar_wait_bounded(b_fin, 0, kLtProbes);
-                if (loads_x) mbar_wait_bounded(b_x, (loads_x - 1) & 1, kLtProbes);
+                lt_commit(b_fin);
+                lt_drain(b_fin, 0);
+                if (loads_x) lt_drain(b_x, (loads_x - 1) & 1);
                 for (int i = 0; i < 2; ++i)
-                    if (loads_yz[i]) mbar_wait_bounded(&b_yz[i], (loads_yz[i] - 1) & 1, kLtProbes);
+                    if (loads_yz[i]) lt_drain(b_yz + 8 * i, (loads_yz[i] - 1) & 1);
             }
         }
         __syncwarp();
@@ -326,10 +423,21 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             }
         };
         fetch(0);
-        double seglog = 0.0;
+        float seglog = 0.f;
         bool ok = true;
+        // chunk it's output rows, staged by the arithmetic warps, on their way
+        auto store_out = [&](int it) {
+            bool done = lt_wait(b_out, it & 1, abort);
+            if (lane == 0 && done) {
+                tma_store_3d(&A.out, zh * kLtZN, chunk(it) * C, bh, sm + L::PARTS);
+                tc::bulk_commit();
+                tc::bulk_wait_read0();
+                lt_arrive(b_ofree);
+            }
+            return __all_sync(0xffffffffu, done);
+        };
         for (int it = 0; it < NL; ++it) {
-            if (it >= 2) ok = __all_sync(0xffffffffu, lt_wait(&b_tfree[it & 1], ((it - 2) >> 1) & 1, abort));
+            if (it >= 2) ok = __all_sync(0xffffffffu, lt_wait(b_tfree + 8 * (it & 1), ((it - 2) >> 1) & 1, abort));
             if (!ok) break;
             float cb[4], cg[4];
 #pragma unroll
@@ -339,10 +447,14 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             }
             if (it + 1 < NL) fetch(it + 1);
             seglog += lt_tables<REV>(s_tab + (it & 1) * L::TABF, cb, cg, p.scale, log2_min);
-            mbar_arrive(&b_w[it & 1]);
+            lt_arrive(b_w + 8 * (it & 1));
+            if (OUT && it >= 1) ok = store_out(it - 1);
+            if (!ok) break;
         }
+        if (OUT && ok) store_out(NL - 1);
+        if (lane == 0) tc::bulk_wait0();
         if (!OUT && ok && lane == 0 && blockIdx.x == 0)
-            p.segdec[(size_t)bh * p.S + seg] = exp2f((float)seglog);
+            p.segdec[(size_t)bh * p.S + seg] = exp2f(seglog);
     } else {
         const int quarter = warp & 3, cg = warp >> 2;
         const int row = quarter * 32 + lane;              // TMEM lane: token of P, OI, OS; y row of S
@@ -360,18 +472,38 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
 #pragma unroll
             for (int j = 0; j < 16; ++j) st[j] = p.start[at(base, j)];
         }
+        auto arrive = [&](uint32_t bar) {
+            __syncwarp();
+            if (lane == 0) lt_arrive(bar);
+        };
         bool ok = true;
         for (int it = 0; it < NL; ++it) {
             const int sg = it & 1, ph = it & 1, ph2 = (it >> 1) & 1, n = chunk(it);
             const float *tab = s_tab + sg * L::TABF;
-            auto arrive = [&](uint64_t *bar) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar);
-            };
+            if (OUT) {
+                // the state before the chunk as the B operand, rows of y, two bf16 parts
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t a[4], b[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y0 = st[h * 8 + 2 * e], y1 = st[h * 8 + 2 * e + 1];
+                        a[e] = bf16x2_bits(y0, y1);
+                        b[e] = bf16x2_bits(y0 - bf16_lo(a[e]), y1 - bf16_hi(a[e]));
+                    }
+                    uint8_t *dst = sm + L::SOP + row * 128 + (((cg * 2 + h) ^ (row & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
+                    *reinterpret_cast<uint4 *>(dst + L::HALF) = make_uint4(b[0], b[1], b[2], b[3]);
+                }
+                fence_proxy_async_smem();
+                arrive(b_s);
+            }
             ok = __all_sync(0xffffffffu,
-                            lt_wait(&b_w[sg], ph2, abort) && lt_wait(&b_yz[sg], ph2, abort));
+                            lt_wait(b_w + 8 * sg, ph2, abort) && lt_wait(b_yz + 8 * sg, ph2, abort));
             if (!ok) break;
-            // (u z) in three bf16 parts, at the places of z
+            // (u z) in three bf16 parts, at the places of z (and of the last chunk's staged rows)
+            if (OUT && it >= 1) ok = __all_sync(0xffffffffu, lt_wait(b_ofree, (it - 1) & 1, abort));
+            if (!ok) break;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const uint32_t item = tid + j * kLtMath, off = item * 16;   // row item / 8
@@ -396,32 +528,16 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             fence_proxy_async_smem();
             arrive(b_parts);
             if (OUT) {
-                // the state before the chunk as the B operand, rows of y, two bf16 parts
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t a[4], b[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float y0 = st[h * 8 + 2 * e], y1 = st[h * 8 + 2 * e + 1];
-                        a[e] = bf16x2_bits(y0, y1);
-                        b[e] = bf16x2_bits(y0 - bf16_lo(a[e]), y1 - bf16_hi(a[e]));
-                    }
-                    uint8_t *dst = sm + L::SOP + row * 128 + (((cg * 2 + h) ^ (row & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
-                    *reinterpret_cast<uint4 *>(dst + L::HALF) = make_uint4(b[0], b[1], b[2], b[3]);
-                }
-                fence_proxy_async_smem();
-                arrive(b_s);
                 if (p.states) {
-                    float *dst = p.states + ((size_t)bh * p.N + n) * D * D;
+                    float *dst = p.states + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) dst[at(0, j)] = st[j];
+                    for (int j = 0; j < 16; ++j) dst[j * D] = st[j];
                 }
                 if (p.states_in) {
-                    const float *src = p.states_in + ((size_t)bh * p.N + n) * D * D;
+                    const float *src = p.states_in + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
                     float f = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) f = fmaf(st[j], src[at(0, j)], f);
+                    for (int j = 0; j < 16; ++j) f = fmaf(st[j], __ldcs(src + j * D), f);
                     f = warp_sum(f);
                     if (lane == 0)
                         p.fdot[((size_t)(zh * 16 + warp) * p.BH + bh) * p.N + n] = tab[8 * C] * f;
@@ -432,33 +548,54 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 ok = __all_sync(0xffffffffu, lt_wait(b_p, ph, abort));
                 if (!ok) break;
                 tc::fence_after_sync();
-                if (zero) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) pk[j] = 0.f;
-                } else {
-                    float v[32];
-                    tc::tmem_ld16(tl + kP + cg * 32, v);
-                    tc::tmem_ld16(tl + kP + cg * 32 + 16, v + 16);
-                    tc::tmem_wait_ld();
-                    if (cg == quarter) {
-                        const float lt = tab[3 * C + row];
+                for (int j = 0; j < 16; ++j) pk[j] = 0.f;
+                if (!zero) {
+                    // 16 columns at a time, so that the state's registers need not be spilled
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float d = lt - tab[3 * C + cg * 32 + j];
-                            const float w = REV ? p.scale : tab[2 * C + cg * 32 + j];
-                            const bool in = REV ? j >= lane : j <= lane;
-                            v[j] = in ? v[j] * (w * exp2f(REV ? -d : d)) : 0.f;
+                    for (int h = 0; h < 32; h += 16) {
+                        const int c0 = cg * 32 + h;
+                        float v[16];
+                        tc::tmem_ld16(tl + kP + c0, v);
+                        tc::tmem_wait_ld();
+                        if (cg == quarter) {
+                            const float lt = tab[3 * C + row];
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 l4 = *reinterpret_cast<const float4 *>(tab + 3 * C + c0 + j);
+                                const float4 g4 = *reinterpret_cast<const float4 *>(tab + 2 * C + c0 + j);
+                                const float li[4] = {l4.x, l4.y, l4.z, l4.w};
+                                const float gi[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float d = lt - li[e], w = REV ? p.scale : gi[e];
+                                    const bool in = REV ? h + j + e >= lane : h + j + e <= lane;
+                                    v[j + e] = in ? v[j + e] * (w * exp2f(REV ? -d : d)) : 0.f;
+                                }
+                            }
+                        } else {
+                            const float ta = tab[4 * C + row];
+                            const float *c = tab + (5 + (REV ? quarter : quarter - 1)) * C + c0;
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 c4 = *reinterpret_cast<const float4 *>(c + j);
+                                v[j] *= ta * c4.x;
+                                v[j + 1] *= ta * c4.y;
+                                v[j + 2] *= ta * c4.z;
+                                v[j + 3] *= ta * c4.w;
+                            }
                         }
-                    } else {
-                        const float ta = tab[4 * C + row];
-                        const float *c = tab + (5 + (REV ? quarter : quarter - 1)) * C + cg * 32;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] *= ta * c[j];
+                        for (int j = 0; j < 8; ++j)
+                            pk[h / 2 + j] = __uint_as_float(bf16x2_bits(v[2 * j], v[2 * j + 1]));
                     }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        pk[j] = __uint_as_float(bf16x2_bits(v[2 * j], v[2 * j + 1]));
                 }
+                // the four warps of these lanes have their scores: the columns are free
+                tc::fence_before_sync();
+                arrive(b_quart + 8 * quarter);
+                ok = __all_sync(0xffffffffu, lt_wait(b_quart + 8 * quarter, ph, abort));
+                if (!ok) break;
+                tc::fence_after_sync();
                 tc::tmem_st16(tl + kPB + cg * 16, pk);
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
@@ -469,22 +606,28 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             if (!ok) break;
             tc::fence_after_sync();
             {
-                float v[16];
-                tc::tmem_ld16(tl + kDS + cg * 16, v);
+                float v[16], w[16];
+                tc::tmem_ld16(tl + kDS + 64 + cg * 16, v);
+                tc::tmem_ld16(tl + kDS + 128 + cg * 16, w);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] += w[j];
+                tc::tmem_ld16(tl + kDS + cg * 16, w);
                 tc::tmem_wait_ld();
                 const float b = tab[8 * C];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) st[j] = fmaf(b, st[j], v[j]);
+                for (int j = 0; j < 16; ++j) st[j] = fmaf(b, st[j], w[j] + v[j]);
             }
             if (OUT) {
                 const int t = n * C + row;
                 const size_t grow = (size_t)bh * p.T + t;
                 const bool in = t < p.T;
-                float xd[16];
+                uint4 xd[2] = {};
                 if (p.dot && in) {
-                    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.xd) + grow * D + z0;
-                    Vec16<__nv_bfloat16>::load(src, xd);
-                    Vec16<__nv_bfloat16>::load(src + 8, xd + 8);
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        static_cast<const __nv_bfloat16 *>(p.xd) + grow * D + z0);
+                    xd[0] = __ldg(src);
+                    xd[1] = __ldg(src + 1);
                 }
                 const float a = tab[row], g = tab[2 * C + row];
                 ok = __all_sync(0xffffffffu, lt_wait(b_o, ph, abort));
@@ -492,24 +635,37 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 tc::fence_after_sync();
                 float vs[16], vi[16];
                 tc::tmem_ld16(tl + kOS + cg * 16, vs);
-                tc::tmem_ld16(tl + kOI + cg * 16, vi);
+                tc::tmem_ld16(tl + kOS + 64 + cg * 16, vi);
                 tc::tmem_wait_ld();
-                float d = 0.f;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    vs[j] *= a;
-                    if (p.dot && in) d = fmaf(vs[j], xd[j], d);
+                for (int j = 0; j < 16; ++j) vs[j] = a * (vs[j] + vi[j]);
+                tc::tmem_ld16(tl + kOI + cg * 16, vi);
+                float d = 0.f;
+                if (p.dot) {
+                    const uint32_t w[8] = {xd[0].x, xd[0].y, xd[0].z, xd[0].w,
+                                           xd[1].x, xd[1].y, xd[1].z, xd[1].w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        d = fmaf(vs[2 * j], bf16_lo(w[j]), fmaf(vs[2 * j + 1], bf16_hi(w[j]), d));
+                }
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
                     vi[j] = REV ? g * (vs[j] + vi[j]) : fmaf(p.scale, vi[j], vs[j]);
-                }
-                if (in) {
-                    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + grow * D + z0;
-                    Vec16<__nv_bfloat16>::store(o, vi);
-                    Vec16<__nv_bfloat16>::store(o + 8, vi + 8);
-                    if (p.dot) p.dot[(size_t)(zh * 4 + cg) * p.BH * p.T + grow] = d;
-                }
+                if (p.dot && in) p.dot[(size_t)(zh * 4 + cg) * p.BH * p.T + grow] = d;
+                // staged where the increments' parts were (their product has completed)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    Vec16<__nv_bfloat16>::store(
+                        reinterpret_cast<__nv_bfloat16 *>(sm + L::PARTS + row * 128 +
+                                                          (((cg * 2 + h) ^ (row & 7)) << 4)),
+                        vi + 8 * h);
+                fence_proxy_async_smem();
+                tc::fence_before_sync();
+                arrive(b_out);
             }
             tc::fence_before_sync();
-            arrive(&b_tfree[sg]);
+            arrive(b_tfree + 8 * sg);
         }
         float *dst = OUT ? (seg == (REV ? 0 : p.S - 1) ? p.last : nullptr) : p.agg;
         if (ok && dst) {
@@ -583,9 +739,9 @@ k_linear_pairs_tc(const __grid_constant__ LinPairsTc args, int *__restrict__ tim
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smem_align1024(smraw);
     const uint32_t sb = smem_u32(sm);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);   // load[2], mma[2], fin
+    const uint32_t bars = sb + L::BARS;   // load[2], mma[2], fin
     uint32_t *tbase = reinterpret_cast<uint32_t *>(sm + L::TBASE);
-    volatile int *abort = reinterpret_cast<volatile int *>(sm + L::TBASE + 4);
+    const uint32_t abort = sb + L::TBASE + 4;
     float *s_lh = reinterpret_cast<float *>(sm + L::LH), *s_ll = s_lh + C;
     float *s_g = reinterpret_cast<float *>(sm + L::G), *s_rs = reinterpret_cast<float *>(sm + L::RS);
     float *s_cg = reinterpret_cast<float *>(sm + L::CG), *s_cx = reinterpret_cast<float *>(sm + L::CX);
@@ -597,8 +753,8 @@ k_linear_pairs_tc(const __grid_constant__ LinPairsTc args, int *__restrict__ tim
     const size_t head = (size_t)bh * p.T, all = (size_t)p.BH * p.T;
 
     if (tid == 0) {
-        for (int i = 0; i < 5; ++i) mbar_init(&bars[i], 1);
-        *abort = 0;
+        for (int i = 0; i < 5; ++i) lt_init(bars + 8 * i, 1);
+        asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(0u) : "memory");
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -611,8 +767,8 @@ k_linear_pairs_tc(const __grid_constant__ LinPairsTc args, int *__restrict__ tim
     const uint32_t tmem = *tbase;
     bool ok = true;
     if (tid == kLpThreads - 32) {   // warps 0-3 prepare the tokens meanwhile
-        auto load = [&](const CUtensorMap *a, const CUtensorMap *b, uint64_t *bar) {
-            mbar_arrive_expect_tx(bar, 2 * LtSmem::TILE);
+        auto load = [&](const CUtensorMap *a, const CUtensorMap *b, uint32_t bar) {
+            lt_expect(bar, 2 * LtSmem::TILE);
             for (int h = 0; h < 2; ++h) {
                 tma_load_3d(sm + L::A + h * LtSmem::HALF, a, h * 64, t0, bh, bar);
                 tma_load_3d(sm + L::B + h * LtSmem::HALF, b, h * 64, t0, bh, bar);
@@ -621,30 +777,30 @@ k_linear_pairs_tc(const __grid_constant__ LinPairsTc args, int *__restrict__ tim
         auto kmaj = [&](uint32_t base, int kk) {
             return tc::sdesc(sb + base + (kk >> 2) * LtSmem::HALF + (kk & 3) * 32, 16, 1024);
         };
-        auto mma = [&](uint32_t col, uint64_t *bar) {
+        auto mma = [&](uint32_t col, uint32_t bar) {
             constexpr uint32_t ID = tc::idesc_bf16(128, 128, false, false);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
                 tc::mma_f16(tmem + col, kmaj(L::A, kk), kmaj(L::B, kk), ID, kk > 0);
-            tc::commit(bar);
+            lt_commit(bar);
         };
-        load(&args.q, &args.k, &bars[0]);
-        ok = lt_wait(&bars[0], 0, abort);
+        load(&args.q, &args.k, bars + 8 * 0);
+        ok = lt_wait(bars + 8 * 0, 0, abort);
         if (ok) {
-            mma(0, &bars[2]);
-            ok = lt_wait(&bars[2], 0, abort);
+            mma(0, bars + 8 * 2);
+            ok = lt_wait(bars + 8 * 2, 0, abort);
         }
         if (ok) {
-            load(&args.d_o, &args.v, &bars[1]);
-            ok = lt_wait(&bars[1], 0, abort);
-            if (ok) mma(128, &bars[3]);
+            load(&args.d_o, &args.v, bars + 8 * 1);
+            ok = lt_wait(bars + 8 * 1, 0, abort);
+            if (ok) mma(128, bars + 8 * 3);
         }
         if (!ok) {
             atomicExch(timeout_flag, 1);
-            tc::commit(&bars[4]);
-            mbar_wait_bounded(&bars[4], 0, kLtProbes);
-            mbar_wait_bounded(&bars[1], 0, kLtProbes);
-            mbar_wait_bounded(&bars[0], 0, kLtProbes);
+            lt_commit(bars + 8 * 4);
+            lt_drain(bars + 8 * 4, 0);
+            lt_drain(bars + 8 * 1, 0);
+            lt_drain(bars + 8 * 0, 0);
         }
     }
     __syncwarp();
@@ -694,7 +850,7 @@ k_linear_pairs_tc(const __grid_constant__ LinPairsTc args, int *__restrict__ tim
         s_ll[tid] = (float)(l - (double)(float)l);
     }
     __syncthreads();
-    ok = lt_wait(&bars[3], 0, abort);
+    ok = lt_wait(bars + 8 * 3, 0, abort);
     ok = __syncthreads_and(ok);
     tc::fence_after_sync();
     const int quarter = warp & 3, half = warp >> 2, s = quarter * 32 + lane;
