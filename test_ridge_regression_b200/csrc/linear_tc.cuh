@@ -67,8 +67,9 @@ struct LtSmem {
     static constexpr uint32_t PARTS = Z + 2 * HALF;       // hi, mid, lo of u z
     static constexpr uint32_t SOP = PARTS + 3 * HALF;     // hi, lo of the state
     static constexpr uint32_t TAB = SOP + 2 * HALF;       // 2 x decay tables
-    // table floats: a, u, g, lrel, ta, c[3] of 128 tokens each, then b
-    static constexpr uint32_t TABF = 8 * kLtC + 4;
+    // table floats, 128 tokens each: a, u, g, l (of the row), m (l less log2 of the gate, of
+    // the column; forward), ta, c[3]; then b
+    static constexpr uint32_t TABF = 9 * kLtC + 4;
     static constexpr uint32_t BARS = TAB + 2 * 4 * TABF;
     static constexpr uint32_t TBASE = BARS + 8 * 22;      // TMEM base, abort flag
     static constexpr uint32_t END = TBASE + 16;
@@ -179,9 +180,21 @@ __device__ __forceinline__ Log2Sum operator+(Log2Sum a, Log2Sum b) {
     const float h = s + e;
     return {h, e - (h - s)};
 }
+// 2^x, results below 2^-126 as zero (relative error 2^-22: the hardware's function)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // 2^(a - b)
 __device__ __forceinline__ float exp2_diff(Log2Sum a, Log2Sum b) {
-    return exp2f((a.hi - b.hi) + (a.lo - b.lo));
+    return ex2((a.hi - b.hi) + (a.lo - b.lo));
+}
+// Two bf16 as a pair of floats, a pair as two bf16, and what the rounding left.
+__device__ __forceinline__ float2 bf16x2_f2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ uint32_t f2_bf16x2(float2 y) { return bf16x2_bits(y.x, y.y); }
+__device__ __forceinline__ float2 f2_rest(float2 y, uint32_t w) {
+    return __ffma2_rn(bf16x2_f2(w), make_float2(-1.f, -1.f), y);
 }
 __device__ __forceinline__ Log2Sum shfl(Log2Sum x, int src) {
     return {__shfl_sync(0xffffffffu, x.hi, src), __shfl_sync(0xffffffffu, x.lo, src)};
@@ -194,7 +207,7 @@ __device__ __forceinline__ float lt_tables(float *tab, const float *bv, const fl
                                            float log2_min) {
     const int lane = threadIdx.x & 31, blk = lane >> 3;
     float *ta_a = tab, *ta_u = tab + kLtC, *ta_g = tab + 2 * kLtC, *ta_l = tab + 3 * kLtC,
-          *ta_t = tab + 4 * kLtC, *ta_c = tab + 5 * kLtC;
+          *ta_m = tab + 4 * kLtC, *ta_t = tab + 5 * kLtC, *ta_c = tab + 6 * kLtC;
     const Log2Sum zero = {0.f, 0.f};
     Log2Sum l[4], run = zero;
 #pragma unroll
@@ -215,14 +228,15 @@ __device__ __forceinline__ float lt_tables(float *tab, const float *bv, const fl
     for (int b = 0; b < 4; ++b) edge[b] = shfl(incl, 8 * b + 7);
     const Log2Sum start = blk == 0 ? zero : blk == 1 ? edge[0] : blk == 2 ? edge[1] : edge[2];
     const Log2Sum stop = blk == 0 ? edge[0] : blk == 1 ? edge[1] : blk == 2 ? edge[2] : edge[3];
-    float va[4], vu[4], vl[4], vt[4], vc[3][4];
+    float va[4], vu[4], vl[4], vm[4], vt[4], vc[3][4];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const Log2Sum lt = excl + l[p];
         va[p] = REV ? exp2_diff(edge[3], lt) : scale * exp2_diff(lt, zero);
         vu[p] = REV ? scale * exp2_diff(lt, zero) : gv[p] * exp2_diff(edge[3], lt);
         vl[p] = (lt.hi - start.hi) + (lt.lo - start.lo);
-        vt[p] = REV ? scale * exp2_diff(stop, lt) : exp2f(vl[p]);
+        vm[p] = vl[p] - log2f(gv[p]);   // closed gate: +inf, whose weight is 0
+        vt[p] = REV ? exp2_diff(stop, lt) : ex2(vl[p]);
         // forward: c[b] serves block row b + 1, the blocks before it; backward: block row
         // b, the blocks after it (other entries are not read)
 #pragma unroll
@@ -236,12 +250,13 @@ __device__ __forceinline__ float lt_tables(float *tab, const float *bv, const fl
     put(ta_u, vu);
     put(ta_g, gv);
     put(ta_l, vl);
+    if (!REV) put(ta_m, vm);
     put(ta_t, vt);
 #pragma unroll
     for (int b = 0; b < 3; ++b)
         if (REV ? blk > b : blk <= b) put(ta_c + b * kLtC, vc[b]);
     const float lC = edge[3].hi + edge[3].lo;
-    if (lane == 0) tab[8 * kLtC] = exp2f(lC);
+    if (lane == 0) tab[9 * kLtC] = ex2(lC);
     return lC;
 }
 
@@ -487,9 +502,9 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                     uint32_t a[4], b[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float y0 = st[h * 8 + 2 * e], y1 = st[h * 8 + 2 * e + 1];
-                        a[e] = bf16x2_bits(y0, y1);
-                        b[e] = bf16x2_bits(y0 - bf16_lo(a[e]), y1 - bf16_hi(a[e]));
+                        const float2 y = make_float2(st[h * 8 + 2 * e], st[h * 8 + 2 * e + 1]);
+                        a[e] = f2_bf16x2(y);
+                        b[e] = f2_bf16x2(f2_rest(y, a[e]));
                     }
                     uint8_t *dst = sm + L::SOP + row * 128 + (((cg * 2 + h) ^ (row & 7)) << 4);
                     *reinterpret_cast<uint4 *>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
@@ -513,12 +528,11 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 uint32_t a[4], b[4], c[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float y0 = u * bf16_lo(w[e]), y1 = u * bf16_hi(w[e]);
-                    a[e] = bf16x2_bits(y0, y1);
-                    y0 -= bf16_lo(a[e]);
-                    y1 -= bf16_hi(a[e]);
-                    b[e] = bf16x2_bits(y0, y1);
-                    c[e] = bf16x2_bits(y0 - bf16_lo(b[e]), y1 - bf16_hi(b[e]));
+                    float2 y = __fmul2_rn(bf16x2_f2(w[e]), make_float2(u, u));
+                    a[e] = f2_bf16x2(y);
+                    y = f2_rest(y, a[e]);
+                    b[e] = f2_bf16x2(y);
+                    c[e] = f2_bf16x2(f2_rest(y, b[e]));
                 }
                 uint8_t *dst = sm + L::PARTS + off;
                 *reinterpret_cast<uint4 *>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
@@ -540,7 +554,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                     for (int j = 0; j < 16; ++j) f = fmaf(st[j], __ldcs(src + j * D), f);
                     f = warp_sum(f);
                     if (lane == 0)
-                        p.fdot[((size_t)(zh * 16 + warp) * p.BH + bh) * p.N + n] = tab[8 * C] * f;
+                        p.fdot[((size_t)(zh * 16 + warp) * p.BH + bh) * p.N + n] = tab[9 * C] * f;
                 }
                 // weighted scores: columns 32 cg .. of token `row`
                 const bool zero = REV ? cg < quarter : cg > quarter;
@@ -558,36 +572,36 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                         float v[16];
                         tc::tmem_ld16(tl + kP + c0, v);
                         tc::tmem_wait_ld();
+                        const float4 *w4;   // weights' exponents, or their column factors
+                        float2 rf;
                         if (cg == quarter) {
-                            const float lt = tab[3 * C + row];
-#pragma unroll
-                            for (int j = 0; j < 16; j += 4) {
-                                const float4 l4 = *reinterpret_cast<const float4 *>(tab + 3 * C + c0 + j);
-                                const float4 g4 = *reinterpret_cast<const float4 *>(tab + 2 * C + c0 + j);
-                                const float li[4] = {l4.x, l4.y, l4.z, l4.w};
-                                const float gi[4] = {g4.x, g4.y, g4.z, g4.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const float d = lt - li[e], w = REV ? p.scale : gi[e];
-                                    const bool in = REV ? h + j + e >= lane : h + j + e <= lane;
-                                    v[j + e] = in ? v[j + e] * (w * exp2f(REV ? -d : d)) : 0.f;
-                                }
-                            }
+                            w4 = reinterpret_cast<const float4 *>(tab + (REV ? 3 : 4) * C + c0);
+                            rf.x = rf.y = tab[3 * C + row];
                         } else {
-                            const float ta = tab[4 * C + row];
-                            const float *c = tab + (5 + (REV ? quarter : quarter - 1)) * C + c0;
-#pragma unroll
-                            for (int j = 0; j < 16; j += 4) {
-                                const float4 c4 = *reinterpret_cast<const float4 *>(c + j);
-                                v[j] *= ta * c4.x;
-                                v[j + 1] *= ta * c4.y;
-                                v[j + 2] *= ta * c4.z;
-                                v[j + 3] *= ta * c4.w;
-                            }
+                            w4 = reinterpret_cast<const float4 *>(
+                                tab + (6 + (REV ? quarter : quarter - 1)) * C + c0);
+                            rf.x = rf.y = tab[5 * C + row];
                         }
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            pk[h / 2 + j] = __uint_as_float(bf16x2_bits(v[2 * j], v[2 * j + 1]));
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 c4 = w4[j / 4];
+#pragma unroll
+                            for (int e = 0; e < 4; e += 2) {
+                                float2 w = e ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
+                                if (cg == quarter) {
+                                    // 2^(l_t - l_i) up to and including the token itself
+                                    w = REV ? __ffma2_rn(rf, make_float2(-1.f, -1.f), w)
+                                            : __ffma2_rn(w, make_float2(-1.f, -1.f), rf);
+                                    const int i = h + j + e;
+                                    w.x = (REV ? i >= lane : i <= lane) ? ex2(w.x) : 0.f;
+                                    w.y = (REV ? i + 1 >= lane : i + 1 <= lane) ? ex2(w.y) : 0.f;
+                                } else {
+                                    w = __fmul2_rn(w, rf);
+                                }
+                                w = __fmul2_rn(w, make_float2(v[j + e], v[j + e + 1]));
+                                pk[(h + j + e) / 2] = __uint_as_float(f2_bf16x2(w));
+                            }
+                        }
                     }
                 }
                 // the four warps of these lanes have their scores: the columns are free
@@ -614,7 +628,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 for (int j = 0; j < 16; ++j) v[j] += w[j];
                 tc::tmem_ld16(tl + kDS + cg * 16, w);
                 tc::tmem_wait_ld();
-                const float b = tab[8 * C];
+                const float b = tab[9 * C];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) st[j] = fmaf(b, st[j], w[j] + v[j]);
             }
@@ -651,7 +665,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 tc::tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    vi[j] = REV ? g * (vs[j] + vi[j]) : fmaf(p.scale, vi[j], vs[j]);
+                    vi[j] = fmaf(p.scale, vi[j], vs[j]) * (REV ? g : 1.f);
                 if (p.dot && in) p.dot[(size_t)(zh * 4 + cg) * p.BH * p.T + grow] = d;
                 // staged where the increments' parts were (their product has completed)
 #pragma unroll
