@@ -53,10 +53,11 @@ namespace gka {
 
 constexpr int kLtC = 128;                       // tokens per chunk
 constexpr int kLtZN = 64;                       // columns of z a CTA owns
-constexpr int kLtMath = 512;                    // arithmetic threads
-constexpr int kLtThreads = kLtMath + 64;        // + issuer, decay warp
-constexpr int kLtDots = 8, kLtFdots = 32;       // planes of dot and fdot partials per pass
+constexpr int kLtGroup = 256;                   // threads of an arithmetic group (two)
+constexpr int kLtThreads = 2 * kLtGroup + 128;  // + issuer, two decay warps, store warp
+constexpr int kLtDots = 4, kLtFdots = 16;       // planes of dot and fdot partials per pass
 constexpr uint32_t kLtProbes = 1u << 20;
+constexpr uint32_t kLtHintNs = 2000;            // a probe suspends its warp for up to this long
 
 struct LtSmem {
     static constexpr uint32_t TILE = kLtC * 256;          // [128][128] bf16, two column halves
@@ -104,6 +105,20 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int c0, int
         : "memory");
 }
 
+// 128 rows x 32 bytes of a K-major operand (one K step) from shared memory to 8 TMEM columns.
+__device__ __forceinline__ void cp_128x256b(uint32_t dst_tmem, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(dst_tmem), "l"(sdesc) : "memory");
+}
+// One lane of the warp, always the same.  Issuing under it from a warp that runs the loop as
+// a whole costs 33 cycles an MMA; under `lane == 0`, 70 to 200 (operands go through
+// per-thread registers and a loop that makes them uniform).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]: A is bf16, two K elements to a 32-bit column.
 __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                             uint32_t idesc, bool accumulate) {
@@ -123,10 +138,10 @@ __device__ __forceinline__ bool lt_wait(uint32_t bar, uint32_t parity, uint32_t 
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
-            : "r"(bar), "r"(parity)
+            : "r"(bar), "r"(parity), "r"(kLtHintNs)
             : "memory");
         if (ok) return true;
         if ((i & 255) == 255) {
@@ -200,64 +215,52 @@ __device__ __forceinline__ Log2Sum shfl(Log2Sum x, int src) {
     return {__shfl_sync(0xffffffffu, x.hi, src), __shfl_sync(0xffffffffu, x.lo, src)};
 }
 
-// Decay tables of one chunk by one warp; lane l holds tokens 4l..4l+3, whose beta and
-// gate are bv and gv (1 and 0 past the sequence's end).  Returns the chunk's log2 decay.
+// Decay tables of one chunk by one warp; lane l holds tokens 32 j + l, whose beta and
+// gate are bv[j] and gv[j] (1 and 0 past the sequence's end). 
 template <bool REV>
-__device__ __forceinline__ float lt_tables(float *tab, const float *bv, const float *gv, float scale,
-                                           float log2_min) {
-    const int lane = threadIdx.x & 31, blk = lane >> 3;
-    float *ta_a = tab, *ta_u = tab + kLtC, *ta_g = tab + 2 * kLtC, *ta_l = tab + 3 * kLtC,
-          *ta_m = tab + 4 * kLtC, *ta_t = tab + 5 * kLtC, *ta_c = tab + 6 * kLtC;
+__device__ __forceinline__ void lt_tables(float *tab, const float *bv, const float *gv, float scale,
+                                          float log2_min) {
+    const int lane = threadIdx.x & 31;
+    float *ta_a = tab + lane, *ta_u = ta_a + kLtC, *ta_g = ta_u + kLtC, *ta_l = ta_g + kLtC,
+          *ta_m = ta_l + kLtC, *ta_t = ta_m + kLtC, *ta_c = ta_t + kLtC;
     const Log2Sum zero = {0.f, 0.f};
-    Log2Sum l[4], run = zero;
+    Log2Sum l[4], edge[4], base = zero;   // edge[b]: cumulative log at the end of block b
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        run = run + Log2Sum{fmaxf(log2f(bv[p]), log2_min), 0.f};
-        l[p] = run;
-    }
-    Log2Sum incl = run;
-#pragma unroll
+    for (int j = 0; j < 4; ++j) l[j] = {fmaxf(log2f(bv[j]), log2_min), 0.f};
+    // the four blocks' scans, step by step together
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-        const Log2Sum y = {__shfl_up_sync(0xffffffffu, incl.hi, o), __shfl_up_sync(0xffffffffu, incl.lo, o)};
-        if (lane >= o) incl = incl + y;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const Log2Sum y = {__shfl_up_sync(0xffffffffu, l[j].hi, o), __shfl_up_sync(0xffffffffu, l[j].lo, o)};
+            if (lane >= o) l[j] = l[j] + y;
+        }
     }
-    Log2Sum excl = {__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
-    if (lane == 0) excl = zero;
-    Log2Sum edge[4];   // cumulative log at the end of block 0..3
 #pragma unroll
-    for (int b = 0; b < 4; ++b) edge[b] = shfl(incl, 8 * b + 7);
-    const Log2Sum start = blk == 0 ? zero : blk == 1 ? edge[0] : blk == 2 ? edge[1] : edge[2];
-    const Log2Sum stop = blk == 0 ? edge[0] : blk == 1 ? edge[1] : blk == 2 ? edge[2] : edge[3];
-    float va[4], vu[4], vl[4], vm[4], vt[4], vc[3][4];
+    for (int j = 0; j < 4; ++j) {
+        const Log2Sum start = base;
+        base = base + shfl(l[j], 31);
+        edge[j] = base;
+        ta_l[32 * j] = l[j].hi + l[j].lo;
+        l[j] = start + l[j];
+    }
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const Log2Sum lt = excl + l[p];
-        va[p] = REV ? exp2_diff(edge[3], lt) : scale * exp2_diff(lt, zero);
-        vu[p] = REV ? scale * exp2_diff(lt, zero) : gv[p] * exp2_diff(edge[3], lt);
-        vl[p] = (lt.hi - start.hi) + (lt.lo - start.lo);
-        vm[p] = vl[p] - log2f(gv[p]);   // closed gate: +inf, whose weight is 0
-        vt[p] = REV ? exp2_diff(stop, lt) : ex2(vl[p]);
+    for (int j = 0; j < 4; ++j) {
+        const int t = 32 * j;
+        const float to = exp2_diff(l[j], zero), from = exp2_diff(edge[3], l[j]);
+        ta_a[t] = REV ? from : scale * to;
+        ta_u[t] = REV ? scale * to : gv[j] * from;
+        ta_g[t] = gv[j];
+        if (!REV) ta_m[t] = ta_l[t] - log2f(gv[j]);   // closed gate: +inf, whose weight is 0
+        ta_t[t] = REV ? exp2_diff(edge[j], l[j]) : ex2(ta_l[t]);
         // forward: c[b] serves block row b + 1, the blocks before it; backward: block row
         // b, the blocks after it (other entries are not read)
 #pragma unroll
         for (int b = 0; b < 3; ++b)
-            vc[b][p] = REV ? exp2_diff(lt, edge[b]) : gv[p] * exp2_diff(edge[b], lt);
+            if (REV ? j > b : j <= b)
+                ta_c[b * kLtC + t] = REV ? exp2_diff(l[j], edge[b]) : gv[j] * exp2_diff(edge[b], l[j]);
     }
-    auto put = [&](float *dst, const float *v) {
-        *reinterpret_cast<float4 *>(dst + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
-    };
-    put(ta_a, va);
-    put(ta_u, vu);
-    put(ta_g, gv);
-    put(ta_l, vl);
-    if (!REV) put(ta_m, vm);
-    put(ta_t, vt);
-#pragma unroll
-    for (int b = 0; b < 3; ++b)
-        if (REV ? blk > b : blk <= b) put(ta_c + b * kLtC, vc[b]);
-    const float lC = edge[3].hi + edge[3].lo;
-    if (lane == 0) tab[9 * kLtC] = ex2(lC);
-    return lC;
+    if (lane == 0) tab[9 * kLtC] = ex2(edge[3].hi + edge[3].lo);
 }
 
 // grid (2 * passes, B*H, S), block kLtThreads.  OUT = false: segment aggregates.
@@ -271,11 +274,13 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     const uint32_t sb = smem_u32(sm);
     const uint32_t bars = sb + L::BARS;
     const uint32_t b_x = bars, b_p = bars + 8, b_parts = bars + 16, b_s = bars + 24, b_pb = bars + 32,
-                   b_ds = bars + 40, b_o = bars + 48, b_xfree = bars + 56, b_out = bars + 64,
-                   b_ofree = bars + 72, b_fin = bars + 80;
-    const uint32_t b_yz = bars + 88, b_w = bars + 104, b_tfree = bars + 120, b_quart = bars + 136;
-    const uint32_t abort = sb + L::TBASE + 4;
+                   b_ds = bars + 40, b_o = bars + 48, b_xfree = bars + 56, b_oread = bars + 64,
+                   b_fin = bars + 72;
+    const uint32_t b_y = bars + 80, b_z = bars + 96, b_w = bars + 112, b_tfree = bars + 128,
+                   b_out = bars + 144;                                                         // [2]
+    const uint32_t b_os = bars + 160;
     uint32_t *tbase = reinterpret_cast<uint32_t *>(sm + L::TBASE);
+    const uint32_t abort = sb + L::TBASE + 4;
     float *s_tab = reinterpret_cast<float *>(sm + L::TAB);
     const LinTcPass &A = args.pass[blockIdx.x >> 1];
     const LinPass &p = A.p;
@@ -285,49 +290,56 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     // the last segment's aggregate is never carried on
     if (!OUT && seg == (REV ? 0 : p.S - 1)) return;
     auto chunk = [&](int it) { return REV ? n1 - 1 - it : n0 + it; };
+    constexpr int kIssuer = 2 * kLtGroup;   // first thread of the issuing warp
 
-    if (tid == kLtMath) {
+    if (tid == kIssuer) {
         for (int i = 0; i < 2; ++i) {
-            lt_init(b_yz + 8 * i, 1);
+            lt_init(b_y + 8 * i, 1);
+            lt_init(b_z + 8 * i, 1);
             lt_init(b_w + 8 * i, 32);
-            lt_init(b_tfree + 8 * i, 16);
+            lt_init(b_tfree + 8 * i, OUT ? 16 : 8);
+            lt_init(b_out + 8 * i, 8);
         }
         lt_init(b_x, 1);
         lt_init(b_p, 1);
-        lt_init(b_parts, 16);
-        lt_init(b_s, 16);
-        lt_init(b_pb, 16);
+        lt_init(b_parts, 8);
+        lt_init(b_s, 8);
+        lt_init(b_pb, 8);
         lt_init(b_ds, 1);
         lt_init(b_o, 1);
         lt_init(b_xfree, 1);
-        lt_init(b_out, 16);
-        lt_init(b_ofree, 1);
-        for (int i = 0; i < 4; ++i) lt_init(b_quart + 8 * i, 4);
         lt_init(b_fin, 1);
+        lt_init(b_oread, 8);
+        lt_init(b_os, 1);
         asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(0u) : "memory");
         fence_mbar_init();
     }
     __syncthreads();
-    int loads_x = 0, loads_yz[2] = {0, 0};   // issuer: loads begun per barrier
-    auto load_yz = [&](int it) {
-        const int st = it & 1, t0 = chunk(it) * C;
-        lt_expect(b_yz + 8 * st, L::TILE + L::HALF);
-        tma_load_3d(sm + L::Y + st * L::TILE, &A.y, 0, t0, bh, b_yz + 8 * st);
-        tma_load_3d(sm + L::Y + st * L::TILE + L::HALF, &A.y, 64, t0, bh, b_yz + 8 * st);
-        tma_load_3d(sm + L::Z + st * L::HALF, &A.z, zh * kLtZN, t0, bh, b_yz + 8 * st);
-        ++loads_yz[st];
-    };
     auto load_x = [&](int it) {
         const int t0 = chunk(it) * C;
         lt_expect(b_x, L::TILE);
         tma_load_3d(sm + L::X, &A.x, 0, t0, bh, b_x);
         tma_load_3d(sm + L::X + L::HALF, &A.x, 64, t0, bh, b_x);
-        ++loads_x;
     };
-    if (tid == kLtMath) {
-        load_yz(0);
+    auto load_y = [&](int it) {
+        const int st = it & 1, t0 = chunk(it) * C;
+        lt_expect(b_y + 8 * st, L::TILE);
+        tma_load_3d(sm + L::Y + st * L::TILE, &A.y, 0, t0, bh, b_y + 8 * st);
+        tma_load_3d(sm + L::Y + st * L::TILE + L::HALF, &A.y, 64, t0, bh, b_y + 8 * st);
+    };
+    auto load_z = [&](int it) {
+        const int st = it & 1;
+        lt_expect(b_z + 8 * st, L::HALF);
+        tma_load_3d(sm + L::Z + st * L::HALF, &A.z, zh * kLtZN, chunk(it) * C, bh, b_z + 8 * st);
+    };
+    if (tid == kIssuer) {
+        load_z(0);
+        load_y(0);
         if (OUT) load_x(0);
-        if (NL > 1) load_yz(1);
+        if (NL > 1) {
+            load_z(1);
+            load_y(1);
+        }
     }
     if (warp == 0) {
         tc::tmem_alloc(tbase, 512);
@@ -337,168 +349,318 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tbase;
-    // TMEM columns; the bf16 weighted scores take the place of the scores
-    constexpr uint32_t kP = 0, kPB = 0, kOI = 128, kOS = 192, kDS = 320;
+    // TMEM columns; the bf16 weighted scores of each half of the columns lie over its scores
+    constexpr uint32_t kP = 0, kOI = 128, kOS = 192, kDS = 256, kX = 448;
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;              // TMEM lane: token of P, OI, OS; y row of S
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    auto arrive = [&](uint32_t bar) {
+        __syncwarp();
+        if (lane == 0) lt_arrive(bar);
+    };
+    auto wait = [&](uint32_t bar, uint32_t parity) {   // the whole warp, one outcome
+        return __all_sync(0xffffffffu, lt_wait(bar, parity, abort)) != 0;
+    };
 
     if (warp == 16) {
-        if (lane == 0) {
-            constexpr uint32_t ID_P = tc::idesc_bf16(128, 128, false, false);
-            constexpr uint32_t ID_O = tc::idesc_bf16(128, 64, false, true);
-            constexpr uint32_t ID_S = tc::idesc_bf16(128, 128, false, true);
-            constexpr uint32_t ID_D = tc::idesc_bf16(128, 192, true, true);
-            // first descriptors of an operand, opaque so that the eight K steps' are not kept
-            // in registers across the loop, and the step to the kk-th
-            auto first = [&](uint32_t base, uint32_t lbo) {
-                uint64_t d = tc::sdesc(sb + base, lbo, 1024);
-                asm volatile("" : "+l"(d));
-                return d;
-            };
-            auto kmaj = [](int kk) { return (uint64_t)(((kk >> 2) * L::HALF + (kk & 3) * 32) >> 4); };
-            auto mnmaj = [](int kk) { return (uint64_t)((kk * 2048) >> 4); };
-            auto issue_p = [&](int it) {
-                if (!lt_wait(b_x, it & 1, abort) || !lt_wait(b_yz + 8 * (it & 1), (it >> 1) & 1, abort))
-                    return false;
-                const uint64_t x = first(L::X, 16), y = first(L::Y + (it & 1) * L::TILE, 16);
+        // ---- issuer: the whole warp runs the loop, one lane issues ----
+        constexpr uint32_t ID_P = tc::idesc_bf16(128, 128, false, false);
+        constexpr uint32_t ID_O = tc::idesc_bf16(128, 64, false, true);
+        constexpr uint32_t ID_D = tc::idesc_bf16(128, 192, true, true);
+        auto kmaj = [&](uint32_t base, int kk) {
+            return tc::sdesc(sb + base + (kk >> 2) * L::HALF + (kk & 3) * 32, 16, 1024);
+        };
+        auto mnmaj = [&](uint32_t base, int kk) { return tc::sdesc(sb + base + kk * 2048, L::HALF, 1024); };
+        int loads_x = OUT, loads_y[2] = {1, NL > 1};   // loads begun
+        // x(it) from shared memory to TMEM, which frees its stage; the last chunk's readers
+        // of those columns are done
+        auto copy_x = [&](int it) {
+            if (!wait(b_x, it & 1)) return false;
+            tc::fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) cp_128x256b(tmem + kX + kk * 8, kmaj(L::X, kk));
+                lt_commit(b_xfree);
+            }
+            return true;
+        };
+        auto issue_p = [&](int it) {
+            const int st = it & 1;
+            if (!wait(b_y + 8 * st, (it >> 1) & 1)) return false;
+            if (elect_one()) {
+                const uint32_t y = L::Y + st * L::TILE;
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    tc::mma_f16(tmem + kP, x + kmaj(kk), y + kmaj(kk), ID_P, kk > 0);
+                    mma_bf16_ta(tmem + kP, tmem + kX + kk * 8, kmaj(y, kk), ID_P, kk > 0);
                 lt_commit(b_p);
-                return true;
-            };
-            bool ok = !OUT || issue_p(0);
-            for (int it = 0; ok && it < NL; ++it) {
-                const int st = it & 1, ph = it & 1;
-                if (OUT) {
-                    ok = lt_wait(b_s, ph, abort);
+            }
+            return true;
+        };
+        bool ok = !OUT || (copy_x(0) && issue_p(0));
+        for (int it = 0; ok && it < NL; ++it) {
+            const int st = it & 1, ph = it & 1;
+            if (OUT) {
+                if (it + 1 < NL) {
+                    ok = wait(b_xfree, ph);
                     if (!ok) break;
-                    tc::fence_after_sync();
-                    const uint64_t x = first(L::X, 16), s = first(L::SOP, L::HALF);
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        tc::mma_f16(tmem + kOS, x + kmaj(kk), s + mnmaj(kk), ID_S, kk > 0);
-                    lt_commit(b_xfree);
+                    if (elect_one()) load_x(it + 1);
+                    ++loads_x;
                 }
-                ok = lt_wait(b_parts, ph, abort);
+                // the state operand is there and the last chunk's OS has been read
+                ok = wait(b_s, ph) && (it == 0 || wait(b_oread, ph ^ 1));
                 if (!ok) break;
                 tc::fence_after_sync();
-                {
-                    const uint64_t y = first(L::Y + st * L::TILE, L::HALF), u = first(L::PARTS, L::HALF);
+                if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        tc::mma_f16(tmem + kDS, y + mnmaj(kk), u + mnmaj(kk), ID_D, kk > 0);
-                }
-                lt_commit(b_ds);
-                if (OUT) {
-                    if (it + 1 < NL) {
-                        ok = lt_wait(b_xfree, ph, abort);
-                        if (!ok) break;
-                        load_x(it + 1);
-                    }
-                    ok = lt_wait(b_pb, ph, abort);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    const uint64_t z = first(L::Z + st * L::HALF, L::HALF);
+                    for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_ta(tmem + kOI, tmem + kPB + kk * 8, z + mnmaj(kk), ID_O, kk > 0);
-                    lt_commit(b_o);
-                    if (it + 1 < NL) ok = issue_p(it + 1);
-                    if (ok && it + 2 < NL) {
-                        ok = lt_wait(b_o, ph, abort);
-                        if (ok) load_yz(it + 2);
-                    }
-                } else if (it + 2 < NL) {
-                    ok = lt_wait(b_ds, ph, abort);
-                    if (ok) load_yz(it + 2);
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_bf16_ta(tmem + kOS, tmem + kX + kk * 8, mnmaj(L::SOP + q * L::HALF, kk),
+                                        ID_O, (q | kk) != 0);
+                    lt_commit(b_os);
                 }
+            } else {
+                ok = wait(b_y + 8 * st, (it >> 1) & 1);
+                if (!ok) break;
             }
-            if (!ok) {
-                // a wait gave up: flag it, then drain this thread's products and copies
-                atomicExch(timeout_flag, 1);
-                lt_commit(b_fin);
-                lt_drain(b_fin, 0);
-                if (loads_x) lt_drain(b_x, (loads_x - 1) & 1);
-                for (int i = 0; i < 2; ++i)
-                    if (loads_yz[i]) lt_drain(b_yz + 8 * i, (loads_yz[i] - 1) & 1);
+            ok = wait(b_parts, ph);
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (elect_one()) {
+                const uint32_t y = L::Y + st * L::TILE;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    tc::mma_f16(tmem + kDS, mnmaj(y, kk), mnmaj(L::PARTS, kk), ID_D, kk > 0);
+                lt_commit(b_ds);
+            }
+            if (OUT) {
+                ok = wait(b_pb, ph);
+                if (!ok) break;
+                tc::fence_after_sync();
+                if (elect_one()) {
+                    const uint32_t z = L::Z + st * L::HALF;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_bf16_ta(tmem + kOI, tmem + kP + (kk >> 2) * 64 + (kk & 3) * 8, mnmaj(z, kk), ID_O,
+                                    kk > 0);
+                    lt_commit(b_o);
+                }
+                // x of the next chunk once this one's P and OS have read TMEM's; its scores once
+                // OI has read the weighted ones, whose columns they take
+                if (it + 1 < NL) ok = wait(b_os, ph) && copy_x(it + 1) && wait(b_o, ph) && issue_p(it + 1);
+                if (!ok) break;
+            }
+            if (it + 2 < NL) {
+                // y's readers, P(it) and DS(it), are done
+                ok = wait(OUT ? b_o : b_ds, ph);
+                if (!ok) break;
+                if (elect_one()) {
+                    load_y(it + 2);
+                    if (!OUT) load_z(it + 2);
+                }
+                ++loads_y[st];
             }
         }
+        if (!ok && elect_one()) {
+            // a wait gave up: flag it, then drain this thread's products and copies
+            atomicExch(timeout_flag, 1);
+            lt_commit(b_fin);
+            lt_drain(b_fin, 0);
+            if (loads_x) lt_drain(b_x, (loads_x - 1) & 1);
+            for (int i = 0; i < 2; ++i)
+                if (loads_y[i]) {
+                    lt_drain(b_y + 8 * i, (loads_y[i] - 1) & 1);
+                    if (!OUT) lt_drain(b_z + 8 * i, (loads_y[i] - 1) & 1);
+                }
+        }
         __syncwarp();
-    } else if (warp == 17) {
+    } else if (warp == 17 || warp == 18) {
+        // ---- decay tables: even chunks by one warp, odd ones by the other ----
         const float *beta = p.beta + (size_t)bh * p.T;
         const float *gate = p.gate ? p.gate + (size_t)bh * p.T : nullptr;
         const float log2_min = (float)(p.log_min * 1.4426950408889634);
         float bv[4], gv[4];
         auto fetch = [&](int it) {
-            const int t0 = chunk(it) * C + 4 * lane;
+            const int t0 = chunk(it) * C + lane;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bool in = t0 + j < p.T;
-                bv[j] = in ? beta[t0 + j] : 1.f;
-                gv[j] = in ? (gate ? gate[t0 + j] : 1.f) : 0.f;
+                const bool in = t0 + 32 * j < p.T;
+                bv[j] = in ? beta[t0 + 32 * j] : 1.f;
+                gv[j] = in ? (gate ? gate[t0 + 32 * j] : 1.f) : 0.f;
             }
         };
-        fetch(0);
-        float seglog = 0.f;
-        bool ok = true;
-        // chunk it's output rows, staged by the arithmetic warps, on their way
-        auto store_out = [&](int it) {
-            bool done = lt_wait(b_out, it & 1, abort);
-            if (lane == 0 && done) {
-                tma_store_3d(&A.out, zh * kLtZN, chunk(it) * C, bh, sm + L::PARTS);
-                tc::bulk_commit();
-                tc::bulk_wait_read0();
-                lt_arrive(b_ofree);
-            }
-            return __all_sync(0xffffffffu, done);
-        };
-        for (int it = 0; it < NL; ++it) {
-            if (it >= 2) ok = __all_sync(0xffffffffu, lt_wait(b_tfree + 8 * (it & 1), ((it - 2) >> 1) & 1, abort));
-            if (!ok) break;
+        const int par = warp - 17;
+        if (par < NL) fetch(par);
+        for (int it = par; it < NL; it += 2) {
+            if (it >= 2 && !wait(b_tfree + 8 * par, ((it - 2) >> 1) & 1)) break;
             float cb[4], cg[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 cb[j] = bv[j];
                 cg[j] = gv[j];
             }
-            if (it + 1 < NL) fetch(it + 1);
-            seglog += lt_tables<REV>(s_tab + (it & 1) * L::TABF, cb, cg, p.scale, log2_min);
-            lt_arrive(b_w + 8 * (it & 1));
-            if (OUT && it >= 1) ok = store_out(it - 1);
-            if (!ok) break;
+            if (it + 2 < NL) fetch(it + 2);
+            lt_tables<REV>(s_tab + par * L::TABF, cb, cg, p.scale, log2_min);
+            lt_arrive(b_w + 8 * par);
         }
-        if (OUT && ok) store_out(NL - 1);
-        if (lane == 0) tc::bulk_wait0();
-        if (!OUT && ok && lane == 0 && blockIdx.x == 0)
-            p.segdec[(size_t)bh * p.S + seg] = exp2f(seglog);
+    } else if (warp == 19) {
+        // ---- rows out, and z of the chunk after next into the same place ----
+        if (OUT && lane == 0) {
+            int loads[2] = {1, NL > 1};
+            bool ok = true;
+            for (int it = 0; it < NL; ++it) {
+                const int st = it & 1;
+                ok = lt_wait(b_out + 8 * st, (it >> 1) & 1, abort);
+                if (!ok) break;
+                tma_store_3d(&A.out, zh * kLtZN, chunk(it) * C, bh, sm + L::Z + st * L::HALF);
+                tc::bulk_commit();
+                tc::bulk_wait_read0();
+                if (it + 2 < NL) {
+                    load_z(it + 2);
+                    ++loads[st];
+                }
+            }
+            tc::bulk_wait0();
+            if (!ok)
+                for (int i = 0; i < 2; ++i)
+                    if (loads[i]) lt_drain(b_z + 8 * i, (loads[i] - 1) & 1);
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ---- scores and outputs: thread has token `row`, 64 score columns, 32 of z ----
+        if (OUT) {
+            const int half = warp >> 2, z0 = zh * kLtZN + half * 32;
+            for (int it = 0; it < NL; ++it) {
+                const int sg = it & 1, ph = it & 1;
+                const float *tab = s_tab + sg * L::TABF;
+                if (!wait(b_w + 8 * sg, (it >> 1) & 1) || !wait(b_p, ph)) break;
+                tc::fence_after_sync();
+                // 16 columns at a time, in a loop: straight-line code for all of them would not
+                // stay in the instruction caches.  A warp's bf16 columns lie over scores that
+                // it has read itself.
+#pragma unroll 1
+                for (int h = 0; h < 4; ++h) {
+                    const int c0 = half * 64 + h * 16, cb = c0 >> 5;
+                    float pk[8];   // pairs of bf16 as 32-bit columns
+                    if (REV ? cb < quarter : cb > quarter) {   // beyond the diagonal
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) pk[j] = 0.f;
+                    } else {
+                        float v[16];
+                        tc::tmem_ld16(tl + kP + c0, v);
+                        if (cb == quarter) {
+                            const float4 *w4 = reinterpret_cast<const float4 *>(tab + (REV ? 3 : 4) * C + c0);
+                            const float lt = tab[3 * C + row];
+                            const int first = lane - (h & 1) * 16;   // column of the token itself
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 c4 = w4[j / 4];
+                                float w[4] = {lt - c4.x, lt - c4.y, lt - c4.z, lt - c4.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    // 2^(l_t - l_i) up to and including the token itself
+                                    w[e] = ex2(REV ? -w[e] : w[e]) * v[j + e];
+                                    w[e] = (REV ? j + e >= first : j + e <= first) ? w[e] : 0.f;
+                                }
+                                pk[j / 2] = __uint_as_float(bf16x2_bits(w[0], w[1]));
+                                pk[j / 2 + 1] = __uint_as_float(bf16x2_bits(w[2], w[3]));
+                            }
+                        } else {
+                            const float4 *w4 = reinterpret_cast<const float4 *>(
+                                tab + (6 + (REV ? quarter : quarter - 1)) * C + c0);
+                            float2 rf;
+                            rf.x = rf.y = tab[5 * C + row];
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 c4 = w4[j / 4];
+                                const float2 x = __fmul2_rn(__fmul2_rn(make_float2(c4.x, c4.y), rf),
+                                                            make_float2(v[j], v[j + 1]));
+                                const float2 y = __fmul2_rn(__fmul2_rn(make_float2(c4.z, c4.w), rf),
+                                                            make_float2(v[j + 2], v[j + 3]));
+                                pk[j / 2] = __uint_as_float(f2_bf16x2(x));
+                                pk[j / 2 + 1] = __uint_as_float(f2_bf16x2(y));
+                            }
+                        }
+                    }
+                    tc::tmem_st8(tl + kP + half * 64 + h * 8, pk);
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                arrive(b_pb);
+
+                const int t = chunk(it) * C + row;
+                const size_t grow = (size_t)bh * p.T + t;
+                const bool in = t < p.T;
+                const uint4 *xd = reinterpret_cast<const uint4 *>(
+                    static_cast<const __nv_bfloat16 *>(p.xd) + grow * D + z0);
+                const bool dots = p.dot && in;
+                const float a = tab[row], g = tab[2 * C + row];
+                float d = 0.f;
+                if (!wait(b_o, ph)) break;
+                tc::fence_after_sync();
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    float vs[16], vi[16];
+                    tc::tmem_ld16(tl + kOS + half * 32 + h * 16, vs);
+                    tc::tmem_ld16(tl + kOI + half * 32 + h * 16, vi);
+                    tc::tmem_wait_ld();
+                    if (h == 1) {
+                        tc::fence_before_sync();
+                        arrive(b_oread);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) vs[j] *= a;
+                    if (dots) {
+                        const uint4 x0 = __ldg(xd + 2 * h), x1 = __ldg(xd + 2 * h + 1);
+                        const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            d = fmaf(vs[2 * j], bf16_lo(w[j]), fmaf(vs[2 * j + 1], bf16_hi(w[j]), d));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        vi[j] = fmaf(p.scale, vi[j], vs[j]) * (REV ? g : 1.f);
+                    // staged where the chunk's z was (its last reader, OI, has completed)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        Vec16<__nv_bfloat16>::store(
+                            reinterpret_cast<__nv_bfloat16 *>(
+                                sm + L::Z + sg * L::HALF + row * 128 +
+                                (((half * 4 + h * 2 + e) ^ (row & 7)) << 4)),
+                            vi + 8 * e);
+                }
+                if (dots) p.dot[(size_t)(zh * 2 + half) * p.BH * p.T + grow] = d;
+                fence_proxy_async_smem();
+                arrive(b_out + 8 * sg);
+                arrive(b_tfree + 8 * sg);
+            }
+        }
     } else {
-        const int quarter = warp & 3, cg = warp >> 2;
-        const int row = quarter * 32 + lane;              // TMEM lane: token of P, OI, OS; y row of S
-        const int z0 = zh * kLtZN + cg * 16;              // this thread's columns of z
-        const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
-        float st[16];
+        // ---- state: thread has y row `row`, 32 columns of z ----
+        const int half = (warp >> 2) & 1, z0 = zh * kLtZN + half * 32, gt = tid - kLtGroup;
+        float st[32];
         // a state in memory: [y][z], or [z][y] (then lanes are neighbours)
         auto at = [&](size_t base, int j) {
             return base + (p.zy ? (size_t)(z0 + j) * D + row : (size_t)row * D + z0 + j);
         };
 #pragma unroll
-        for (int j = 0; j < 16; ++j) st[j] = 0.f;
+        for (int j = 0; j < 32; ++j) st[j] = 0.f;
         if (OUT && p.start) {
             const size_t base = ((size_t)bh * p.S + seg) * D * D;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) st[j] = p.start[at(base, j)];
+            for (int j = 0; j < 32; ++j) st[j] = p.start[at(base, j)];
         }
-        auto arrive = [&](uint32_t bar) {
-            __syncwarp();
-            if (lane == 0) lt_arrive(bar);
-        };
+        float dec = 1.f;   // the segment's decay so far
         bool ok = true;
         for (int it = 0; it < NL; ++it) {
-            const int sg = it & 1, ph = it & 1, ph2 = (it >> 1) & 1, n = chunk(it);
+            const int sg = it & 1, ph = it & 1, n = chunk(it);
             const float *tab = s_tab + sg * L::TABF;
             if (OUT) {
                 // the state before the chunk as the B operand, rows of y, two bf16 parts
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < 4; ++h) {
                     uint32_t a[4], b[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -506,22 +668,19 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                         a[e] = f2_bf16x2(y);
                         b[e] = f2_bf16x2(f2_rest(y, a[e]));
                     }
-                    uint8_t *dst = sm + L::SOP + row * 128 + (((cg * 2 + h) ^ (row & 7)) << 4);
+                    uint8_t *dst = sm + L::SOP + row * 128 + (((half * 4 + h) ^ (row & 7)) << 4);
                     *reinterpret_cast<uint4 *>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
                     *reinterpret_cast<uint4 *>(dst + L::HALF) = make_uint4(b[0], b[1], b[2], b[3]);
                 }
                 fence_proxy_async_smem();
                 arrive(b_s);
             }
-            ok = __all_sync(0xffffffffu,
-                            lt_wait(b_w + 8 * sg, ph2, abort) && lt_wait(b_yz + 8 * sg, ph2, abort));
+            ok = wait(b_w + 8 * sg, (it >> 1) & 1) && wait(b_z + 8 * sg, (it >> 1) & 1);
             if (!ok) break;
-            // (u z) in three bf16 parts, at the places of z (and of the last chunk's staged rows)
-            if (OUT && it >= 1) ok = __all_sync(0xffffffffu, lt_wait(b_ofree, (it - 1) & 1, abort));
-            if (!ok) break;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t item = tid + j * kLtMath, off = item * 16;   // row item / 8
+            // (u z) in three bf16 parts, at the places of z
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t item = gt + j * kLtGroup, off = item * 16;   // row item / 8
                 const uint4 w4 = *reinterpret_cast<const uint4 *>(sm + L::Z + sg * L::HALF + off);
                 const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
                 const float u = tab[C + (item >> 3)];
@@ -541,142 +700,37 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             }
             fence_proxy_async_smem();
             arrive(b_parts);
-            if (OUT) {
-                if (p.states) {
-                    float *dst = p.states + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
+            const float b = tab[9 * C];
+            if (OUT && p.states) {
+                float *dst = p.states + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) dst[j * D] = st[j];
-                }
-                if (p.states_in) {
-                    const float *src = p.states_in + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
-                    float f = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) f = fmaf(st[j], __ldcs(src + j * D), f);
-                    f = warp_sum(f);
-                    if (lane == 0)
-                        p.fdot[((size_t)(zh * 16 + warp) * p.BH + bh) * p.N + n] = tab[9 * C] * f;
-                }
-                // weighted scores: columns 32 cg .. of token `row`
-                const bool zero = REV ? cg < quarter : cg > quarter;
-                float pk[16];   // pairs of bf16 as 32-bit columns
-                ok = __all_sync(0xffffffffu, lt_wait(b_p, ph, abort));
-                if (!ok) break;
-                tc::fence_after_sync();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) pk[j] = 0.f;
-                if (!zero) {
-                    // 16 columns at a time, so that the state's registers need not be spilled
-#pragma unroll
-                    for (int h = 0; h < 32; h += 16) {
-                        const int c0 = cg * 32 + h;
-                        float v[16];
-                        tc::tmem_ld16(tl + kP + c0, v);
-                        tc::tmem_wait_ld();
-                        const float4 *w4;   // weights' exponents, or their column factors
-                        float2 rf;
-                        if (cg == quarter) {
-                            w4 = reinterpret_cast<const float4 *>(tab + (REV ? 3 : 4) * C + c0);
-                            rf.x = rf.y = tab[3 * C + row];
-                        } else {
-                            w4 = reinterpret_cast<const float4 *>(
-                                tab + (6 + (REV ? quarter : quarter - 1)) * C + c0);
-                            rf.x = rf.y = tab[5 * C + row];
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 c4 = w4[j / 4];
-#pragma unroll
-                            for (int e = 0; e < 4; e += 2) {
-                                float2 w = e ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
-                                if (cg == quarter) {
-                                    // 2^(l_t - l_i) up to and including the token itself
-                                    w = REV ? __ffma2_rn(rf, make_float2(-1.f, -1.f), w)
-                                            : __ffma2_rn(w, make_float2(-1.f, -1.f), rf);
-                                    const int i = h + j + e;
-                                    w.x = (REV ? i >= lane : i <= lane) ? ex2(w.x) : 0.f;
-                                    w.y = (REV ? i + 1 >= lane : i + 1 <= lane) ? ex2(w.y) : 0.f;
-                                } else {
-                                    w = __fmul2_rn(w, rf);
-                                }
-                                w = __fmul2_rn(w, make_float2(v[j + e], v[j + e + 1]));
-                                pk[(h + j + e) / 2] = __uint_as_float(f2_bf16x2(w));
-                            }
-                        }
-                    }
-                }
-                // the four warps of these lanes have their scores: the columns are free
-                tc::fence_before_sync();
-                arrive(b_quart + 8 * quarter);
-                ok = __all_sync(0xffffffffu, lt_wait(b_quart + 8 * quarter, ph, abort));
-                if (!ok) break;
-                tc::fence_after_sync();
-                tc::tmem_st16(tl + kPB + cg * 16, pk);
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                arrive(b_pb);
+                for (int j = 0; j < 32; ++j) dst[j * D] = st[j];
             }
+            if (OUT && p.states_in) {
+                const float *src = p.states_in + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
+                float f = 0.f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) f = fmaf(st[j], __ldcs(src + j * D), f);
+                f = warp_sum(f);
+                if (lane == 0) p.fdot[((size_t)(zh * 8 + warp - 8) * p.BH + bh) * p.N + n] = b * f;
+            }
+            dec *= b;
             // S' = b S + DS
-            ok = __all_sync(0xffffffffu, lt_wait(b_ds, ph, abort));
+            ok = wait(b_ds, ph);
             if (!ok) break;
             tc::fence_after_sync();
-            {
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
                 float v[16], w[16];
-                tc::tmem_ld16(tl + kDS + 64 + cg * 16, v);
-                tc::tmem_ld16(tl + kDS + 128 + cg * 16, w);
+                tc::tmem_ld16(tl + kDS + 64 + half * 32 + h, v);
+                tc::tmem_ld16(tl + kDS + 128 + half * 32 + h, w);
                 tc::tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] += w[j];
-                tc::tmem_ld16(tl + kDS + cg * 16, w);
-                tc::tmem_wait_ld();
-                const float b = tab[9 * C];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) st[j] = fmaf(b, st[j], w[j] + v[j]);
-            }
-            if (OUT) {
-                const int t = n * C + row;
-                const size_t grow = (size_t)bh * p.T + t;
-                const bool in = t < p.T;
-                uint4 xd[2] = {};
-                if (p.dot && in) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(
-                        static_cast<const __nv_bfloat16 *>(p.xd) + grow * D + z0);
-                    xd[0] = __ldg(src);
-                    xd[1] = __ldg(src + 1);
-                }
-                const float a = tab[row], g = tab[2 * C + row];
-                ok = __all_sync(0xffffffffu, lt_wait(b_o, ph, abort));
-                if (!ok) break;
-                tc::fence_after_sync();
-                float vs[16], vi[16];
-                tc::tmem_ld16(tl + kOS + cg * 16, vs);
-                tc::tmem_ld16(tl + kOS + 64 + cg * 16, vi);
+                tc::tmem_ld16(tl + kDS + half * 32 + h, w);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) vs[j] = a * (vs[j] + vi[j]);
-                tc::tmem_ld16(tl + kOI + cg * 16, vi);
-                float d = 0.f;
-                if (p.dot) {
-                    const uint32_t w[8] = {xd[0].x, xd[0].y, xd[0].z, xd[0].w,
-                                           xd[1].x, xd[1].y, xd[1].z, xd[1].w};
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        d = fmaf(vs[2 * j], bf16_lo(w[j]), fmaf(vs[2 * j + 1], bf16_hi(w[j]), d));
-                }
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    vi[j] = fmaf(p.scale, vi[j], vs[j]) * (REV ? g : 1.f);
-                if (p.dot && in) p.dot[(size_t)(zh * 4 + cg) * p.BH * p.T + grow] = d;
-                // staged where the increments' parts were (their product has completed)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    Vec16<__nv_bfloat16>::store(
-                        reinterpret_cast<__nv_bfloat16 *>(sm + L::PARTS + row * 128 +
-                                                          (((cg * 2 + h) ^ (row & 7)) << 4)),
-                        vi + 8 * h);
-                fence_proxy_async_smem();
-                tc::fence_before_sync();
-                arrive(b_out);
+                for (int j = 0; j < 16; ++j) st[h + j] = fmaf(b, st[h + j], w[j] + v[j]);
             }
             tc::fence_before_sync();
             arrive(b_tfree + 8 * sg);
@@ -685,8 +739,9 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         if (ok && dst) {
             const size_t base = OUT ? (size_t)bh * D * D : ((size_t)bh * p.S + seg) * D * D;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) dst[at(base, j)] = st[j];
+            for (int j = 0; j < 32; ++j) dst[at(base, j)] = st[j];
         }
+        if (!OUT && ok && gt == 0 && blockIdx.x == 0) p.segdec[(size_t)bh * p.S + seg] = dec;
     }
     // every product and copy has completed (the arithmetic warps waited for the last
     // chunk's; after a time-out the issuer drained them)
