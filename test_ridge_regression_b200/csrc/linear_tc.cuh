@@ -72,7 +72,7 @@ struct LtSmem {
     // the column; forward), ta, c[3]; then b
     static constexpr uint32_t TABF = 9 * kLtC + 4;
     static constexpr uint32_t BARS = TAB + 2 * 4 * TABF;
-    static constexpr uint32_t TBASE = BARS + 8 * 22;      // TMEM base, abort flag
+    static constexpr uint32_t TBASE = BARS + 8 * 20;      // TMEM base, abort flag
     static constexpr uint32_t END = TBASE + 16;
     static constexpr size_t bytes = END + 1024;
 };
@@ -152,6 +152,11 @@ __device__ __forceinline__ bool lt_wait(uint32_t bar, uint32_t parity, uint32_t 
     }
     asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
     return false;
+}
+// The same as a call: one copy of the code for the warps that mostly wait, which the
+// instruction caches keep.
+__device__ __noinline__ bool lt_wait_call(uint32_t bar, uint32_t parity, uint32_t abort) {
+    return lt_wait(bar, parity, abort);
 }
 // After a time-out: a bounded wait for work in flight.
 __device__ __noinline__ void lt_drain(uint32_t bar, uint32_t parity) {
@@ -274,11 +279,10 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     const uint32_t sb = smem_u32(sm);
     const uint32_t bars = sb + L::BARS;
     const uint32_t b_x = bars, b_p = bars + 8, b_parts = bars + 16, b_s = bars + 24, b_pb = bars + 32,
-                   b_ds = bars + 40, b_o = bars + 48, b_xfree = bars + 56, b_oread = bars + 64,
+                   b_ds = bars + 40, b_o = bars + 48, b_xfree = bars + 56, b_os = bars + 64,
                    b_fin = bars + 72;
     const uint32_t b_y = bars + 80, b_z = bars + 96, b_w = bars + 112, b_tfree = bars + 128,
                    b_out = bars + 144;                                                         // [2]
-    const uint32_t b_os = bars + 160;
     uint32_t *tbase = reinterpret_cast<uint32_t *>(sm + L::TBASE);
     const uint32_t abort = sb + L::TBASE + 4;
     float *s_tab = reinterpret_cast<float *>(sm + L::TAB);
@@ -303,13 +307,12 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         lt_init(b_x, 1);
         lt_init(b_p, 1);
         lt_init(b_parts, 8);
-        lt_init(b_s, 8);
+        lt_init(b_s, 16);   // S staged, and the last chunk's OS read
         lt_init(b_pb, 8);
         lt_init(b_ds, 1);
         lt_init(b_o, 1);
         lt_init(b_xfree, 1);
         lt_init(b_fin, 1);
-        lt_init(b_oread, 8);
         lt_init(b_os, 1);
         asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(0u) : "memory");
         fence_mbar_init();
@@ -361,117 +364,99 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     auto wait = [&](uint32_t bar, uint32_t parity) {   // the whole warp, one outcome
         return __all_sync(0xffffffffu, lt_wait(bar, parity, abort)) != 0;
     };
+    auto wait_call = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, lt_wait_call(bar, parity, abort)) != 0;
+    };
 
     if (warp == 16) {
         // ---- issuer: the whole warp runs the loop, one lane issues ----
         constexpr uint32_t ID_P = tc::idesc_bf16(128, 128, false, false);
         constexpr uint32_t ID_O = tc::idesc_bf16(128, 64, false, true);
         constexpr uint32_t ID_D = tc::idesc_bf16(128, 192, true, true);
-        auto kmaj = [&](uint32_t base, int kk) {
-            return tc::sdesc(sb + base + (kk >> 2) * L::HALF + (kk & 3) * 32, 16, 1024);
-        };
-        auto mnmaj = [&](uint32_t base, int kk) { return tc::sdesc(sb + base + kk * 2048, L::HALF, 1024); };
-        int loads_x = OUT, loads_y[2] = {1, NL > 1};   // loads begun
+        // descriptors: one per operand, and the steps (in 16 bytes) to the kk-th K step and to
+        // the other stage, so that a product costs an addition and the instruction
+        const uint64_t d_x = tc::sdesc(sb + L::X, 16, 1024), d_yk = tc::sdesc(sb + L::Y, 16, 1024),
+                       d_ym = tc::sdesc(sb + L::Y, L::HALF, 1024), d_z = tc::sdesc(sb + L::Z, L::HALF, 1024),
+                       d_s = tc::sdesc(sb + L::SOP, L::HALF, 1024),
+                       d_u = tc::sdesc(sb + L::PARTS, L::HALF, 1024);
+        auto kmaj = [](int kk) { return (uint64_t)((kk >> 2) * (L::HALF / 16) + (kk & 3) * 2); };
+        auto mnmaj = [](int kk) { return (uint64_t)(kk * 128); };
         // x(it) from shared memory to TMEM, which frees its stage; the last chunk's readers
         // of those columns are done
         auto copy_x = [&](int it) {
-            if (!wait(b_x, it & 1)) return false;
+            if (!wait_call(b_x, it & 1)) return false;
             tc::fence_after_sync();
             if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) cp_128x256b(tmem + kX + kk * 8, kmaj(L::X, kk));
+                for (int kk = 0; kk < 8; ++kk) cp_128x256b(tmem + kX + kk * 8, d_x + kmaj(kk));
                 lt_commit(b_xfree);
             }
             return true;
         };
         auto issue_p = [&](int it) {
             const int st = it & 1;
-            if (!wait(b_y + 8 * st, (it >> 1) & 1)) return false;
+            if (!wait_call(b_y + 8 * st, (it >> 1) & 1)) return false;
             if (elect_one()) {
-                const uint32_t y = L::Y + st * L::TILE;
+                const uint64_t y = d_yk + st * (L::TILE / 16);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16_ta(tmem + kP, tmem + kX + kk * 8, kmaj(y, kk), ID_P, kk > 0);
+                    mma_bf16_ta(tmem + kP, tmem + kX + kk * 8, y + kmaj(kk), ID_P, kk > 0);
                 lt_commit(b_p);
             }
             return true;
         };
         bool ok = !OUT || (copy_x(0) && issue_p(0));
+#pragma unroll 1
         for (int it = 0; ok && it < NL; ++it) {
             const int st = it & 1, ph = it & 1;
             if (OUT) {
-                if (it + 1 < NL) {
-                    ok = wait(b_xfree, ph);
-                    if (!ok) break;
-                    if (elect_one()) load_x(it + 1);
-                    ++loads_x;
-                }
                 // the state operand is there and the last chunk's OS has been read
-                ok = wait(b_s, ph) && (it == 0 || wait(b_oread, ph ^ 1));
+                ok = wait_call(b_s, ph);
                 if (!ok) break;
                 tc::fence_after_sync();
                 if (elect_one()) {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_bf16_ta(tmem + kOS, tmem + kX + kk * 8, mnmaj(L::SOP + q * L::HALF, kk),
-                                        ID_O, (q | kk) != 0);
+                    for (int kk = 0; kk < 16; ++kk)   // K steps against S_hi, then S_lo, 16 KB on
+                        mma_bf16_ta(tmem + kOS, tmem + kX + (kk & 7) * 8, d_s + mnmaj(kk), ID_O, kk > 0);
                     lt_commit(b_os);
                 }
             } else {
-                ok = wait(b_y + 8 * st, (it >> 1) & 1);
+                ok = wait_call(b_y + 8 * st, (it >> 1) & 1);
                 if (!ok) break;
             }
-            ok = wait(b_parts, ph);
+            ok = wait_call(b_parts, ph);
             if (!ok) break;
             tc::fence_after_sync();
             if (elect_one()) {
-                const uint32_t y = L::Y + st * L::TILE;
+                const uint64_t y = d_ym + st * (L::TILE / 16);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    tc::mma_f16(tmem + kDS, mnmaj(y, kk), mnmaj(L::PARTS, kk), ID_D, kk > 0);
+                    tc::mma_f16(tmem + kDS, y + mnmaj(kk), d_u + mnmaj(kk), ID_D, kk > 0);
                 lt_commit(b_ds);
             }
             if (OUT) {
-                ok = wait(b_pb, ph);
+                ok = wait_call(b_pb, ph);
                 if (!ok) break;
                 tc::fence_after_sync();
                 if (elect_one()) {
-                    const uint32_t z = L::Z + st * L::HALF;
+                    const uint64_t z = d_z + st * (L::HALF / 16);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_ta(tmem + kOI, tmem + kP + (kk >> 2) * 64 + (kk & 3) * 8, mnmaj(z, kk), ID_O,
+                        mma_bf16_ta(tmem + kOI, tmem + kP + (kk >> 2) * 64 + (kk & 3) * 8, z + mnmaj(kk), ID_O,
                                     kk > 0);
                     lt_commit(b_o);
                 }
                 // x of the next chunk once this one's P and OS have read TMEM's; its scores once
                 // OI has read the weighted ones, whose columns they take
-                if (it + 1 < NL) ok = wait(b_os, ph) && copy_x(it + 1) && wait(b_o, ph) && issue_p(it + 1);
-                if (!ok) break;
-            }
-            if (it + 2 < NL) {
-                // y's readers, P(it) and DS(it), are done
-                ok = wait(OUT ? b_o : b_ds, ph);
-                if (!ok) break;
-                if (elect_one()) {
-                    load_y(it + 2);
-                    if (!OUT) load_z(it + 2);
-                }
-                ++loads_y[st];
+                if (it + 1 < NL)
+                    ok = wait_call(b_os, ph) && copy_x(it + 1) && wait_call(b_o, ph) && issue_p(it + 1);
             }
         }
         if (!ok && elect_one()) {
-            // a wait gave up: flag it, then drain this thread's products and copies
+            // a wait gave up: flag it, then drain this thread's products
             atomicExch(timeout_flag, 1);
             lt_commit(b_fin);
             lt_drain(b_fin, 0);
-            if (loads_x) lt_drain(b_x, (loads_x - 1) & 1);
-            for (int i = 0; i < 2; ++i)
-                if (loads_y[i]) {
-                    lt_drain(b_y + 8 * i, (loads_y[i] - 1) & 1);
-                    if (!OUT) lt_drain(b_z + 8 * i, (loads_y[i] - 1) & 1);
-                }
         }
         __syncwarp();
     } else if (warp == 17 || warp == 18) {
@@ -492,7 +477,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         const int par = warp - 17;
         if (par < NL) fetch(par);
         for (int it = par; it < NL; it += 2) {
-            if (it >= 2 && !wait(b_tfree + 8 * par, ((it - 2) >> 1) & 1)) break;
+            if (it >= 2 && !wait_call(b_tfree + 8 * par, ((it - 2) >> 1) & 1)) break;
             float cb[4], cg[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -504,32 +489,53 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             lt_arrive(b_w + 8 * par);
         }
     } else if (warp == 19) {
-        // ---- rows out, and z of the chunk after next into the same place ----
-        if (OUT && lane == 0) {
-            int loads[2] = {1, NL > 1};
+        // ---- loads into freed stages, rows out ----
+        if (lane == 0) {
+            int loads_x = OUT, loads_y[2] = {1, NL > 1}, loads_z[2] = {1, NL > 1};   // begun
             bool ok = true;
+#pragma unroll 1
             for (int it = 0; it < NL; ++it) {
-                const int st = it & 1;
-                ok = lt_wait(b_out + 8 * st, (it >> 1) & 1, abort);
-                if (!ok) break;
-                tma_store_3d(&A.out, zh * kLtZN, chunk(it) * C, bh, sm + L::Z + st * L::HALF);
-                tc::bulk_commit();
-                tc::bulk_wait_read0();
+                const int st = it & 1, ph = it & 1;
+                if (OUT && it + 1 < NL) {   // x(it) is in TMEM
+                    ok = lt_wait_call(b_xfree, ph, abort);
+                    if (!ok) break;
+                    load_x(it + 1);
+                    ++loads_x;
+                }
+                if (it + 2 < NL) {   // y's readers, P(it) and DS(it), are done
+                    ok = lt_wait_call(OUT ? b_o : b_ds, ph, abort);
+                    if (!ok) break;
+                    load_y(it + 2);
+                    ++loads_y[st];
+                }
+                if (OUT) {   // the rows lie where z did, whose next chunk follows them
+                    ok = lt_wait_call(b_out + 8 * st, (it >> 1) & 1, abort);
+                    if (!ok) break;
+                    tma_store_3d(&A.out, zh * kLtZN, chunk(it) * C, bh, sm + L::Z + st * L::HALF);
+                    tc::bulk_commit();
+                    tc::bulk_wait_read0();
+                }
                 if (it + 2 < NL) {
                     load_z(it + 2);
-                    ++loads[st];
+                    ++loads_z[st];
                 }
             }
-            tc::bulk_wait0();
-            if (!ok)
-                for (int i = 0; i < 2; ++i)
-                    if (loads[i]) lt_drain(b_z + 8 * i, (loads[i] - 1) & 1);
+            if (OUT) tc::bulk_wait0();
+            if (!ok) {   // a wait gave up: drain this thread's copies
+                if (loads_x) lt_drain(b_x, (loads_x - 1) & 1);
+                for (int i = 0; i < 2; ++i) {
+                    if (loads_y[i]) lt_drain(b_y + 8 * i, (loads_y[i] - 1) & 1);
+                    if (loads_z[i]) lt_drain(b_z + 8 * i, (loads_z[i] - 1) & 1);
+                }
+            }
         }
         __syncwarp();
     } else if (warp < 8) {
         // ---- scores and outputs: thread has token `row`, 64 score columns, 32 of z ----
         if (OUT) {
             const int half = warp >> 2, z0 = zh * kLtZN + half * 32;
+            arrive(b_s);   // no OS to read before the first
+#pragma unroll 1
             for (int it = 0; it < NL; ++it) {
                 const int sg = it & 1, ph = it & 1;
                 const float *tab = s_tab + sg * L::TABF;
@@ -608,7 +614,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                     tc::tmem_wait_ld();
                     if (h == 1) {
                         tc::fence_before_sync();
-                        arrive(b_oread);
+                        arrive(b_s);
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j) vs[j] *= a;
