@@ -55,6 +55,7 @@ constexpr int kLtC = 128;                       // tokens per chunk
 constexpr int kLtZN = 64;                       // columns of z a CTA owns
 constexpr int kLtGroup = 256;                   // threads of an arithmetic group (two)
 constexpr int kLtThreads = 2 * kLtGroup + 128;  // + issuer, two decay warps, store warp
+constexpr int kLtTabs = 4;                      // stages of decay tables
 constexpr int kLtDots = 4, kLtFdots = 16;       // planes of dot and fdot partials per pass
 constexpr uint32_t kLtProbes = 1u << 20;
 constexpr uint32_t kLtHintNs = 2000;            // a probe suspends its warp for up to this long
@@ -67,12 +68,12 @@ struct LtSmem {
     static constexpr uint32_t Z = Y + 2 * TILE;           // 2 stages
     static constexpr uint32_t PARTS = Z + 2 * HALF;       // hi, mid, lo of u z
     static constexpr uint32_t SOP = PARTS + 3 * HALF;     // hi, lo of the state
-    static constexpr uint32_t TAB = SOP + 2 * HALF;       // 2 x decay tables
-    // table floats, 128 tokens each: a, u, g, l (of the row), m (l less log2 of the gate, of
-    // the column; forward), ta, c[3]; then b
-    static constexpr uint32_t TABF = 9 * kLtC + 4;
-    static constexpr uint32_t BARS = TAB + 2 * 4 * TABF;
-    static constexpr uint32_t TBASE = BARS + 8 * 20;      // TMEM base, abort flag
+    static constexpr uint32_t TAB = SOP + 2 * HALF;       // decay tables of the chunks in flight
+    // table floats, 128 tokens each: a, u, l (of the row), ta, c[3], and g (backward) or m (l
+    // less log2 of the gate, of the column; forward); then b
+    static constexpr uint32_t TABF = 8 * kLtC + 4;
+    static constexpr uint32_t BARS = TAB + kLtTabs * 4 * TABF;
+    static constexpr uint32_t TBASE = BARS + 8 * (16 + 2 * kLtTabs);      // TMEM base, abort flag
     static constexpr uint32_t END = TBASE + 16;
     static constexpr size_t bytes = END + 1024;
 };
@@ -221,51 +222,59 @@ __device__ __forceinline__ Log2Sum shfl(Log2Sum x, int src) {
 }
 
 // Decay tables of one chunk by one warp; lane l holds tokens 32 j + l, whose beta and
-// gate are bv[j] and gv[j] (1 and 0 past the sequence's end). 
+// gate are bv[j] and gv[j] (1 and 0 past the sequence's end).  Loops stay rolled: the
+// kernel's hot code has to share the instruction caches.
 template <bool REV>
 __device__ __forceinline__ void lt_tables(float *tab, const float *bv, const float *gv, float scale,
                                           float log2_min) {
     const int lane = threadIdx.x & 31;
-    float *ta_a = tab + lane, *ta_u = ta_a + kLtC, *ta_g = ta_u + kLtC, *ta_l = ta_g + kLtC,
-          *ta_m = ta_l + kLtC, *ta_t = ta_m + kLtC, *ta_c = ta_t + kLtC;
+    float *ta_a = tab + lane, *ta_u = ta_a + kLtC, *ta_l = ta_u + kLtC, *ta_t = ta_l + kLtC,
+          *ta_c = ta_t + kLtC, *ta_gm = ta_c + 3 * kLtC;
     const Log2Sum zero = {0.f, 0.f};
-    Log2Sum l[4], edge[4], base = zero;   // edge[b]: cumulative log at the end of block b
-#pragma unroll
-    for (int j = 0; j < 4; ++j) l[j] = {fmaxf(log2f(bv[j]), log2_min), 0.f};
-    // the four blocks' scans, step by step together
+    Log2Sum e0 = zero, e1 = zero, e2 = zero, end = zero;   // cumulative log at the ends of the blocks
+    float b0 = bv[0], b1 = bv[1], b2 = bv[2], b3 = bv[3];
 #pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const Log2Sum y = {__shfl_up_sync(0xffffffffu, l[j].hi, o), __shfl_up_sync(0xffffffffu, l[j].lo, o)};
-            if (lane >= o) l[j] = l[j] + y;
-        }
-    }
-#pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const Log2Sum start = base;
-        base = base + shfl(l[j], 31);
-        edge[j] = base;
-        ta_l[32 * j] = l[j].hi + l[j].lo;
-        l[j] = start + l[j];
+        Log2Sum l = {fmaxf(log2f(b0), log2_min), 0.f};
+        b0 = b1;
+        b1 = b2;
+        b2 = b3;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const Log2Sum y = {__shfl_up_sync(0xffffffffu, l.hi, o), __shfl_up_sync(0xffffffffu, l.lo, o)};
+            if (lane >= o) l = l + y;
+        }
+        ta_l[32 * j] = l.hi + l.lo;   // from the block's start
+        const Log2Sum c = end + l;
+        ta_a[32 * j] = c.hi;          // parked until the second loop
+        ta_u[32 * j] = c.lo;
+        end = end + shfl(l, 31);
+        if (j == 0) e0 = end;
+        if (j == 1) e1 = end;
+        if (j == 2) e2 = end;
     }
-#pragma unroll
+    float g0 = gv[0], g1 = gv[1], g2 = gv[2], g3 = gv[3];
+#pragma unroll 1
     for (int j = 0; j < 4; ++j) {
         const int t = 32 * j;
-        const float to = exp2_diff(l[j], zero), from = exp2_diff(edge[3], l[j]);
+        const Log2Sum l = {ta_a[t], ta_u[t]};
+        const float g = g0, lb = ta_l[t];
+        g0 = g1;
+        g1 = g2;
+        g2 = g3;
+        const float to = exp2_diff(l, zero), from = exp2_diff(end, l);
         ta_a[t] = REV ? from : scale * to;
-        ta_u[t] = REV ? scale * to : gv[j] * from;
-        ta_g[t] = gv[j];
-        if (!REV) ta_m[t] = ta_l[t] - log2f(gv[j]);   // closed gate: +inf, whose weight is 0
-        ta_t[t] = REV ? exp2_diff(edge[j], l[j]) : ex2(ta_l[t]);
+        ta_u[t] = REV ? scale * to : g * from;
+        ta_gm[t] = REV ? g : lb - log2f(g);   // closed gate: +inf, whose weight is 0
+        const Log2Sum ej = j == 0 ? e0 : j == 1 ? e1 : j == 2 ? e2 : end;
+        ta_t[t] = REV ? exp2_diff(ej, l) : ex2(lb);
         // forward: c[b] serves block row b + 1, the blocks before it; backward: block row
-        // b, the blocks after it (other entries are not read)
-#pragma unroll
-        for (int b = 0; b < 3; ++b)
-            if (REV ? j > b : j <= b)
-                ta_c[b * kLtC + t] = REV ? exp2_diff(l[j], edge[b]) : gv[j] * exp2_diff(edge[b], l[j]);
+        // b, the blocks after it (the other entries are not read; their exponents are > 0)
+        ta_c[t] = REV ? exp2_diff(l, e0) : g * exp2_diff(e0, l);
+        ta_c[kLtC + t] = REV ? exp2_diff(l, e1) : g * exp2_diff(e1, l);
+        ta_c[2 * kLtC + t] = REV ? exp2_diff(l, e2) : g * exp2_diff(e2, l);
     }
-    if (lane == 0) tab[9 * kLtC] = ex2(edge[3].hi + edge[3].lo);
+    if (lane == 0) tab[8 * kLtC] = ex2(end.hi + end.lo);
 }
 
 // grid (2 * passes, B*H, S), block kLtThreads.  OUT = false: segment aggregates.
@@ -274,15 +283,17 @@ __global__ void __launch_bounds__(kLtThreads, 1)
 k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_flag) {
     using L = LtSmem;
     constexpr int C = kLtC, D = 128;
-    extern __shared__ uint8_t smraw[];
-    uint8_t *sm = smem_align1024(smraw);
+    // the swizzled tiles start at the array's own 1024-byte boundary: operand addresses are
+    // constants, which an MMA takes without a register (checked below)
+    extern __shared__ __align__(1024) uint8_t lt_smem[];
+    uint8_t *sm = lt_smem;
     const uint32_t sb = smem_u32(sm);
     const uint32_t bars = sb + L::BARS;
     const uint32_t b_x = bars, b_p = bars + 8, b_parts = bars + 16, b_s = bars + 24, b_pb = bars + 32,
                    b_ds = bars + 40, b_o = bars + 48, b_xfree = bars + 56, b_os = bars + 64,
                    b_fin = bars + 72;
-    const uint32_t b_y = bars + 80, b_z = bars + 96, b_w = bars + 112, b_tfree = bars + 128,
-                   b_out = bars + 144;                                                         // [2]
+    const uint32_t b_y = bars + 80, b_z = bars + 96, b_out = bars + 112;                     // [2]
+    const uint32_t b_w = bars + 128, b_tfree = b_w + 8 * kLtTabs;                            // [kLtTabs]
     uint32_t *tbase = reinterpret_cast<uint32_t *>(sm + L::TBASE);
     const uint32_t abort = sb + L::TBASE + 4;
     float *s_tab = reinterpret_cast<float *>(sm + L::TAB);
@@ -300,9 +311,11 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         for (int i = 0; i < 2; ++i) {
             lt_init(b_y + 8 * i, 1);
             lt_init(b_z + 8 * i, 1);
+            lt_init(b_out + 8 * i, 8);
+        }
+        for (int i = 0; i < kLtTabs; ++i) {
             lt_init(b_w + 8 * i, 32);
             lt_init(b_tfree + 8 * i, OUT ? 16 : 8);
-            lt_init(b_out + 8 * i, 8);
         }
         lt_init(b_x, 1);
         lt_init(b_p, 1);
@@ -351,7 +364,12 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = *tbase;
+    // all 512 columns: they begin at 0
+    constexpr uint32_t tmem = 0;
+    if (*tbase != tmem || (sb & 1023u)) {
+        if (tid == 0) atomicExch(timeout_flag, 1);
+        asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
+    }
     // TMEM columns; the bf16 weighted scores of each half of the columns lie over its scores
     constexpr uint32_t kP = 0, kOI = 128, kOS = 192, kDS = 256, kX = 448;
     const int quarter = warp & 3;
@@ -362,9 +380,6 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         if (lane == 0) lt_arrive(bar);
     };
     auto wait = [&](uint32_t bar, uint32_t parity) {   // the whole warp, one outcome
-        return __all_sync(0xffffffffu, lt_wait(bar, parity, abort)) != 0;
-    };
-    auto wait_call = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, lt_wait_call(bar, parity, abort)) != 0;
     };
 
@@ -384,7 +399,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         // x(it) from shared memory to TMEM, which frees its stage; the last chunk's readers
         // of those columns are done
         auto copy_x = [&](int it) {
-            if (!wait_call(b_x, it & 1)) return false;
+            if (!wait(b_x, it & 1)) return false;
             tc::fence_after_sync();
             if (elect_one()) {
 #pragma unroll
@@ -395,7 +410,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         };
         auto issue_p = [&](int it) {
             const int st = it & 1;
-            if (!wait_call(b_y + 8 * st, (it >> 1) & 1)) return false;
+            if (!wait(b_y + 8 * st, (it >> 1) & 1)) return false;
             if (elect_one()) {
                 const uint64_t y = d_yk + st * (L::TILE / 16);
 #pragma unroll
@@ -411,7 +426,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             const int st = it & 1, ph = it & 1;
             if (OUT) {
                 // the state operand is there and the last chunk's OS has been read
-                ok = wait_call(b_s, ph);
+                ok = wait(b_s, ph);
                 if (!ok) break;
                 tc::fence_after_sync();
                 if (elect_one()) {
@@ -421,10 +436,10 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                     lt_commit(b_os);
                 }
             } else {
-                ok = wait_call(b_y + 8 * st, (it >> 1) & 1);
+                ok = wait(b_y + 8 * st, (it >> 1) & 1);
                 if (!ok) break;
             }
-            ok = wait_call(b_parts, ph);
+            ok = wait(b_parts, ph);
             if (!ok) break;
             tc::fence_after_sync();
             if (elect_one()) {
@@ -435,7 +450,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 lt_commit(b_ds);
             }
             if (OUT) {
-                ok = wait_call(b_pb, ph);
+                ok = wait(b_pb, ph);
                 if (!ok) break;
                 tc::fence_after_sync();
                 if (elect_one()) {
@@ -446,10 +461,9 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                                     kk > 0);
                     lt_commit(b_o);
                 }
-                // x of the next chunk once this one's P and OS have read TMEM's; its scores once
-                // OI has read the weighted ones, whose columns they take
-                if (it + 1 < NL)
-                    ok = wait_call(b_os, ph) && copy_x(it + 1) && wait_call(b_o, ph) && issue_p(it + 1);
+                // x of the next chunk into TMEM once this one's P and OS have read it there; its
+                // scores once OI has read the weighted ones, whose columns they take
+                if (it + 1 < NL) ok = wait(b_os, ph) && copy_x(it + 1) && wait(b_o, ph) && issue_p(it + 1);
             }
         }
         if (!ok && elect_one()) {
@@ -477,7 +491,8 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         const int par = warp - 17;
         if (par < NL) fetch(par);
         for (int it = par; it < NL; it += 2) {
-            if (it >= 2 && !wait_call(b_tfree + 8 * par, ((it - 2) >> 1) & 1)) break;
+            const int ts = it % kLtTabs;
+            if (it >= kLtTabs && !wait(b_tfree + 8 * ts, (it / kLtTabs - 1) & 1)) break;
             float cb[4], cg[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -485,8 +500,8 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 cg[j] = gv[j];
             }
             if (it + 2 < NL) fetch(it + 2);
-            lt_tables<REV>(s_tab + par * L::TABF, cb, cg, p.scale, log2_min);
-            lt_arrive(b_w + 8 * par);
+            lt_tables<REV>(s_tab + ts * L::TABF, cb, cg, p.scale, log2_min);
+            lt_arrive(b_w + 8 * ts);
         }
     } else if (warp == 19) {
         // ---- loads into freed stages, rows out ----
@@ -497,19 +512,19 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             for (int it = 0; it < NL; ++it) {
                 const int st = it & 1, ph = it & 1;
                 if (OUT && it + 1 < NL) {   // x(it) is in TMEM
-                    ok = lt_wait_call(b_xfree, ph, abort);
+                    ok = lt_wait(b_xfree, ph, abort);
                     if (!ok) break;
                     load_x(it + 1);
                     ++loads_x;
                 }
                 if (it + 2 < NL) {   // y's readers, P(it) and DS(it), are done
-                    ok = lt_wait_call(OUT ? b_o : b_ds, ph, abort);
+                    ok = lt_wait(OUT ? b_o : b_ds, ph, abort);
                     if (!ok) break;
                     load_y(it + 2);
                     ++loads_y[st];
                 }
                 if (OUT) {   // the rows lie where z did, whose next chunk follows them
-                    ok = lt_wait_call(b_out + 8 * st, (it >> 1) & 1, abort);
+                    ok = lt_wait(b_out + 8 * st, (it >> 1) & 1, abort);
                     if (!ok) break;
                     tma_store_3d(&A.out, zh * kLtZN, chunk(it) * C, bh, sm + L::Z + st * L::HALF);
                     tc::bulk_commit();
@@ -537,9 +552,9 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             arrive(b_s);   // no OS to read before the first
 #pragma unroll 1
             for (int it = 0; it < NL; ++it) {
-                const int sg = it & 1, ph = it & 1;
-                const float *tab = s_tab + sg * L::TABF;
-                if (!wait(b_w + 8 * sg, (it >> 1) & 1) || !wait(b_p, ph)) break;
+                const int sg = it & 1, ph = it & 1, ts = it % kLtTabs;
+                const float *tab = s_tab + ts * L::TABF;
+                if (!wait(b_w + 8 * ts, (it / kLtTabs) & 1) || !wait(b_p, ph)) break;
                 tc::fence_after_sync();
                 // 16 columns at a time, in a loop: straight-line code for all of them would not
                 // stay in the instruction caches.  A warp's bf16 columns lie over scores that
@@ -555,8 +570,8 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                         float v[16];
                         tc::tmem_ld16(tl + kP + c0, v);
                         if (cb == quarter) {
-                            const float4 *w4 = reinterpret_cast<const float4 *>(tab + (REV ? 3 : 4) * C + c0);
-                            const float lt = tab[3 * C + row];
+                            const float4 *w4 = reinterpret_cast<const float4 *>(tab + (REV ? 2 : 7) * C + c0);
+                            const float lt = tab[2 * C + row];
                             const int first = lane - (h & 1) * 16;   // column of the token itself
                             tc::tmem_wait_ld();
 #pragma unroll
@@ -574,9 +589,9 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                             }
                         } else {
                             const float4 *w4 = reinterpret_cast<const float4 *>(
-                                tab + (6 + (REV ? quarter : quarter - 1)) * C + c0);
+                                tab + (4 + (REV ? quarter : quarter - 1)) * C + c0);
                             float2 rf;
-                            rf.x = rf.y = tab[5 * C + row];
+                            rf.x = rf.y = tab[3 * C + row];
                             tc::tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 16; j += 4) {
@@ -602,7 +617,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 const uint4 *xd = reinterpret_cast<const uint4 *>(
                     static_cast<const __nv_bfloat16 *>(p.xd) + grow * D + z0);
                 const bool dots = p.dot && in;
-                const float a = tab[row], g = tab[2 * C + row];
+                const float a = tab[row], g = REV ? tab[7 * C + row] : 1.f;
                 float d = 0.f;
                 if (!wait(b_o, ph)) break;
                 tc::fence_after_sync();
@@ -627,7 +642,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        vi[j] = fmaf(p.scale, vi[j], vs[j]) * (REV ? g : 1.f);
+                        vi[j] = fmaf(p.scale, vi[j], vs[j]) * g;
                     // staged where the chunk's z was (its last reader, OI, has completed)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
@@ -640,7 +655,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 if (dots) p.dot[(size_t)(zh * 2 + half) * p.BH * p.T + grow] = d;
                 fence_proxy_async_smem();
                 arrive(b_out + 8 * sg);
-                arrive(b_tfree + 8 * sg);
+                arrive(b_tfree + 8 * ts);
             }
         }
     } else {
@@ -661,8 +676,8 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         float dec = 1.f;   // the segment's decay so far
         bool ok = true;
         for (int it = 0; it < NL; ++it) {
-            const int sg = it & 1, ph = it & 1, n = chunk(it);
-            const float *tab = s_tab + sg * L::TABF;
+            const int sg = it & 1, ph = it & 1, ts = it % kLtTabs, n = chunk(it);
+            const float *tab = s_tab + ts * L::TABF;
             if (OUT) {
                 // the state before the chunk as the B operand, rows of y, two bf16 parts
 #pragma unroll
@@ -681,7 +696,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 fence_proxy_async_smem();
                 arrive(b_s);
             }
-            ok = wait(b_w + 8 * sg, (it >> 1) & 1) && wait(b_z + 8 * sg, (it >> 1) & 1);
+            ok = wait(b_w + 8 * ts, (it / kLtTabs) & 1) && wait(b_z + 8 * sg, (it >> 1) & 1);
             if (!ok) break;
             // (u z) in three bf16 parts, at the places of z
 #pragma unroll 1
@@ -706,7 +721,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             }
             fence_proxy_async_smem();
             arrive(b_parts);
-            const float b = tab[9 * C];
+            const float b = tab[8 * C];
             if (OUT && p.states) {
                 float *dst = p.states + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
 #pragma unroll
@@ -739,7 +754,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 for (int j = 0; j < 16; ++j) st[h + j] = fmaf(b, st[h + j], w[j] + v[j]);
             }
             tc::fence_before_sync();
-            arrive(b_tfree + 8 * sg);
+            arrive(b_tfree + 8 * ts);
         }
         float *dst = OUT ? (seg == (REV ? 0 : p.S - 1) ? p.last : nullptr) : p.agg;
         if (ok && dst) {
