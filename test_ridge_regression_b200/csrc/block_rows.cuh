@@ -14,8 +14,11 @@
 // bounds them.  A row is spread over D * sizeof(T) / 16 neighbouring lanes, 16
 // bytes a lane, so a warp's loads and stores are whole rows (64 to 512 bytes
 // each) whichever of the two layouts a side has, and a row's sum is a few
-// shuffles.  Threads walk the head-major side in order (t fastest).  All sums
-// are fp32; the gradients of what is shared by many rows (biases, w, skip) are
+// shuffles.  A block takes a tile of tokens x heads (8 heads where there are as
+// many tokens), so that it touches kilobytes in a run on either side, and finds
+// the tile with one division; with a division a row, in 64 bits, index arithmetic
+// bounded the kernels (block_in of bf16 B8 T2048 H8 D128: 88 us).  All sums are
+// fp32; the gradients of what is shared by many rows (biases, w, skip) are
 // summed per block and then over the blocks in a fixed order, so results do not
 // depend on scheduling.
 #pragma once
@@ -80,6 +83,41 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 __device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-x)); }
+// For rows that are rounded to bf16 in the end the hardware's exponential and quotient
+// (relative error 2^-20) do.
+template <typename T>
+__device__ __forceinline__ float sigmoid_row(float x) {
+    if constexpr (sizeof(T) == 2) return __fdividef(1.f, 1.f + __expf(-x));
+    return sigmoid_f(x);
+}
+
+// Tile of a block of R rows: 2^tb tokens x R / 2^tb slots; tiles count tokens first.
+struct RowTile {
+    int tb;             // log2 of the tile's tokens
+    unsigned tcount;    // tiles along t
+    unsigned scount;    // tiles along the slots
+};
+// Row i of the block's tile; false past the end.
+struct SlotRow {
+    int b, slot, t;
+    bool in;
+};
+struct TileAt {
+    int b, s0, t0;
+};
+template <int R>
+__device__ __forceinline__ TileAt tile_at(const RowTile &g) {
+    const unsigned q = blockIdx.x / g.tcount, b = q / g.scount;
+    return {(int)b, (int)((q - b * g.scount) * (R >> g.tb)), (int)((blockIdx.x - q * g.tcount) << g.tb)};
+}
+__device__ __forceinline__ SlotRow tile_row(const RowTile &g, const TileAt &a, int i, int T, int slots) {
+    SlotRow s;
+    s.b = a.b;
+    s.t = a.t0 + (i & ((1 << g.tb) - 1));
+    s.slot = a.s0 + (i >> g.tb);
+    s.in = s.t < T && s.slot < slots;
+    return s;
+}
 
 // ---------------------------------------------------------------------------
 // Before the layer
@@ -91,22 +129,10 @@ struct BlockInArgs {
     int B, T, H, Hk;
     float eps;
     unsigned row_blocks;   // blocks of the row part; the rest do the gates
+    RowTile tile;
 };
 
-// Row index -> (b, slot, t), slots 0..H-1 queries, then Hk keys, then Hk values,
-// t fastest.
-struct SlotRow {
-    int b, slot, t;
-};
-__device__ __forceinline__ SlotRow slot_row(size_t r, int T, int slots) {
-    SlotRow s;
-    const size_t bs = r / (unsigned)T;
-    s.t = (int)(r - bs * (unsigned)T);
-    s.b = (int)(bs / (unsigned)slots);
-    s.slot = (int)(bs - (size_t)s.b * (unsigned)slots);
-    return s;
-}
-
+// Slots: 0..H-1 queries, then Hk keys, then Hk values.
 // grid: row_blocks blocks of rows (RPT rows a lane group), then ceil(B*H*T / 256)
 // blocks of gates.
 template <typename T, int D, int RPT>
@@ -139,19 +165,17 @@ k_block_in(const BlockInArgs a, T *__restrict__ qo, T *__restrict__ ko, T *__res
         }
         return;
     }
-    const size_t rows = (size_t)a.B * slots * a.T;
-    const int lane = threadIdx.x % LPR, rep = a.H / a.Hk;
-    const size_t r0 = (size_t)blockIdx.x * (GROUPS * RPT) + threadIdx.x / LPR;
+    const int lane = threadIdx.x % LPR, rep = a.H / a.Hk, grp = threadIdx.x / LPR;
+    const TileAt at = tile_at<GROUPS * RPT>(a.tile);
+    const int len = a.lengths ? min(a.lengths[at.b], a.T) : a.T;
     float x[RPT][V::N];
     // every load of the group's rows goes out before the first sum
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
-        const size_t r = r0 + (size_t)j * GROUPS;
+        const SlotRow s = tile_row(a.tile, at, grp + j * GROUPS, a.T, slots);
 #pragma unroll
         for (int i = 0; i < V::N; ++i) x[j][i] = 0.f;
-        if (r >= rows) continue;
-        const SlotRow s = slot_row(r, a.T, slots);
-        if (a.lengths && s.t >= a.lengths[s.b]) continue;
+        if (!s.in || s.t >= len) continue;
         const StridedRows &in = s.slot < a.H ? a.q : s.slot < a.H + a.Hk ? a.k : a.v;
         const int h = s.slot < a.H ? s.slot : (s.slot - a.H) % a.Hk;
         V::load(static_cast<const T *>(in.ptr) + s.b * in.sb + s.t * in.st + h * in.sh +
@@ -159,13 +183,12 @@ k_block_in(const BlockInArgs a, T *__restrict__ qo, T *__restrict__ ko, T *__res
     }
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
-        const size_t r = r0 + (size_t)j * GROUPS;
+        const SlotRow s = tile_row(a.tile, at, grp + j * GROUPS, a.T, slots);
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < V::N; ++i) ss = fmaf(x[j][i], x[j][i], ss);
         ss = row_sum<LPR>(ss);
-        if (r >= rows) continue;
-        const SlotRow s = slot_row(r, a.T, slots);
+        if (!s.in) continue;
         if (s.slot < a.H + a.Hk) {
             const float rn = rsqrtf(ss + a.eps);
 #pragma unroll
@@ -204,8 +227,16 @@ k_block_in_grad(const BlockInArgs a, const BlockInGrad g) {
         const float bb = a.beta_bias ? a.beta_bias[h] : 0.f;
         const float gb = a.gate_bias ? a.gate_bias[h] : 0.f;
         float sb = 0.f, sg = 0.f;
-        for (size_t e = e0 + threadIdx.x; e < e1; e += kRowThreads) {
-            const size_t b = e / (unsigned)a.T, t = e - b * (unsigned)a.T;
+        // token e of the head's run, its (b, t) carried along
+        const size_t eb = (e0 + threadIdx.x) / (unsigned)a.T;
+        unsigned t = (unsigned)(e0 + threadIdx.x - eb * (unsigned)a.T);
+        size_t b = eb;
+        for (size_t e = e0 + threadIdx.x; e < e1; e += kRowThreads, t += kRowThreads) {
+            if (t >= (unsigned)a.T) {
+                const unsigned q = t / (unsigned)a.T;
+                b += q;
+                t -= q * (unsigned)a.T;
+            }
             const bool ok = !a.lengths || (int)t < a.lengths[b];
             const size_t src = (b * a.H + h) * a.T + t, dst = e * a.H + h;
             float d = 0.f, dg = 0.f;
@@ -242,18 +273,16 @@ k_block_in_grad(const BlockInArgs a, const BlockInGrad g) {
         }
         return;
     }
-    const size_t rows = (size_t)a.B * slots * a.T;
-    const int rep = a.H / a.Hk;
-    const size_t r0 = (size_t)blockIdx.x * (GROUPS * RPT) + threadIdx.x / LPR;
+    const int rep = a.H / a.Hk, grp = threadIdx.x / LPR;
+    const TileAt at = tile_at<GROUPS * RPT>(a.tile);
+    const int len = a.lengths ? min(a.lengths[at.b], a.T) : a.T;
     float x[RPT][V::N], dy[RPT][V::N];
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
-        const size_t r = r0 + (size_t)j * GROUPS;
+        const SlotRow s = tile_row(a.tile, at, grp + j * GROUPS, a.T, slots);
 #pragma unroll
         for (int i = 0; i < V::N; ++i) x[j][i] = dy[j][i] = 0.f;
-        if (r >= rows) continue;
-        const SlotRow s = slot_row(r, a.T, slots);
-        if (a.lengths && s.t >= a.lengths[s.b]) continue;
+        if (!s.in || s.t >= len) continue;
         const bool is_q = s.slot < a.H, unit = s.slot < a.H + a.Hk;
         const int h = is_q ? s.slot : (s.slot - a.H) % a.Hk;
         if (unit) {
@@ -273,7 +302,7 @@ k_block_in_grad(const BlockInArgs a, const BlockInGrad g) {
     }
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
-        const size_t r = r0 + (size_t)j * GROUPS;
+        const SlotRow s = tile_row(a.tile, at, grp + j * GROUPS, a.T, slots);
         float ss = 0.f, xd = 0.f;
 #pragma unroll
         for (int i = 0; i < V::N; ++i) {
@@ -282,8 +311,7 @@ k_block_in_grad(const BlockInArgs a, const BlockInGrad g) {
         }
         ss = row_sum<LPR>(ss);
         xd = row_sum<LPR>(xd);
-        if (r >= rows) continue;
-        const SlotRow s = slot_row(r, a.T, slots);
+        if (!s.in) continue;
         const bool is_q = s.slot < a.H, unit = s.slot < a.H + a.Hk;
         if (unit) {
             const float rn = rsqrtf(ss + a.eps), c = rn * rn * xd;   // r (dy - r x (r x . dy))
@@ -327,6 +355,7 @@ struct BlockOutArgs {
     const float *w, *skip;     // [D]; [H], non-null exactly when v is
     int B, T, H;
     float eps;
+    RowTile tile;              // (forward)
 };
 
 template <typename T, int D, int RPT>
@@ -334,21 +363,20 @@ __global__ void __launch_bounds__(kRowThreads)
 k_block_out(const BlockOutArgs a, T *__restrict__ y) {
     using V = Vec16<T>;
     constexpr int LPR = D / V::N, GROUPS = kRowThreads / LPR;
-    const size_t rows = (size_t)a.B * a.H * a.T;
-    const int lane = threadIdx.x % LPR;
-    const size_t r0 = (size_t)blockIdx.x * (GROUPS * RPT) + threadIdx.x / LPR;
+    const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+    const TileAt at = tile_at<GROUPS * RPT>(a.tile);
     float w[V::N];
 #pragma unroll
     for (int i = 0; i < V::N; ++i) w[i] = a.w[lane * V::N + i];
     float u[RPT][V::N], z[RPT][V::N];
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
-        const size_t r = r0 + (size_t)j * GROUPS;
+        const SlotRow s = tile_row(a.tile, at, grp + j * GROUPS, a.T, a.H);
 #pragma unroll
         for (int i = 0; i < V::N; ++i) u[j][i] = z[j][i] = 0.f;
-        if (r >= rows) continue;
+        if (!s.in) continue;
+        const size_t r = ((size_t)s.b * a.H + s.slot) * a.T + s.t;
         V::load(static_cast<const T *>(a.o) + r * D + lane * V::N, u[j]);
-        const SlotRow s = slot_row(r, a.T, a.H);
         if (a.z.ptr)
             V::load(static_cast<const T *>(a.z.ptr) + s.b * a.z.sb + s.t * a.z.st + s.slot * a.z.sh +
                         lane * V::N, z[j]);
@@ -362,18 +390,17 @@ k_block_out(const BlockOutArgs a, T *__restrict__ y) {
     }
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
-        const size_t r = r0 + (size_t)j * GROUPS;
+        const SlotRow s = tile_row(a.tile, at, grp + j * GROUPS, a.T, a.H);
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < V::N; ++i) ss = fmaf(u[j][i], u[j][i], ss);
         ss = row_sum<LPR>(ss);
-        if (r >= rows) continue;
-        const SlotRow s = slot_row(r, a.T, a.H);
+        if (!s.in) continue;
         const float rn = rsqrtf(ss * (1.f / D) + a.eps);
 #pragma unroll
         for (int i = 0; i < V::N; ++i) {
             u[j][i] *= rn * w[i];
-            if (a.z.ptr) u[j][i] *= z[j][i] * sigmoid_f(z[j][i]);
+            if (a.z.ptr) u[j][i] *= z[j][i] * sigmoid_row<T>(z[j][i]);
         }
         V::store(y + (((size_t)s.b * a.T + s.t) * a.H + s.slot) * D + lane * V::N, u[j]);
     }
@@ -407,25 +434,35 @@ k_block_out_grad(const BlockOutArgs a, const BlockOutGrad g) {
     }
     // every lane of a warp runs the same number of rounds: the row sums are shuffles
     // over the whole warp
-    const size_t rounds = (e1 - e0 + GROUPS - 1) / GROUPS;
-    for (size_t k = 0; k < rounds; ++k) {
-        const size_t e = e0 + k * GROUPS + grp;
+    const int rounds = (int)((e1 - e0 + GROUPS - 1) / GROUPS);
+    size_t b = (e0 + grp) / (unsigned)a.T;
+    unsigned t = (unsigned)(e0 + grp - b * (unsigned)a.T);
+    for (int k = 0; k < rounds; ++k, t += GROUPS) {
+        if (t >= (unsigned)a.T) {
+            const unsigned q = t / (unsigned)a.T;
+            b += q;
+            t -= q * (unsigned)a.T;
+        }
+        const size_t e = e0 + (size_t)k * GROUPS + grp, ec = b * (unsigned)a.T + t;
         const bool in = e < e1;
-        const size_t ec = in ? e : e0;
-        const size_t b = ec / (unsigned)a.T, t = ec - b * (unsigned)a.T;
         const size_t hm = ((b * a.H + h) * a.T + t) * D + lane * V::N;
         const size_t tm = (ec * a.H + h) * D + lane * V::N;
         float u[V::N], v[V::N], z[V::N], dy[V::N];
-        V::load(static_cast<const T *>(a.o) + hm, u);
-        V::load(static_cast<const T *>(g.dy) + tm, dy);
+        if (in) {
+            V::load(static_cast<const T *>(a.o) + hm, u);
+            V::load(static_cast<const T *>(g.dy) + tm, dy);
+            if (a.v) V::load(static_cast<const T *>(a.v) + hm, v);
+            if (a.z.ptr)
+                V::load(static_cast<const T *>(a.z.ptr) + b * a.z.sb + t * a.z.st + h * a.z.sh +
+                            lane * V::N, z);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V::N; ++i) u[i] = v[i] = z[i] = dy[i] = 0.f;
+        }
         if (a.v) {
-            V::load(static_cast<const T *>(a.v) + hm, v);
 #pragma unroll
             for (int i = 0; i < V::N; ++i) u[i] = fmaf(sk, v[i], u[i]);
         }
-        if (a.z.ptr)
-            V::load(static_cast<const T *>(a.z.ptr) + b * a.z.sb + t * a.z.st + h * a.z.sh +
-                        lane * V::N, z);
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < V::N; ++i) ss = fmaf(u[i], u[i], ss);
@@ -435,14 +472,14 @@ k_block_out_grad(const BlockOutArgs a, const BlockOutGrad g) {
         for (int i = 0; i < V::N; ++i) {
             u[i] *= rn;   // n
             if (a.z.ptr) {
-                const float sg = sigmoid_f(z[i]);
-                // d silu(z) / dz = s (1 + z (1 - s)), with 1 - s = sigmoid(-z)
-                const float dsil = sg * fmaf(z[i], sigmoid_f(-z[i]), 1.f);
+                const float sg = sigmoid_row<T>(z[i]);
+                // d silu(z) / dz = s (1 + z (1 - s)); where 1 - s cancels, it is added to 1
+                const float dsil = sg * fmaf(z[i], 1.f - sg, 1.f);
                 const float dyi = dy[i];
                 dy[i] = dyi * (z[i] * sg);
                 z[i] = dyi * u[i] * w[i] * dsil;
             }
-            if (in) dw[i] = fmaf(dy[i], u[i], dw[i]);
+            dw[i] = fmaf(dy[i], u[i], dw[i]);   // (rows past the end are zeros)
             dy[i] *= w[i];   // dn
             dot = fmaf(dy[i], u[i], dot);
         }

@@ -336,8 +336,8 @@ static int rows_ok(int B, int T, int H, int Hk, int D, gka_dtype dt, float eps) 
     if (H > 0 && (Hk == 0 || H % Hk)) return GKA_ERR_INVALID_ARG;
     if (!supported_d(D)) return GKA_ERR_UNSUPPORTED;
     if (H > 65535) return GKA_ERR_UNSUPPORTED;
-    // blocks of 32 to 256 rows each, in one grid dimension
-    if ((double)B * T * ((double)H + 2.0 * Hk) > 3e10) return GKA_ERR_UNSUPPORTED;
+    // blocks in one grid dimension
+    if ((double)B * T * ((double)H + 2.0 * Hk) > 2e9) return GKA_ERR_UNSUPPORTED;
     return GKA_OK;
 }
 
@@ -354,10 +354,19 @@ static int out_blocks(int B, int T, int H, int D, gka_dtype dt) {
     return (int)std::max<size_t>(1, std::min(rounds, most));
 }
 
+// Tiles of R rows over B x slots x T: 8 slots by R / 8 tokens, or fewer tokens and more
+// slots where the sequences are short.  Returns their number.
+static size_t row_tiles(int R, int B, int T, int slots, RowTile *g) {
+    int tb = 0;
+    while ((1 << tb) < T && (1 << tb) < R / 8) ++tb;
+    g->tb = tb;
+    g->tcount = (unsigned)(((size_t)T + (1u << tb) - 1) >> tb);
+    g->scount = (unsigned)((slots + (R >> tb) - 1) / (R >> tb));
+    return (size_t)B * g->scount * g->tcount;
+}
 template <typename T, int D>
-static size_t row_blocks(size_t rows, int rpt) {
-    const size_t per = (size_t)kRowThreads / (D / Vec16<T>::N) * rpt;
-    return (rows + per - 1) / per;
+constexpr int rows_per_block(int rpt) {
+    return kRowThreads / (D / Vec16<T>::N) * rpt;
 }
 
 }  // namespace gka
@@ -505,7 +514,7 @@ int gka_block_in_forward(const gka_strided *q, const gka_strided *k, const gka_s
     return by_type(dt, D, [&](auto tag, auto d) {
         using Tin = decltype(tag);
         constexpr int DD = decltype(d)::value, RPT = 4;
-        a.row_blocks = (unsigned)row_blocks<Tin, DD>((size_t)B * T * (H + 2 * Hk), RPT);
+        a.row_blocks = (unsigned)row_tiles(rows_per_block<Tin, DD>(RPT), B, T, H + 2 * Hk, &a.tile);
         const size_t gates = (n + kRowThreads - 1) / kRowThreads;
         ProfScope ps(GKA_KERNEL_BLOCK_ROWS, s);
         k_block_in<Tin, DD, RPT><<<(unsigned)(a.row_blocks + gates), kRowThreads, 0, s>>>(
@@ -566,7 +575,7 @@ int gka_block_in_backward(const gka_strided *q, const gka_strided *k,
     return by_type(dt, D, [&](auto tag, auto d) {
         using Tin = decltype(tag);
         constexpr int DD = decltype(d)::value, RPT = 2;
-        a.row_blocks = (unsigned)row_blocks<Tin, DD>((size_t)B * T * (H + 2 * Hk), RPT);
+        a.row_blocks = (unsigned)row_tiles(rows_per_block<Tin, DD>(RPT), B, T, H + 2 * Hk, &a.tile);
         {
             ProfScope ps(GKA_KERNEL_BLOCK_ROWS, s);
             k_block_in_grad<Tin, DD, RPT>
@@ -601,7 +610,8 @@ int gka_block_out_forward(const void *o, const void *v, const gka_strided *z, co
         using Tin = decltype(tag);
         constexpr int DD = decltype(d)::value, RPT = 2;
         ProfScope ps(GKA_KERNEL_BLOCK_ROWS, s);
-        k_block_out<Tin, DD, RPT><<<(unsigned)row_blocks<Tin, DD>(n, RPT), kRowThreads, 0, s>>>(
+        const size_t blocks = row_tiles(rows_per_block<Tin, DD>(RPT), B, T, H, &a.tile);
+        k_block_out<Tin, DD, RPT><<<(unsigned)blocks, kRowThreads, 0, s>>>(
             a, static_cast<Tin *>(y));
         return check_launch();
     });

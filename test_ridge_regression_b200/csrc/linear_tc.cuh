@@ -348,15 +348,6 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         lt_expect(b_z + 8 * st, L::HALF);
         tma_load_3d(sm + L::Z + st * L::HALF, &A.z, zh * kLtZN, chunk(it) * C, bh, b_z + 8 * st);
     };
-    if (tid == kIssuer) {
-        load_z(0);
-        load_y(0);
-        if (OUT) load_x(0);
-        if (NL > 1) {
-            load_z(1);
-            load_y(1);
-        }
-    }
     if (warp == 0) {
         tc::tmem_alloc(tbase, 512);
         tc::tmem_relinquish();
@@ -366,9 +357,20 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     tc::fence_after_sync();
     // all 512 columns: they begin at 0
     constexpr uint32_t tmem = 0;
-    if (*tbase != tmem || (sb & 1023u)) {
+    if (*tbase != tmem || (sb & 1023u)) {   // what the constants rest on; nothing is in flight yet
         if (tid == 0) atomicExch(timeout_flag, 1);
-        asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
+        __syncthreads();
+        if (warp == 0) tc::tmem_dealloc(*tbase, 512);
+        return;
+    }
+    if (tid == kIssuer) {
+        load_z(0);
+        load_y(0);
+        if (OUT) load_x(0);
+        if (NL > 1) {
+            load_z(1);
+            load_y(1);
+        }
     }
     // TMEM columns; the bf16 weighted scores of each half of the columns lie over its scores
     constexpr uint32_t kP = 0, kOI = 128, kOS = 192, kDS = 256, kX = 448;
@@ -381,6 +383,34 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     };
     auto wait = [&](uint32_t bar, uint32_t parity) {   // the whole warp, one outcome
         return __all_sync(0xffffffffu, lt_wait_call(bar, parity, abort)) != 0;
+    };
+
+    // (u z) in three bf16 parts, at the places of z: two (OUT: both groups share the rows) or
+    // four 16-byte items a thread
+    auto parts = [&](const float *tab, int sg) {
+        constexpr int kStep = kLtGroup;
+        const int first = tid - kLtGroup;
+#pragma unroll 1
+        for (int item = first; item < 1024; item += kStep) {   // row item / 8
+            const uint4 w4 = *reinterpret_cast<const uint4 *>(sm + L::Z + sg * L::HALF + item * 16);
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+            const float u = tab[C + (item >> 3)];
+            uint32_t a[4], b[4], c[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float2 y = __fmul2_rn(bf16x2_f2(w[e]), make_float2(u, u));
+                a[e] = f2_bf16x2(y);
+                y = f2_rest(y, a[e]);
+                b[e] = f2_bf16x2(y);
+                c[e] = f2_bf16x2(f2_rest(y, b[e]));
+            }
+            uint8_t *dst = sm + L::PARTS + item * 16;
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
+            *reinterpret_cast<uint4 *>(dst + L::HALF) = make_uint4(b[0], b[1], b[2], b[3]);
+            *reinterpret_cast<uint4 *>(dst + 2 * L::HALF) = make_uint4(c[0], c[1], c[2], c[3]);
+        }
+        fence_proxy_async_smem();
+        arrive(b_parts);
     };
 
     if (warp == 16) {
@@ -420,7 +450,13 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             }
             return true;
         };
+        int loads_x = OUT;   // begun
         bool ok = !OUT || (copy_x(0) && issue_p(0));
+        if (OUT && ok && NL > 1) {
+            ok = wait(b_xfree, 0);
+            if (ok && elect_one()) load_x(1);
+            loads_x += ok;
+        }
 #pragma unroll 1
         for (int it = 0; ok && it < NL; ++it) {
             const int st = it & 1, ph = it & 1;
@@ -450,7 +486,10 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 lt_commit(b_ds);
             }
             if (OUT) {
-                ok = wait(b_pb, ph);
+                // x of the next chunk into TMEM once this one's P and OS have read it there, while
+                // the weighted scores are formed
+                if (it + 1 < NL) ok = wait(b_os, ph) && copy_x(it + 1);
+                ok = ok && wait(b_pb, ph);
                 if (!ok) break;
                 tc::fence_after_sync();
                 if (elect_one()) {
@@ -461,16 +500,22 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                                     kk > 0);
                     lt_commit(b_o);
                 }
-                // x of the next chunk into TMEM once this one's P and OS have read it there; its
-                // scores once OI has read the weighted ones, whose columns they take
-                if (it + 1 < NL) ok = wait(b_os, ph) && copy_x(it + 1) && wait(b_o, ph) && issue_p(it + 1);
+                if (it + 2 < NL) {   // its stage is free again
+                    ok = wait(b_xfree, ph ^ 1);
+                    if (!ok) break;
+                    if (elect_one()) load_x(it + 2);
+                    ++loads_x;
+                }
+                // the next chunk's scores once OI has read the weighted ones, whose columns they take
+                if (it + 1 < NL) ok = wait(b_o, ph) && issue_p(it + 1);
             }
         }
         if (!ok && elect_one()) {
-            // a wait gave up: flag it, then drain this thread's products
+            // a wait gave up: flag it, then drain this thread's products and copies
             atomicExch(timeout_flag, 1);
             lt_commit(b_fin);
             lt_drain(b_fin, 0);
+            if (loads_x) lt_drain(b_x, (loads_x - 1) & 1);
         }
         __syncwarp();
     } else if (warp == 17 || warp == 18) {
@@ -506,17 +551,11 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     } else if (warp == 19) {
         // ---- loads into freed stages, rows out ----
         if (lane == 0) {
-            int loads_x = OUT, loads_y[2] = {1, NL > 1}, loads_z[2] = {1, NL > 1};   // begun
+            int loads_y[2] = {1, NL > 1}, loads_z[2] = {1, NL > 1};   // begun
             bool ok = true;
 #pragma unroll 1
             for (int it = 0; it < NL; ++it) {
                 const int st = it & 1, ph = it & 1;
-                if (OUT && it + 1 < NL) {   // x(it) is in TMEM
-                    ok = lt_wait(b_xfree, ph, abort);
-                    if (!ok) break;
-                    load_x(it + 1);
-                    ++loads_x;
-                }
                 if (it + 2 < NL) {   // y's readers, P(it) and DS(it), are done
                     ok = lt_wait(OUT ? b_o : b_ds, ph, abort);
                     if (!ok) break;
@@ -537,7 +576,6 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             }
             if (OUT) tc::bulk_wait0();
             if (!ok) {   // a wait gave up: drain this thread's copies
-                if (loads_x) lt_drain(b_x, (loads_x - 1) & 1);
                 for (int i = 0; i < 2; ++i) {
                     if (loads_y[i]) lt_drain(b_y + 8 * i, (loads_y[i] - 1) & 1);
                     if (loads_z[i]) lt_drain(b_z + 8 * i, (loads_z[i] - 1) & 1);
@@ -698,29 +736,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             }
             ok = wait(b_w + 8 * ts, (it / kLtTabs) & 1) && wait(b_z + 8 * sg, (it >> 1) & 1);
             if (!ok) break;
-            // (u z) in three bf16 parts, at the places of z
-#pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t item = gt + j * kLtGroup, off = item * 16;   // row item / 8
-                const uint4 w4 = *reinterpret_cast<const uint4 *>(sm + L::Z + sg * L::HALF + off);
-                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-                const float u = tab[C + (item >> 3)];
-                uint32_t a[4], b[4], c[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float2 y = __fmul2_rn(bf16x2_f2(w[e]), make_float2(u, u));
-                    a[e] = f2_bf16x2(y);
-                    y = f2_rest(y, a[e]);
-                    b[e] = f2_bf16x2(y);
-                    c[e] = f2_bf16x2(f2_rest(y, b[e]));
-                }
-                uint8_t *dst = sm + L::PARTS + off;
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
-                *reinterpret_cast<uint4 *>(dst + L::HALF) = make_uint4(b[0], b[1], b[2], b[3]);
-                *reinterpret_cast<uint4 *>(dst + 2 * L::HALF) = make_uint4(c[0], c[1], c[2], c[3]);
-            }
-            fence_proxy_async_smem();
-            arrive(b_parts);
+            parts(tab, sg);
             const float b = tab[8 * C];
             if (OUT && p.states) {
                 float *dst = p.states + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;

@@ -8,6 +8,7 @@ There is no fallback: if the library is missing or a call fails, it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 from pathlib import Path
 
 import torch
@@ -375,18 +376,14 @@ def gka_backward(q, k, v, beta, dout, a: float, r: int, chunk: int = 32, *, gate
 # the stream that is current at the call, as torch's allocator has it: with a
 # `stream` of one's own, pass them, or call under `torch.cuda.stream(stream)`.
 # ---------------------------------------------------------------------------
-def _same_device(*ts):
+def _device_of(first, *rest):
     """The one CUDA device of the tensors given (None: not given)."""
-    dev = None
-    for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("tensors must be on one device")
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors must be on one CUDA device")
     return dev
 
 
@@ -413,16 +410,25 @@ def _apart(*outs):
 def _invoke(fn, dev, stream, *args):
     """Calls a C entry point whose last argument is the stream, on device ``dev``."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
     elif stream.device != dev:
         raise ValueError("stream must belong to the tensors' device")
+    else:
+        raw = stream.cuda_stream
     call = getattr(_lib(), fn)
     if torch.cuda.current_device() == dev.index:
-        rc = call(*args, stream.cuda_stream)
+        rc = call(*args, raw)
     else:
         with torch.cuda.device(dev):
-            rc = call(*args, stream.cuda_stream)
-    _check(fn, rc)
+            rc = call(*args, raw)
+    if rc != 0:
+        raise GkaError(fn, rc)
+
+
+@functools.lru_cache(maxsize=1024)
+def _query(fn, *sizes):
+    """A workspace query of the library (a function of the sizes alone)."""
+    return int(getattr(_lib(), fn)(*sizes))
 
 
 def _p(t):
@@ -444,7 +450,7 @@ def _nbytes(t):
 def linear_workspace_bytes(B, H, T, D, dtype=torch.bfloat16, *, backward=False) -> int:
     """Workspace bytes of gka_linear_forward (or gka_linear_backward); may be 0."""
     fn = "gka_linear_backward_workspace_bytes" if backward else "gka_linear_forward_workspace_bytes"
-    return int(getattr(_lib(), fn)(B, H, T, D, _DT[dtype]))
+    return _query(fn, B, H, T, D, _DT[dtype])
 
 
 def _linear_inputs(q, k, v, beta, gate, shape):
@@ -463,7 +469,7 @@ def gka_linear_forward(q, k, v, beta, *, gate=None, scale=1.0, initial_state=Non
     (see include/gka.h).  q, k, v: [B, H, T, D] fp32 or bf16 CUDA tensors, any T; beta
     (and the optional gate): [B, H, T] fp32; initial_state, final_state (written; may be
     initial_state): fp32 [B, H, D, D].  Returns o (shape and dtype of v)."""
-    dev = _same_device(q, k, v, beta, gate, initial_state, final_state, o, workspace)
+    dev = _device_of(q, k, v, beta, gate, initial_state, final_state, o, workspace)
     _dense(q, k, v, beta, gate, initial_state, final_state, o)
     B, H, T, D = q.shape
     dt = _linear_inputs(q, k, v, beta, gate, (B, H, T))
@@ -476,7 +482,7 @@ def gka_linear_forward(q, k, v, beta, *, gate=None, scale=1.0, initial_state=Non
         _apart(o, final_state)
         for t in (q, k, v, beta, gate, initial_state, workspace):
             _apart(o, t)
-    n = _lib().gka_linear_forward_workspace_bytes(B, H, T, D, dt)
+    n = _query("gka_linear_forward_workspace_bytes", B, H, T, D, dt)
     workspace = _scratch(n, workspace, dev)
     _invoke("gka_linear_forward", dev, stream, _p(q), _p(k), _p(v), _p(beta), _p(gate), _p(o), B, H,
             T, D, dt, scale, _p(initial_state), _p(final_state), _p(workspace), _nbytes(workspace))
@@ -486,7 +492,7 @@ def gka_linear_forward(q, k, v, beta, *, gate=None, scale=1.0, initial_state=Non
 def gka_linear_decode_step(state, q, k, v, beta, *, gate=None, scale=1.0, o=None, stream=None):
     """One token of the gated linear recurrence, in place on state [B, H, D, D] fp32;
     q, k, v: [B, H, D]; beta (and the optional gate): [B, H] fp32.  Returns o [B, H, D]."""
-    dev = _same_device(state, q, k, v, beta, gate, o)
+    dev = _device_of(state, q, k, v, beta, gate, o)
     _dense(state, q, k, v, beta, gate, o)
     B, H, D = q.shape
     dt = _linear_inputs(q, k, v, beta, gate, (B, H))
@@ -509,7 +515,7 @@ def gka_linear_backward(q, k, v, beta, dout, *, gate=None, scale=1.0, initial_st
     inputs' dtype; dfinal_state: optional gradient of the final state, fp32 [B, H, D, D].
     Returns a dict with dq, dk, dv (dtype of q), dbeta, with a gate dgate (fp32), and with
     an initial_state dstate (its gradient, fp32)."""
-    dev = _same_device(q, k, v, beta, gate, dout, initial_state, dfinal_state, workspace)
+    dev = _device_of(q, k, v, beta, gate, dout, initial_state, dfinal_state, workspace)
     _dense(q, k, v, beta, gate, dout, initial_state, dfinal_state)
     B, H, T, D = q.shape
     dt = _linear_inputs(q, k, v, beta, gate, (B, H, T))
@@ -522,7 +528,7 @@ def gka_linear_backward(q, k, v, beta, dout, *, gate=None, scale=1.0, initial_st
         out["dgate"] = torch.empty_like(gate)
     if initial_state is not None:
         out["dstate"] = torch.empty_like(initial_state)
-    n = _lib().gka_linear_backward_workspace_bytes(B, H, T, D, dt)
+    n = _query("gka_linear_backward_workspace_bytes", B, H, T, D, dt)
     workspace = _scratch(n, workspace, dev)
     _invoke("gka_linear_backward", dev, stream, _p(q), _p(k), _p(v), _p(beta), _p(gate), _p(dout),
             _p(initial_state), _p(dfinal_state), _p(out["dq"]), _p(out["dk"]), _p(out["dv"]),
@@ -568,7 +574,7 @@ def gka_block_in(q, k, v, beta_logit, *, gate_logit=None, beta_bias=None, gate_b
     dtype; beta_bias, gate_bias: [H] fp32; lengths: [B] int32, tokens past it are padding.
     Returns (q, k, v [B, H, T, D], beta [B, H, T] fp32, gate or None): the inputs of
     gka_forward_gated and gka_linear_forward."""
-    dev = _same_device(q, k, v, beta_logit, gate_logit, beta_bias, gate_bias, lengths)
+    dev = _device_of(q, k, v, beta_logit, gate_logit, beta_bias, gate_bias, lengths)
     B, T, H, Hk, D, dt, (sq, sk, sb, sg) = _block_in_args(q, k, beta_logit, gate_logit, beta_bias,
                                                           gate_bias, lengths)
     sv = _strided("v", v, q.dtype, (B, T, Hk, D))
@@ -587,7 +593,7 @@ def gka_block_in_backward(q, k, beta_logit, dq, dk, dv, dbeta, *, gate_logit=Non
     inputs' dtype, dbeta (and dgate exactly with gate_logit) [B, H, T] fp32.  Returns a dict
     with dq [B, T, H, D], dk, dv [B, T, Hk, D], dbeta_logit (dgate_logit) [B, T, H], and for
     each bias given dbeta_bias (dgate_bias) [H] fp32."""
-    dev = _same_device(q, k, beta_logit, gate_logit, dq, dk, dv, dbeta, dgate, beta_bias, gate_bias,
+    dev = _device_of(q, k, beta_logit, gate_logit, dq, dk, dv, dbeta, dgate, beta_bias, gate_bias,
                        lengths, workspace)
     B, T, H, Hk, D, dt, (sq, sk, sb, sg) = _block_in_args(q, k, beta_logit, gate_logit, beta_bias,
                                                           gate_bias, lengths)
@@ -607,7 +613,7 @@ def gka_block_in_backward(q, k, beta_logit, dq, dk, dv, dbeta, *, gate_logit=Non
     for n, t in (("dbeta_bias", beta_bias), ("dgate_bias", gate_bias)):
         if t is not None:
             out[n] = torch.empty_like(t)
-    n = _lib().gka_block_in_backward_workspace_bytes(B, T, H, Hk, D, dt)
+    n = _query("gka_block_in_backward_workspace_bytes", B, T, H, Hk, D, dt)
     workspace = _scratch(n, workspace, dev)
     _invoke("gka_block_in_backward", dev, stream, sq, sk, sb, sg, _p(beta_bias), _p(gate_bias),
             _p(lengths), _p(dq), _p(dk), _p(dv), _p(dbeta), _p(dgate), _p(out["dq"]), _p(out["dk"]),
@@ -633,7 +639,7 @@ def gka_block_out(o, w, *, z=None, v=None, skip=None, eps=1e-6, y=None, stream=N
     """After the layer (see include/gka.h): y = rmsnorm(o + skip_h v) w silu(z), token-major.
     o (and the layer's v): [B, H, T, D] fp32 or bf16; w: [D] fp32; skip: [H] fp32, with v;
     z: [B, T, H, D] at any strides with contiguous rows.  Returns y [B, T, H, D]."""
-    dev = _same_device(o, w, z, v, skip, y)
+    dev = _device_of(o, w, z, v, skip, y)
     B, H, T, D, dt, sz = _block_out_args(o, w, z, v, skip)
     if y is None:
         y = torch.empty(B, T, H, D, dtype=o.dtype, device=dev)
@@ -651,7 +657,7 @@ def gka_block_out_backward(o, w, dy, *, z=None, v=None, skip=None, eps=1e-6, wor
                            stream=None):
     """Gradients of gka_block_out from dy [B, T, H, D].  Returns a dict with do [B, H, T, D],
     dw [D] fp32; with z: dz [B, T, H, D]; with v and skip: dv [B, H, T, D], dskip [H] fp32."""
-    dev = _same_device(o, w, dy, z, v, skip, workspace)
+    dev = _device_of(o, w, dy, z, v, skip, workspace)
     B, H, T, D, dt, sz = _block_out_args(o, w, z, v, skip)
     _dense(dy)
     _need("dy", dy, (B, T, H, D), o.dtype)
@@ -660,7 +666,7 @@ def gka_block_out_backward(o, w, dy, *, z=None, v=None, skip=None, eps=1e-6, wor
         out["dz"] = torch.empty(B, T, H, D, dtype=o.dtype, device=dev)
     if v is not None:
         out["dv"], out["dskip"] = torch.empty_like(v), torch.empty_like(skip)
-    n = _lib().gka_block_out_backward_workspace_bytes(B, T, H, D, dt)
+    n = _query("gka_block_out_backward_workspace_bytes", B, T, H, D, dt)
     workspace = _scratch(n, workspace, dev)
     _invoke("gka_block_out_backward", dev, stream, _p(o), _p(v), sz, _p(w), _p(skip), _p(dy),
             _p(out["do"]), _p(out.get("dv")), _p(out.get("dz")), _p(out["dw"]), _p(out.get("dskip")),
