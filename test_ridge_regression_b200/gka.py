@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 from pathlib import Path
 
 import torch
@@ -37,12 +38,6 @@ _KERNEL_COUNT = 16
 
 class KernelTimes(ctypes.Structure):
     _fields_ = [("ms", ctypes.c_double * _KERNEL_COUNT), ("launches", ctypes.c_int * _KERNEL_COUNT)]
-
-
-class Strided(ctypes.Structure):
-    """gka_strided: rows [B, T, heads, D] (or scalars [B, T, heads]) at element strides."""
-    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_longlong),
-                ("stride_t", ctypes.c_longlong), ("stride_h", ctypes.c_longlong)]
 
 
 class WorkspaceLayout(ctypes.Structure):
@@ -100,7 +95,7 @@ def _lib():
         lib.gka_linear_backward.restype = i
         lib.gka_linear_decode_step.argtypes = [vp] * 7 + [i] * 4 + [f, vp]
         lib.gka_linear_decode_step.restype = i
-        rows = ctypes.POINTER(Strided)
+        rows = vp   # const gka_strided *: packed by _strided
         lib.gka_block_in_forward.argtypes = [rows] * 5 + [vp] * 8 + [i] * 6 + [f, vp]
         lib.gka_block_in_forward.restype = i
         lib.gka_block_in_backward_workspace_bytes.argtypes = [i] * 6
@@ -416,7 +411,7 @@ def _invoke(fn, dev, stream, *args):
     else:
         raw = stream.cuda_stream
     call = getattr(_lib(), fn)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         rc = call(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -537,17 +532,21 @@ def gka_linear_backward(q, k, v, beta, dout, *, gate=None, scale=1.0, initial_st
     return out
 
 
+_pack_strided = struct.Struct("Pqqq").pack   # gka_strided: pointer, strides of b, t, heads
+
+
 def _strided(name, t, dtype, shape):
     """gka_strided of a [B, T, heads(, D)] tensor with contiguous rows (None: NULL)."""
     if t is None:
         return None
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {str(dtype)[6:]} {list(shape)}")
-    if t.dim() == 4 and t.stride(3) != 1 and t.numel():
+    s = t.stride()
+    if len(s) == 4 and s[3] != 1 and t.numel():
         raise ValueError(f"{name} must have contiguous rows")
     # the stride of an axis of one is never used, whatever torch reports for it
-    sb, st, sh = (t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))
-    return ctypes.byref(Strided(t.data_ptr(), sb, st, sh))
+    return _pack_strided(t.data_ptr(), s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0,
+                         s[2] if shape[2] > 1 else 0)
 
 
 def _block_in_args(q, k, beta_logit, gate_logit, beta_bias, gate_bias, lengths):
@@ -578,8 +577,9 @@ def gka_block_in(q, k, v, beta_logit, *, gate_logit=None, beta_bias=None, gate_b
     B, T, H, Hk, D, dt, (sq, sk, sb, sg) = _block_in_args(q, k, beta_logit, gate_logit, beta_bias,
                                                           gate_bias, lengths)
     sv = _strided("v", v, q.dtype, (B, T, Hk, D))
-    qo, ko, vo = (torch.empty(B, H, T, D, dtype=q.dtype, device=dev) for _ in range(3))
-    beta = torch.empty(B, H, T, device=dev, dtype=torch.float32)
+    qo = torch.empty((B, H, T, D), dtype=q.dtype, device=dev)
+    ko, vo = torch.empty_like(qo), torch.empty_like(qo)
+    beta = torch.empty((B, H, T), device=dev, dtype=torch.float32)
     gate = torch.empty_like(beta) if gate_logit is not None or lengths is not None else None
     _invoke("gka_block_in_forward", dev, stream, sq, sk, sv, sb, sg, _p(beta_bias), _p(gate_bias),
             _p(lengths), _p(qo), _p(ko), _p(vo), _p(beta), _p(gate), B, T, H, Hk, D, dt, eps)

@@ -1,8 +1,8 @@
 """Gated linear recurrence and block rows without a GPU: the definitions the GPU tests
 hold the kernels to (gradients against central differences, the chunk form of dbeta
 against the adjoint recurrence), and the refusals of the C ABI and of the binding."""
-import ctypes
 import math
+import struct
 
 import pytest
 import torch
@@ -138,7 +138,7 @@ def test_linear_step_refusals(lib):
 
 
 def rows(gka, ptr=P, sb=64 * 64, st=64, sh=64):
-    return ctypes.byref(gka.Strided(ptr, sb, st, sh))
+    return struct.pack("Pqqq", ptr or 0, sb, st, sh)
 
 
 def test_block_in_refusals(lib):
