@@ -195,12 +195,12 @@ static int head_map(CUtensorMap *m, const void *base, int T, int BH) {
     return r == CUDA_SUCCESS ? GKA_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
-template <bool REV, bool OUT>
+template <bool REV>
 static int lin_tc_launch(const LinTcArgs &a, int passes, int prof, cudaStream_t s) {
     cudaError_t e;
     int *flag = nullptr;
     if (int rc = timeout_flag_ptr(&flag)) return rc;
-    auto kern = k_linear_tc<REV, OUT>;
+    auto kern = k_linear_tc<REV>;
     if ((e = set_smem(kern, LtSmem::bytes)) != cudaSuccess) return cuda_fail(e);
     const LinPass &p = a.pass[0].p;
     ProfScope ps(prof, s);
@@ -218,7 +218,16 @@ static int lin_tc_starts(LinTcArgs &a, const LinLayout &L, char *ws, const float
     }
     p.agg = reinterpret_cast<float *>(ws + L.agg);
     p.segdec = reinterpret_cast<float *>(ws + L.segdec);
-    if (int rc = lin_tc_launch<REV, false>(a, 1, prof, s)) return rc;
+    cudaError_t e;
+    int *flag = nullptr;
+    if (int rc = timeout_flag_ptr(&flag)) return rc;
+    auto kern = k_linear_agg_tc<REV>;
+    if ((e = set_smem(kern, LaSmem::bytes)) != cudaSuccess) return cuda_fail(e);
+    {
+        ProfScope ps(prof, s);
+        kern<<<dim3(2, p.BH, L.S), kLtThreads, LaSmem::bytes, s>>>(a.pass[0], flag);
+    }
+    if (int rc = check_launch()) return rc;
     ProfScope ps(prof, s);
     k_linear_scan<<<dim3(16, p.BH), 256, 0, s>>>(p.agg, p.segdec, init, L.S, 128 * 128, REV);
     p.start = p.agg;
@@ -239,7 +248,7 @@ static int lin_tc_forward(const LinCall &c, const LinLayout &L) {
     p.zy = 1;
     if (int rc = lin_tc_starts<false>(a, L, c.ws, c.init, GKA_KERNEL_LINEAR, c.s)) return rc;
     p.last = c.last;
-    return lin_tc_launch<false, true>(a, 1, GKA_KERNEL_LINEAR, c.s);
+    return lin_tc_launch<false>(a, 1, GKA_KERNEL_LINEAR, c.s);
 }
 
 static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
@@ -268,7 +277,7 @@ static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
     pf.xd = c.q;
     pf.dot = const_cast<float *>(w.p.zeta);
     pf.states = reinterpret_cast<float *>(c.ws + L.states);
-    if (int rc = lin_tc_launch<false, true>(f, 1, kProf, c.s)) return rc;
+    if (int rc = lin_tc_launch<false>(f, 1, kProf, c.s)) return rc;
     // dv and dk, backwards in time, in one launch
     LinTcArgs r = {};
     r.pass[0].x = k; r.pass[0].y = q; r.pass[0].z = d_o;
@@ -287,7 +296,7 @@ static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
     pv.xd = c.v;
     pv.dot = const_cast<float *>(w.p.eta);
     pv.last = c.dinit;
-    if (int rc = lin_tc_launch<true, true>(r, 2, kProf, c.s)) return rc;
+    if (int rc = lin_tc_launch<true>(r, 2, kProf, c.s)) return rc;
     w.q = q; w.k = k; w.v = v; w.d_o = d_o;
     w.p.beta = c.beta; w.p.gate = c.gate;
     w.p.dbeta = c.dbeta; w.p.dgate = c.dgate;

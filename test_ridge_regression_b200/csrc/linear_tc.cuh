@@ -54,10 +54,10 @@ namespace gka {
 constexpr int kLtC = 128;                       // tokens per chunk
 constexpr int kLtZN = 64;                       // columns of z a CTA owns
 constexpr int kLtGroup = 256;                   // threads of an arithmetic group (two)
-constexpr int kLtThreads = 2 * kLtGroup + 128;  // + issuer, two decay warps, store warp
+constexpr int kLtThreads = 2 * kLtGroup + 128;  // + two issuers, the decay warp, the loader
 constexpr int kLtTabs = 4;                      // stages of decay tables
 constexpr int kLtDots = 4, kLtFdots = 16;       // planes of dot and fdot partials per pass
-constexpr uint32_t kLtProbes = 1u << 20;
+constexpr uint32_t kLtProbes = 1u << 17;
 constexpr uint32_t kLtHintNs = 2000;            // a probe suspends its warp for up to this long
 
 struct LtSmem {
@@ -73,7 +73,7 @@ struct LtSmem {
     // less log2 of the gate, of the column; forward); then b
     static constexpr uint32_t TABF = 8 * kLtC + 4;
     static constexpr uint32_t BARS = TAB + kLtTabs * 4 * TABF;
-    static constexpr uint32_t TBASE = BARS + 8 * (16 + 2 * kLtTabs);      // TMEM base, abort flag
+    static constexpr uint32_t TBASE = BARS + 8 * (18 + 2 * kLtTabs);      // TMEM base, abort flag
     static constexpr uint32_t END = TBASE + 16;
     static constexpr size_t bytes = END + 1024;
 };
@@ -131,47 +131,42 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-// Bounded wait that also gives up once another role has (the word at shared address
-// `abort` set).  Barriers here are shared addresses: a register each, made where used.
-__device__ __forceinline__ bool lt_wait(uint32_t bar, uint32_t parity, uint32_t abort) {
-#pragma unroll 1
+// One probe of a barrier's phase (barriers are shared addresses here).
+__device__ __forceinline__ bool lt_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kLtHintNs)
+        : "memory");
+    return ok != 0;
+}
+// The rest of a bounded wait, which also gives up once another role has (the word at
+// shared address `abort` set).
+__device__ __noinline__ bool lt_wait_more(uint32_t bar, uint32_t parity, uint32_t abort) {
     for (uint32_t i = 0; i < kLtProbes; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(kLtHintNs)
-            : "memory");
-        if (ok) return true;
-        if ((i & 255) == 255) {
-            uint32_t a;
-            asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(a) : "r"(abort) : "memory");
-            if (a) break;
-        }
+        if (lt_try(bar, parity)) return true;
+        uint32_t a;
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(a) : "r"(abort) : "memory");
+        if (a) break;
     }
     asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
     return false;
 }
-// The same as a call: one copy of the code for the warps that mostly wait, which the
-// instruction caches keep.
-__device__ __noinline__ bool lt_wait_call(uint32_t bar, uint32_t parity, uint32_t abort) {
-    return lt_wait(bar, parity, abort);
+__device__ __forceinline__ bool lt_wait(uint32_t bar, uint32_t parity, uint32_t abort) {
+    return lt_try(bar, parity) || lt_wait_more(bar, parity, abort);
+}
+// By a whole warp, with one outcome.
+__device__ __forceinline__ bool lt_wait_warp(uint32_t bar, uint32_t parity, uint32_t abort) {
+    if (__all_sync(0xffffffffu, lt_try(bar, parity))) return true;
+    return __all_sync(0xffffffffu, lt_wait_more(bar, parity, abort)) != 0;
 }
 // After a time-out: a bounded wait for work in flight.
 __device__ __noinline__ void lt_drain(uint32_t bar, uint32_t parity) {
-    for (uint32_t i = 0; i < kLtProbes; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (ok) return;
-    }
+    for (uint32_t i = 0; i < kLtProbes; ++i)
+        if (lt_try(bar, parity)) return;
 }
 __device__ __forceinline__ void lt_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -221,9 +216,25 @@ __device__ __forceinline__ Log2Sum shfl(Log2Sum x, int src) {
     return {__shfl_sync(0xffffffffu, x.hi, src), __shfl_sync(0xffffffffu, x.lo, src)};
 }
 
+// Inclusive sums of the clamped log2 decays of a chunk's four blocks of 32 tokens, by one
+// warp (lane = token of every block; the blocks' scans run side by side).
+__device__ __forceinline__ void lt_scan(const float *bv, float log2_min, Log2Sum *l) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) l[j] = {fmaxf(log2f(bv[j]), log2_min), 0.f};
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const Log2Sum y = {__shfl_up_sync(0xffffffffu, l[j].hi, o), __shfl_up_sync(0xffffffffu, l[j].lo, o)};
+            if (lane >= o) l[j] = l[j] + y;
+        }
+    }
+}
+
 // Decay tables of one chunk by one warp; lane l holds tokens 32 j + l, whose beta and
-// gate are bv[j] and gv[j] (1 and 0 past the sequence's end).  Loops stay rolled: the
-// kernel's hot code has to share the instruction caches.
+// gate are bv[j] and gv[j] (1 and 0 past the sequence's end).  The second part is a loop:
+// the kernel's hot code has to share the instruction caches.
 template <bool REV>
 __device__ __forceinline__ void lt_tables(float *tab, const float *bv, const float *gv, float scale,
                                           float log2_min) {
@@ -231,54 +242,61 @@ __device__ __forceinline__ void lt_tables(float *tab, const float *bv, const flo
     float *ta_a = tab + lane, *ta_u = ta_a + kLtC, *ta_l = ta_u + kLtC, *ta_t = ta_l + kLtC,
           *ta_c = ta_t + kLtC, *ta_gm = ta_c + 3 * kLtC;
     const Log2Sum zero = {0.f, 0.f};
-    Log2Sum e0 = zero, e1 = zero, e2 = zero, end = zero;   // cumulative log at the ends of the blocks
-    float b0 = bv[0], b1 = bv[1], b2 = bv[2], b3 = bv[3];
-#pragma unroll 1
+    Log2Sum l[4], e[4], end = zero;   // e[b]: cumulative log at the end of block b
+    lt_scan(bv, log2_min, l);
+#pragma unroll
     for (int j = 0; j < 4; ++j) {
-        Log2Sum l = {fmaxf(log2f(b0), log2_min), 0.f};
-        b0 = b1;
-        b1 = b2;
-        b2 = b3;
-#pragma unroll 1
-        for (int o = 1; o < 32; o <<= 1) {
-            const Log2Sum y = {__shfl_up_sync(0xffffffffu, l.hi, o), __shfl_up_sync(0xffffffffu, l.lo, o)};
-            if (lane >= o) l = l + y;
-        }
-        ta_l[32 * j] = l.hi + l.lo;   // from the block's start
-        const Log2Sum c = end + l;
-        ta_a[32 * j] = c.hi;          // parked until the second loop
+        const Log2Sum c = end + l[j];
+        ta_l[32 * j] = l[j].hi + l[j].lo;   // from the block's start
+        ta_a[32 * j] = c.hi;                // parked until the loop
         ta_u[32 * j] = c.lo;
-        end = end + shfl(l, 31);
-        if (j == 0) e0 = end;
-        if (j == 1) e1 = end;
-        if (j == 2) e2 = end;
+        end = end + shfl(l[j], 31);
+        e[j] = end;
     }
     float g0 = gv[0], g1 = gv[1], g2 = gv[2], g3 = gv[3];
 #pragma unroll 1
     for (int j = 0; j < 4; ++j) {
         const int t = 32 * j;
-        const Log2Sum l = {ta_a[t], ta_u[t]};
+        const Log2Sum lt = {ta_a[t], ta_u[t]};
         const float g = g0, lb = ta_l[t];
         g0 = g1;
         g1 = g2;
         g2 = g3;
-        const float to = exp2_diff(l, zero), from = exp2_diff(end, l);
+        const float to = exp2_diff(lt, zero), from = exp2_diff(end, lt);
         ta_a[t] = REV ? from : scale * to;
         ta_u[t] = REV ? scale * to : g * from;
         ta_gm[t] = REV ? g : lb - log2f(g);   // closed gate: +inf, whose weight is 0
-        const Log2Sum ej = j == 0 ? e0 : j == 1 ? e1 : j == 2 ? e2 : end;
-        ta_t[t] = REV ? exp2_diff(ej, l) : ex2(lb);
+        const Log2Sum ej = j == 0 ? e[0] : j == 1 ? e[1] : j == 2 ? e[2] : end;
+        ta_t[t] = REV ? exp2_diff(ej, lt) : ex2(lb);
         // forward: c[b] serves block row b + 1, the blocks before it; backward: block row
         // b, the blocks after it (the other entries are not read; their exponents are > 0)
-        ta_c[t] = REV ? exp2_diff(l, e0) : g * exp2_diff(e0, l);
-        ta_c[kLtC + t] = REV ? exp2_diff(l, e1) : g * exp2_diff(e1, l);
-        ta_c[2 * kLtC + t] = REV ? exp2_diff(l, e2) : g * exp2_diff(e2, l);
+#pragma unroll
+        for (int b = 0; b < 3; ++b)
+            ta_c[b * kLtC + t] = REV ? exp2_diff(lt, e[b]) : g * exp2_diff(e[b], lt);
     }
     if (lane == 0) tab[8 * kLtC] = ex2(end.hi + end.lo);
 }
 
-// grid (2 * passes, B*H, S), block kLtThreads.  OUT = false: segment aggregates.
-template <bool REV, bool OUT>
+// (u z) of item i (16 bytes of a row) in three bf16 parts, 16 KB apart.
+__device__ __forceinline__ void lt_parts(const uint8_t *z, uint8_t *dst, float u) {
+    const uint4 w4 = *reinterpret_cast<const uint4 *>(z);
+    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+    uint32_t a[4], b[4], c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float2 y = __fmul2_rn(bf16x2_f2(w[e]), make_float2(u, u));
+        a[e] = f2_bf16x2(y);
+        y = f2_rest(y, a[e]);
+        b[e] = f2_bf16x2(y);
+        c[e] = f2_bf16x2(f2_rest(y, b[e]));
+    }
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
+    *reinterpret_cast<uint4 *>(dst + LtSmem::HALF) = make_uint4(b[0], b[1], b[2], b[3]);
+    *reinterpret_cast<uint4 *>(dst + 2 * LtSmem::HALF) = make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// grid (2 * passes, B*H, S), block kLtThreads.
+template <bool REV>
 __global__ void __launch_bounds__(kLtThreads, 1)
 k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_flag) {
     using L = LtSmem;
@@ -289,11 +307,11 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     uint8_t *sm = lt_smem;
     const uint32_t sb = smem_u32(sm);
     const uint32_t bars = sb + L::BARS;
-    const uint32_t b_x = bars, b_p = bars + 8, b_parts = bars + 16, b_s = bars + 24, b_pb = bars + 32,
-                   b_ds = bars + 40, b_o = bars + 48, b_xfree = bars + 56, b_os = bars + 64,
-                   b_fin = bars + 72;
-    const uint32_t b_y = bars + 80, b_z = bars + 96, b_out = bars + 112;                     // [2]
-    const uint32_t b_w = bars + 128, b_tfree = b_w + 8 * kLtTabs;                            // [kLtTabs]
+    const uint32_t b_p = bars, b_parts = bars + 8, b_s = bars + 16, b_pb = bars + 24, b_ds = bars + 32,
+                   b_os = bars + 40, b_xfree = bars + 48, b_oi = bars + 56;
+    const uint32_t b_xy = bars + 64, b_z = bars + 80, b_o = bars + 96, b_out = bars + 112,
+                   b_fin = bars + 128;                                                        // [2]
+    const uint32_t b_w = bars + 144, b_tfree = b_w + 8 * kLtTabs;                             // [kLtTabs]
     uint32_t *tbase = reinterpret_cast<uint32_t *>(sm + L::TBASE);
     const uint32_t abort = sb + L::TBASE + 4;
     float *s_tab = reinterpret_cast<float *>(sm + L::TAB);
@@ -302,53 +320,32 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int zh = blockIdx.x & 1, bh = blockIdx.y, seg = blockIdx.z;
     const int n0 = lin_seg(seg, p.S, p.N), n1 = lin_seg(seg + 1, p.S, p.N), NL = n1 - n0;
-    // the last segment's aggregate is never carried on
-    if (!OUT && seg == (REV ? 0 : p.S - 1)) return;
     auto chunk = [&](int it) { return REV ? n1 - 1 - it : n0 + it; };
-    constexpr int kIssuer = 2 * kLtGroup;   // first thread of the issuing warp
 
-    if (tid == kIssuer) {
+    if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            lt_init(b_y + 8 * i, 1);
+            lt_init(b_xy + 8 * i, 2);   // x's load and y's
             lt_init(b_z + 8 * i, 1);
+            lt_init(b_o + 8 * i, 2);    // both issuers': every product of the chunk is done
             lt_init(b_out + 8 * i, 8);
+            lt_init(b_fin + 8 * i, 1);
         }
         for (int i = 0; i < kLtTabs; ++i) {
             lt_init(b_w + 8 * i, 32);
-            lt_init(b_tfree + 8 * i, OUT ? 16 : 8);
+            lt_init(b_tfree + 8 * i, 16);
         }
-        lt_init(b_x, 1);
         lt_init(b_p, 1);
         lt_init(b_parts, 8);
         lt_init(b_s, 16);   // S staged, and the last chunk's OS read
         lt_init(b_pb, 8);
         lt_init(b_ds, 1);
-        lt_init(b_o, 1);
-        lt_init(b_xfree, 1);
-        lt_init(b_fin, 1);
         lt_init(b_os, 1);
+        lt_init(b_xfree, 1);
+        lt_init(b_oi, 1);
         asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(0u) : "memory");
         fence_mbar_init();
     }
-    __syncthreads();
-    auto load_x = [&](int it) {
-        const int t0 = chunk(it) * C;
-        lt_expect(b_x, L::TILE);
-        tma_load_3d(sm + L::X, &A.x, 0, t0, bh, b_x);
-        tma_load_3d(sm + L::X + L::HALF, &A.x, 64, t0, bh, b_x);
-    };
-    auto load_y = [&](int it) {
-        const int st = it & 1, t0 = chunk(it) * C;
-        lt_expect(b_y + 8 * st, L::TILE);
-        tma_load_3d(sm + L::Y + st * L::TILE, &A.y, 0, t0, bh, b_y + 8 * st);
-        tma_load_3d(sm + L::Y + st * L::TILE + L::HALF, &A.y, 64, t0, bh, b_y + 8 * st);
-    };
-    auto load_z = [&](int it) {
-        const int st = it & 1;
-        lt_expect(b_z + 8 * st, L::HALF);
-        tma_load_3d(sm + L::Z + st * L::HALF, &A.z, zh * kLtZN, chunk(it) * C, bh, b_z + 8 * st);
-    };
-    if (warp == 0) {
+    if (warp == 1) {
         tc::tmem_alloc(tbase, 512);
         tc::tmem_relinquish();
     }
@@ -360,17 +357,8 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     if (*tbase != tmem || (sb & 1023u)) {   // what the constants rest on; nothing is in flight yet
         if (tid == 0) atomicExch(timeout_flag, 1);
         __syncthreads();
-        if (warp == 0) tc::tmem_dealloc(*tbase, 512);
+        if (warp == 1) tc::tmem_dealloc(*tbase, 512);
         return;
-    }
-    if (tid == kIssuer) {
-        load_z(0);
-        load_y(0);
-        if (OUT) load_x(0);
-        if (NL > 1) {
-            load_z(1);
-            load_y(1);
-        }
     }
     // TMEM columns; the bf16 weighted scores of each half of the columns lie over its scores
     constexpr uint32_t kP = 0, kOI = 128, kOS = 192, kDS = 256, kX = 448;
@@ -381,55 +369,58 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         __syncwarp();
         if (lane == 0) lt_arrive(bar);
     };
-    auto wait = [&](uint32_t bar, uint32_t parity) {   // the whole warp, one outcome
-        return __all_sync(0xffffffffu, lt_wait_call(bar, parity, abort)) != 0;
-    };
-
-    // (u z) in three bf16 parts, at the places of z: two (OUT: both groups share the rows) or
-    // four 16-byte items a thread
-    auto parts = [&](const float *tab, int sg) {
-        constexpr int kStep = kLtGroup;
-        const int first = tid - kLtGroup;
-#pragma unroll 1
-        for (int item = first; item < 1024; item += kStep) {   // row item / 8
-            const uint4 w4 = *reinterpret_cast<const uint4 *>(sm + L::Z + sg * L::HALF + item * 16);
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-            const float u = tab[C + (item >> 3)];
-            uint32_t a[4], b[4], c[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float2 y = __fmul2_rn(bf16x2_f2(w[e]), make_float2(u, u));
-                a[e] = f2_bf16x2(y);
-                y = f2_rest(y, a[e]);
-                b[e] = f2_bf16x2(y);
-                c[e] = f2_bf16x2(f2_rest(y, b[e]));
-            }
-            uint8_t *dst = sm + L::PARTS + item * 16;
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
-            *reinterpret_cast<uint4 *>(dst + L::HALF) = make_uint4(b[0], b[1], b[2], b[3]);
-            *reinterpret_cast<uint4 *>(dst + 2 * L::HALF) = make_uint4(c[0], c[1], c[2], c[3]);
-        }
-        fence_proxy_async_smem();
-        arrive(b_parts);
-    };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return lt_wait_warp(bar, parity, abort); };
+    constexpr uint32_t ID_P = tc::idesc_bf16(128, 128, false, false);
+    constexpr uint32_t ID_O = tc::idesc_bf16(128, 64, false, true);
+    constexpr uint32_t ID_D = tc::idesc_bf16(128, 192, true, true);
+    // steps (in 16 bytes) from an operand's descriptor to its kk-th K step
+    auto kmaj = [](int kk) { return (uint64_t)((kk >> 2) * (L::HALF / 16) + (kk & 3) * 2); };
+    auto mnmaj = [](int kk) { return (uint64_t)(kk * 128); };
 
     if (warp == 16) {
-        // ---- issuer: the whole warp runs the loop, one lane issues ----
-        constexpr uint32_t ID_P = tc::idesc_bf16(128, 128, false, false);
-        constexpr uint32_t ID_O = tc::idesc_bf16(128, 64, false, true);
-        constexpr uint32_t ID_D = tc::idesc_bf16(128, 192, true, true);
-        // descriptors: one per operand, and the steps (in 16 bytes) to the kk-th K step and to
-        // the other stage, so that a product costs an addition and the instruction
-        const uint64_t d_x = tc::sdesc(sb + L::X, 16, 1024), d_yk = tc::sdesc(sb + L::Y, 16, 1024),
-                       d_ym = tc::sdesc(sb + L::Y, L::HALF, 1024), d_z = tc::sdesc(sb + L::Z, L::HALF, 1024),
-                       d_s = tc::sdesc(sb + L::SOP, L::HALF, 1024),
+        // ---- issuer of the state's products, OS and DS ----
+        const uint64_t d_y = tc::sdesc(sb + L::Y, L::HALF, 1024), d_s = tc::sdesc(sb + L::SOP, L::HALF, 1024),
                        d_u = tc::sdesc(sb + L::PARTS, L::HALF, 1024);
-        auto kmaj = [](int kk) { return (uint64_t)((kk >> 2) * (L::HALF / 16) + (kk & 3) * 2); };
-        auto mnmaj = [](int kk) { return (uint64_t)(kk * 128); };
-        // x(it) from shared memory to TMEM, which frees its stage; the last chunk's readers
-        // of those columns are done
+        bool ok = true;
+#pragma unroll 1
+        for (int it = 0; it < NL; ++it) {
+            const int st = it & 1, ph = it & 1;
+            // x is in TMEM (and y in shared memory); the state operand is there and the last
+            // chunk's OS has been read
+            ok = wait(b_xfree, ph) && wait(b_s, ph);
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 16; ++kk)   // K steps against S_hi, then S_lo, 16 KB on
+                    mma_bf16_ta(tmem + kOS, tmem + kX + (kk & 7) * 8, d_s + mnmaj(kk), ID_O, kk > 0);
+                lt_commit(b_os);
+            }
+            ok = wait(b_parts, ph);
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (elect_one()) {
+                const uint64_t y = d_y + st * (L::TILE / 16);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    tc::mma_f16(tmem + kDS, y + mnmaj(kk), d_u + mnmaj(kk), ID_D, kk > 0);
+                lt_commit(b_ds);
+                lt_commit(b_o + 8 * st);
+            }
+        }
+        if (!ok && elect_one()) {   // a wait gave up: flag it, then drain this thread's products
+            atomicExch(timeout_flag, 1);
+            lt_commit(b_fin);
+            lt_drain(b_fin, 0);
+        }
+        __syncwarp();
+    } else if (warp == 18) {
+        // ---- issuer of x's copies to TMEM, of the scores P and of OI ----
+        const uint64_t d_x = tc::sdesc(sb + L::X, 16, 1024), d_y = tc::sdesc(sb + L::Y, 16, 1024),
+                       d_z = tc::sdesc(sb + L::Z, L::HALF, 1024);
+        // x(it) to TMEM, which frees its stage
         auto copy_x = [&](int it) {
-            if (!wait(b_x, it & 1)) return false;
+            if (!wait(b_xy + 8 * (it & 1), (it >> 1) & 1)) return false;
             tc::fence_after_sync();
             if (elect_one()) {
 #pragma unroll
@@ -439,87 +430,50 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             return true;
         };
         auto issue_p = [&](int it) {
-            const int st = it & 1;
-            if (!wait(b_y + 8 * st, (it >> 1) & 1)) return false;
             if (elect_one()) {
-                const uint64_t y = d_yk + st * (L::TILE / 16);
+                const uint64_t y = d_y + (it & 1) * (L::TILE / 16);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                     mma_bf16_ta(tmem + kP, tmem + kX + kk * 8, y + kmaj(kk), ID_P, kk > 0);
                 lt_commit(b_p);
             }
-            return true;
         };
-        int loads_x = OUT;   // begun
-        bool ok = !OUT || (copy_x(0) && issue_p(0));
-        if (OUT && ok && NL > 1) {
-            ok = wait(b_xfree, 0);
-            if (ok && elect_one()) load_x(1);
-            loads_x += ok;
-        }
+        bool ok = copy_x(0);
+        if (ok) issue_p(0);
 #pragma unroll 1
         for (int it = 0; ok && it < NL; ++it) {
             const int st = it & 1, ph = it & 1;
-            if (OUT) {
-                // the state operand is there and the last chunk's OS has been read
-                ok = wait(b_s, ph);
-                if (!ok) break;
-                tc::fence_after_sync();
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < 16; ++kk)   // K steps against S_hi, then S_lo, 16 KB on
-                        mma_bf16_ta(tmem + kOS, tmem + kX + (kk & 7) * 8, d_s + mnmaj(kk), ID_O, kk > 0);
-                    lt_commit(b_os);
-                }
-            } else {
-                ok = wait(b_y + 8 * st, (it >> 1) & 1);
-                if (!ok) break;
-            }
-            ok = wait(b_parts, ph);
+            // x of the next chunk once this one's OS and P have read it in TMEM, while the
+            // weighted scores are formed
+            if (it + 1 < NL) ok = wait(b_p, ph) && wait(b_os, ph) && copy_x(it + 1);
+            ok = ok && wait(b_pb, ph);
             if (!ok) break;
             tc::fence_after_sync();
             if (elect_one()) {
-                const uint64_t y = d_ym + st * (L::TILE / 16);
+                const uint64_t z = d_z + st * (L::HALF / 16);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    tc::mma_f16(tmem + kDS, y + mnmaj(kk), d_u + mnmaj(kk), ID_D, kk > 0);
-                lt_commit(b_ds);
+                    mma_bf16_ta(tmem + kOI, tmem + kP + (kk >> 2) * 64 + (kk & 3) * 8, z + mnmaj(kk), ID_O,
+                                kk > 0);
+                lt_commit(b_oi);
+                lt_commit(b_o + 8 * st);
             }
-            if (OUT) {
-                // x of the next chunk into TMEM once this one's P and OS have read it there, while
-                // the weighted scores are formed
-                if (it + 1 < NL) ok = wait(b_os, ph) && copy_x(it + 1);
-                ok = ok && wait(b_pb, ph);
+            // the next chunk's scores once OI has read the weighted ones, whose columns they take
+            if (it + 1 < NL) {
+                ok = wait(b_oi, ph);
                 if (!ok) break;
                 tc::fence_after_sync();
-                if (elect_one()) {
-                    const uint64_t z = d_z + st * (L::HALF / 16);
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_ta(tmem + kOI, tmem + kP + (kk >> 2) * 64 + (kk & 3) * 8, z + mnmaj(kk), ID_O,
-                                    kk > 0);
-                    lt_commit(b_o);
-                }
-                if (it + 2 < NL) {   // its stage is free again
-                    ok = wait(b_xfree, ph ^ 1);
-                    if (!ok) break;
-                    if (elect_one()) load_x(it + 2);
-                    ++loads_x;
-                }
-                // the next chunk's scores once OI has read the weighted ones, whose columns they take
-                if (it + 1 < NL) ok = wait(b_o, ph) && issue_p(it + 1);
+                issue_p(it + 1);
             }
         }
         if (!ok && elect_one()) {
-            // a wait gave up: flag it, then drain this thread's products and copies
             atomicExch(timeout_flag, 1);
-            lt_commit(b_fin);
-            lt_drain(b_fin, 0);
-            if (loads_x) lt_drain(b_x, (loads_x - 1) & 1);
+            lt_commit(b_fin + 8);
+            lt_drain(b_fin + 8, 0);
         }
         __syncwarp();
-    } else if (warp == 17 || warp == 18) {
-        // ---- decay tables: even chunks by one warp, odd ones by the other ----
+    } else if (warp == 17) {
+        // ---- decay tables, up to kLtTabs chunks ahead ----
         const float *beta = p.beta + (size_t)bh * p.T;
         const float *gate = p.gate ? p.gate + (size_t)bh * p.T : nullptr;
         const float log2_min = (float)(p.log_min * 1.4426950408889634);
@@ -533,9 +487,9 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 gv[j] = in ? (gate ? gate[t0 + 32 * j] : 1.f) : 0.f;
             }
         };
-        const int par = warp - 17;
-        if (par < NL) fetch(par);
-        for (int it = par; it < NL; it += 2) {
+        fetch(0);
+#pragma unroll 1
+        for (int it = 0; it < NL; ++it) {
             const int ts = it % kLtTabs;
             if (it >= kLtTabs && !wait(b_tfree + 8 * ts, (it / kLtTabs - 1) & 1)) break;
             float cb[4], cg[4];
@@ -544,48 +498,80 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 cb[j] = bv[j];
                 cg[j] = gv[j];
             }
-            if (it + 2 < NL) fetch(it + 2);
+            if (it + 1 < NL) fetch(it + 1);
             lt_tables<REV>(s_tab + ts * L::TABF, cb, cg, p.scale, log2_min);
             lt_arrive(b_w + 8 * ts);
         }
     } else if (warp == 19) {
         // ---- loads into freed stages, rows out ----
         if (lane == 0) {
-            int loads_y[2] = {1, NL > 1}, loads_z[2] = {1, NL > 1};   // begun
+            int loads_x = 0, loads_y = 0, loads_z = 0;   // begun
+            auto load_x = [&](int it) {
+                const int t0 = chunk(it) * C;
+                lt_expect(b_xy + 8 * (it & 1), L::TILE);
+                tma_load_3d(sm + L::X, &A.x, 0, t0, bh, b_xy + 8 * (it & 1));
+                tma_load_3d(sm + L::X + L::HALF, &A.x, 64, t0, bh, b_xy + 8 * (it & 1));
+                ++loads_x;
+            };
+            auto load_y = [&](int it) {
+                const int st = it & 1, t0 = chunk(it) * C;
+                lt_expect(b_xy + 8 * st, L::TILE);
+                tma_load_3d(sm + L::Y + st * L::TILE, &A.y, 0, t0, bh, b_xy + 8 * st);
+                tma_load_3d(sm + L::Y + st * L::TILE + L::HALF, &A.y, 64, t0, bh, b_xy + 8 * st);
+                ++loads_y;
+            };
+            auto load_z = [&](int it) {
+                const int st = it & 1;
+                lt_expect(b_z + 8 * st, L::HALF);
+                tma_load_3d(sm + L::Z + st * L::HALF, &A.z, zh * kLtZN, chunk(it) * C, bh, b_z + 8 * st);
+                ++loads_z;
+            };
+            load_x(0);
+            load_y(0);
+            load_z(0);
+            if (NL > 1) {
+                load_y(1);
+                load_z(1);
+            }
             bool ok = true;
+            if (NL > 1) {
+                ok = lt_wait(b_xfree, 0, abort);
+                if (ok) load_x(1);
+            }
 #pragma unroll 1
-            for (int it = 0; it < NL; ++it) {
-                const int st = it & 1, ph = it & 1;
-                if (it + 2 < NL) {   // y's readers, P(it) and DS(it), are done
-                    ok = lt_wait(OUT ? b_o : b_ds, ph, abort);
+            for (int it = 0; ok && it < NL; ++it) {
+                const int st = it & 1, ph2 = (it >> 1) & 1;
+                if (it + 2 < NL) {
+                    ok = lt_wait(b_xfree, (it + 1) & 1, abort);   // x(it + 1) is in TMEM
+                    if (!ok) break;
+                    load_x(it + 2);
+                    ok = lt_wait(b_o + 8 * st, ph2, abort);       // y's readers are done
                     if (!ok) break;
                     load_y(it + 2);
-                    ++loads_y[st];
                 }
-                if (OUT) {   // the rows lie where z did, whose next chunk follows them
-                    ok = lt_wait(b_out + 8 * st, (it >> 1) & 1, abort);
-                    if (!ok) break;
-                    tma_store_3d(&A.out, zh * kLtZN, chunk(it) * C, bh, sm + L::Z + st * L::HALF);
-                    tc::bulk_commit();
-                    tc::bulk_wait_read0();
-                }
-                if (it + 2 < NL) {
-                    load_z(it + 2);
-                    ++loads_z[st];
-                }
+                // the rows lie where z did, whose next chunk follows them
+                ok = lt_wait(b_out + 8 * st, ph2, abort);
+                if (!ok) break;
+                tma_store_3d(&A.out, zh * kLtZN, chunk(it) * C, bh, sm + L::Z + st * L::HALF);
+                tc::bulk_commit();
+                tc::bulk_wait_read0();
+                if (it + 2 < NL) load_z(it + 2);
             }
-            if (OUT) tc::bulk_wait0();
-            if (!ok) {   // a wait gave up: drain this thread's copies
+            tc::bulk_wait0();
+            if (!ok) {   // a wait gave up: drain this thread's copies (chunk i's loads on barrier i & 1)
                 for (int i = 0; i < 2; ++i) {
-                    if (loads_y[i]) lt_drain(b_y + 8 * i, (loads_y[i] - 1) & 1);
-                    if (loads_z[i]) lt_drain(b_z + 8 * i, (loads_z[i] - 1) & 1);
+                    const int n = (min(loads_x, loads_y) + 1 - i) / 2, m = (loads_z + 1 - i) / 2;
+                    if (n) lt_drain(b_xy + 8 * i, (n - 1) & 1);
+                    if (m) lt_drain(b_z + 8 * i, (m - 1) & 1);
                 }
+                // a load whose barrier's other half was never begun: time for it to land
+                if (loads_x != loads_y) __nanosleep(1000000);
             }
         }
         __syncwarp();
     } else if (warp < 8) {
         // ---- scores and outputs: thread has token `row`, 64 score columns, 32 of z ----
-        if (OUT) {
+        {
             const int half = warp >> 2, z0 = zh * kLtZN + half * 32;
             arrive(b_s);   // no OS to read before the first
 #pragma unroll 1
@@ -657,7 +643,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 const bool dots = p.dot && in;
                 const float a = tab[row], g = REV ? tab[7 * C + row] : 1.f;
                 float d = 0.f;
-                if (!wait(b_o, ph)) break;
+                if (!wait(b_o + 8 * sg, (it >> 1) & 1)) break;
                 tc::fence_after_sync();
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
@@ -706,17 +692,16 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         };
 #pragma unroll
         for (int j = 0; j < 32; ++j) st[j] = 0.f;
-        if (OUT && p.start) {
+        if (p.start) {
             const size_t base = ((size_t)bh * p.S + seg) * D * D;
 #pragma unroll
             for (int j = 0; j < 32; ++j) st[j] = p.start[at(base, j)];
         }
-        float dec = 1.f;   // the segment's decay so far
         bool ok = true;
         for (int it = 0; it < NL; ++it) {
             const int sg = it & 1, ph = it & 1, ts = it % kLtTabs, n = chunk(it);
             const float *tab = s_tab + ts * L::TABF;
-            if (OUT) {
+            {
                 // the state before the chunk as the B operand, rows of y, two bf16 parts
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
@@ -736,14 +721,18 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             }
             ok = wait(b_w + 8 * ts, (it / kLtTabs) & 1) && wait(b_z + 8 * sg, (it >> 1) & 1);
             if (!ok) break;
-            parts(tab, sg);
+#pragma unroll 1
+            for (int item = gt; item < 1024; item += kLtGroup)   // row item / 8
+                lt_parts(sm + L::Z + sg * L::HALF + item * 16, sm + L::PARTS + item * 16, tab[C + (item >> 3)]);
+            fence_proxy_async_smem();
+            arrive(b_parts);
             const float b = tab[8 * C];
-            if (OUT && p.states) {
+            if (p.states) {
                 float *dst = p.states + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) dst[j * D] = st[j];
             }
-            if (OUT && p.states_in) {
+            if (p.states_in) {
                 const float *src = p.states_in + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
                 float f = 0.f;
 #pragma unroll
@@ -751,7 +740,6 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 f = warp_sum(f);
                 if (lane == 0) p.fdot[((size_t)(zh * 8 + warp - 8) * p.BH + bh) * p.N + n] = b * f;
             }
-            dec *= b;
             // S' = b S + DS
             ok = wait(b_ds, ph);
             if (!ok) break;
@@ -772,21 +760,201 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             tc::fence_before_sync();
             arrive(b_tfree + 8 * ts);
         }
-        float *dst = OUT ? (seg == (REV ? 0 : p.S - 1) ? p.last : nullptr) : p.agg;
-        if (ok && dst) {
-            const size_t base = OUT ? (size_t)bh * D * D : ((size_t)bh * p.S + seg) * D * D;
+        if (ok && p.last && seg == (REV ? 0 : p.S - 1)) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) dst[at(base, j)] = st[j];
+            for (int j = 0; j < 32; ++j) p.last[at((size_t)bh * D * D, j)] = st[j];
         }
-        if (!OUT && ok && gt == 0 && blockIdx.x == 0) p.segdec[(size_t)bh * p.S + seg] = dec;
     }
     // every product and copy has completed (the arithmetic warps waited for the last
-    // chunk's; after a time-out the issuer drained them)
+    // chunk's; after a time-out their issuers drained them)
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 1) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Segment aggregates: a segment's increment from a zero state, its chunks taken from the end
+// the state leaves by (the last chunk first, or in a backward pass the first), so that every
+// weight is a product of decays down from one, A = sum u_i y_i z_i^T with
+//   u_i = g_i prod_{m > i} beta_m   (backward: c prod_{m <= i} beta_m)
+// over the segment: one product per chunk into the same accumulators, with nothing of the
+// state in between.  Warps 0-15 form the weighted rows (as in k_linear_tc), warp 16 issues,
+// warp 17 forms the weights, warp 18 loads.
+struct LaSmem {
+    static constexpr uint32_t Y = 0;                             // 2 stages
+    static constexpr uint32_t Z = Y + 2 * LtSmem::TILE;          // 2 stages
+    static constexpr uint32_t PARTS = Z + 2 * LtSmem::HALF;      // 2 x hi, mid, lo
+    static constexpr uint32_t U = PARTS + 6 * LtSmem::HALF;      // [2][128]
+    static constexpr uint32_t BARS = U + 2 * 4 * kLtC;
+    static constexpr uint32_t TBASE = BARS + 8 * (8 + 2);
+    static constexpr uint32_t END = TBASE + 16;
+    static constexpr size_t bytes = END + 1024;
+};
+
+// grid (2, B*H, S), block kLtThreads.
+template <bool REV>
+__global__ void __launch_bounds__(kLtThreads, 1)
+k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_flag) {
+    using L = LaSmem;
+    constexpr int C = kLtC, D = 128, PARTB = 3 * LtSmem::HALF;
+    extern __shared__ uint8_t smraw[];
+    uint8_t *sm = smem_align1024(smraw);
+    const uint32_t sb = smem_u32(sm), bars = sb + L::BARS;
+    const uint32_t b_yz = bars, b_parts = bars + 16, b_ds = bars + 32, b_fin = bars + 48, b_w = bars + 56;
+    uint32_t *tbase = reinterpret_cast<uint32_t *>(sm + L::TBASE);
+    const uint32_t abort = sb + L::TBASE + 4;
+    float *s_u = reinterpret_cast<float *>(sm + L::U);
+    const LinPass &p = A.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int zh = blockIdx.x, bh = blockIdx.y, seg = blockIdx.z;
+    if (seg == (REV ? 0 : p.S - 1)) return;   // never carried on
+    const int n0 = lin_seg(seg, p.S, p.N), n1 = lin_seg(seg + 1, p.S, p.N), NL = n1 - n0;
+    auto chunk = [&](int it) { return REV ? n0 + it : n1 - 1 - it; };
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            lt_init(b_yz + 8 * i, 1);
+            lt_init(b_parts + 8 * i, 16);
+            lt_init(b_ds + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) lt_init(b_w + 8 * i, 32);
+        lt_init(b_fin, 1);
+        asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(0u) : "memory");
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tbase, 256);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tbase;
+    auto wait = [&](uint32_t bar, uint32_t parity) { return lt_wait_warp(bar, parity, abort); };
+    // phase of chunk it on a barrier of two: (it / 2) & 1; done(it): its product has completed
+    auto done = [&](int it) { return wait(b_ds + 8 * (it & 1), (it >> 1) & 1); };
+    bool ok = true;
+
+    if (warp == 16) {
+        constexpr uint32_t ID_D = tc::idesc_bf16(128, 192, true, true);
+        const uint64_t d_y = tc::sdesc(sb + L::Y, LtSmem::HALF, 1024),
+                       d_u = tc::sdesc(sb + L::PARTS, LtSmem::HALF, 1024);
+#pragma unroll 1
+        for (int it = 0; it < NL; ++it) {
+            const int st = it & 1;
+            ok = wait(b_parts + 8 * st, (it >> 1) & 1);
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (elect_one()) {
+                const uint64_t y = d_y + st * (LtSmem::TILE / 16), u = d_u + st * (PARTB / 16);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    tc::mma_f16(tmem, y + kk * 128, u + kk * 128, ID_D, (it | kk) != 0);
+                lt_commit(b_ds + 8 * st);
+            }
+        }
+        if (!ok && elect_one()) {
+            atomicExch(timeout_flag, 1);
+            lt_commit(b_fin);
+            lt_drain(b_fin, 0);
+        }
+        __syncwarp();
+    } else if (warp == 17) {
+        const float *beta = p.beta + (size_t)bh * p.T;
+        const float *gate = p.gate ? p.gate + (size_t)bh * p.T : nullptr;
+        const float log2_min = (float)(p.log_min * 1.4426950408889634);
+        const Log2Sum zero = {0.f, 0.f};
+        Log2Sum far = zero;   // log decay of the chunks between this one and the segment's end
+#pragma unroll 1
+        for (int it = 0; it < NL; ++it) {
+            const int ts = it & 1, t0 = chunk(it) * C + lane;
+            float bv[4], gv[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool in = t0 + 32 * j < p.T;
+                bv[j] = in ? beta[t0 + 32 * j] : 1.f;
+                gv[j] = in ? (gate ? gate[t0 + 32 * j] : 1.f) : 0.f;
+            }
+            // the weights' last readers, chunk it - 2, are done
+            if (it >= 2) ok = done(it - 2);
+            if (!ok) break;
+            Log2Sum l[4], end = zero;
+            lt_scan(bv, log2_min, l);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const Log2Sum c = end + l[j];
+                end = end + shfl(l[j], 31);
+                l[j] = c;
+            }
+            const Log2Sum all = end + far;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s_u[ts * C + 32 * j + lane] = REV ? p.scale * exp2_diff(far + l[j], zero) : gv[j] * exp2_diff(all, l[j]);
+            far = all;
+            lt_arrive(b_w + 8 * ts);
+        }
+        if (ok && lane == 0 && zh == 0) p.segdec[(size_t)bh * p.S + seg] = exp2_diff(far, zero);
+    } else if (warp == 18) {
+        if (lane == 0) {
+            int loads = 0;
+#pragma unroll 1
+            for (int it = 0; it < NL; ++it) {
+                const int st = it & 1, t0 = chunk(it) * C;
+                if (it >= 2) ok = lt_wait(b_ds + 8 * st, ((it >> 1) - 1) & 1, abort);
+                if (!ok) break;
+                lt_expect(b_yz + 8 * st, LtSmem::TILE + LtSmem::HALF);
+                tma_load_3d(sm + L::Z + st * LtSmem::HALF, &A.z, zh * kLtZN, t0, bh, b_yz + 8 * st);
+                tma_load_3d(sm + L::Y + st * LtSmem::TILE, &A.y, 0, t0, bh, b_yz + 8 * st);
+                tma_load_3d(sm + L::Y + st * LtSmem::TILE + LtSmem::HALF, &A.y, 64, t0, bh, b_yz + 8 * st);
+                ++loads;
+            }
+            if (!ok)
+                for (int i = 0; i < 2; ++i)
+                    if ((loads + 1 - i) / 2) lt_drain(b_yz + 8 * i, ((loads + 1 - i) / 2 - 1) & 1);
+        }
+        __syncwarp();
+    } else if (warp < 16) {
+#pragma unroll 1
+        for (int it = 0; it < NL; ++it) {
+            const int st = it & 1, ts = st;
+            ok = wait(b_w + 8 * ts, (it >> 1) & 1) && wait(b_yz + 8 * st, (it >> 1) & 1) &&
+                 (it < 2 || done(it - 2));
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int item = tid + i * 512;   // row item / 8
+                lt_parts(sm + L::Z + st * LtSmem::HALF + item * 16, sm + L::PARTS + st * PARTB + item * 16,
+                         s_u[ts * C + (item >> 3)]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) lt_arrive(b_parts + 8 * st);
+        }
+        if (ok) ok = done(NL - 1);
+        if (ok) {
+            tc::fence_after_sync();
+            const int quarter = warp & 3, cg = warp >> 2, row = quarter * 32 + lane, z0 = zh * kLtZN + cg * 16;
+            const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + cg * 16;
+            float v[16], w[16];
+            tc::tmem_ld16(tl + 64, v);
+            tc::tmem_ld16(tl + 128, w);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] += w[j];
+            tc::tmem_ld16(tl, w);
+            tc::tmem_wait_ld();
+            const size_t base = ((size_t)bh * p.S + seg) * D * D;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                p.agg[base + (p.zy ? (size_t)(z0 + j) * D + row : (size_t)row * D + z0 + j)] = w[j] + v[j];
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 256);
     }
 }
 
