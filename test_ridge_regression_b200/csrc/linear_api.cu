@@ -27,6 +27,7 @@ struct LinLayout {
     int N, S, ZS;                              // chunks, segments, column splits
     int dots, fdots;                           // planes of the dbeta terms' partial sums
     size_t agg, segdec;                        // segment aggregates, decays (S > 1)
+    size_t tab;                                // decay tables (tensor cores), forward's then backward's
     size_t states, zeta, eta, fdot;            // backward
     size_t total;
 };
@@ -57,6 +58,7 @@ static int lin_layout(int B, int H, int T, int D, gka_dtype dt, bool bwd, LinLay
     };
     L->agg = take(L->S > 1 ? BH * L->S * st : 0);
     L->segdec = take(L->S > 1 ? BH * L->S * sizeof(float) : 0);
+    L->tab = take(L->tc ? (bwd ? 2 : 1) * BH * L->N * kLtTabF * sizeof(float) : 0);
     L->states = L->zeta = L->eta = L->fdot = off;
     if (bwd) {
         L->states = take(BH * L->N * st);
@@ -195,17 +197,47 @@ static int head_map(CUtensorMap *m, const void *base, int T, int BH) {
     return r == CUDA_SUCCESS ? GKA_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
-template <bool REV>
-static int lin_tc_launch(const LinTcArgs &a, int passes, int prof, cudaStream_t s) {
+// Launches `kern` as the programmatic dependent of the kernel before it (`pdl`): it may set
+// itself up while that one ends, and waits for it on the device.
+template <typename K, typename... Args>
+static int launch_after(K kern, dim3 grid, int threads, size_t smem, bool pdl, cudaStream_t s, Args... args) {
     cudaError_t e;
+    if ((e = set_smem(kern, smem)) != cudaSuccess) return cuda_fail(e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    if ((e = cudaLaunchKernelEx(&cfg, kern, args...)) != cudaSuccess) return cuda_fail(e);
+    return GKA_OK;
+}
+
+// Every chunk's decay tables for one direction, into the workspace.
+template <bool REV>
+static int lin_tc_tables(LinTcArgs &a, int passes, const LinLayout &L, char *ws, int prof, cudaStream_t s) {
+    const LinPass &p = a.pass[0].p;
+    float *tab = reinterpret_cast<float *>(ws + L.tab) + (REV ? (size_t)p.BH * L.N * kLtTabF : 0);
+    for (int i = 0; i < passes; ++i) a.pass[i].tab = tab;
+    const long long chunks = (long long)p.BH * L.N;
+    ProfScope ps(prof, s);
+    k_linear_tables<REV><<<(unsigned)((chunks + 7) / 8), 256, 0, s>>>(
+        p.beta, p.gate, tab, p.BH, L.N, p.T, p.scale, (float)(p.log_min * 1.4426950408889634));
+    return check_launch();
+}
+
+// `pdl`: the kernel before is the tables'.
+template <bool REV>
+static int lin_tc_launch(const LinTcArgs &a, int passes, bool pdl, int prof, cudaStream_t s) {
     int *flag = nullptr;
     if (int rc = timeout_flag_ptr(&flag)) return rc;
-    auto kern = k_linear_tc<REV>;
-    if ((e = set_smem(kern, LtSmem::bytes)) != cudaSuccess) return cuda_fail(e);
     const LinPass &p = a.pass[0].p;
     ProfScope ps(prof, s);
-    kern<<<dim3(2 * passes, p.BH, p.S), kLtThreads, LtSmem::bytes, s>>>(a, flag);
-    return check_launch();
+    return launch_after(k_linear_tc<REV>, dim3(2 * passes, p.BH, p.S), kLtThreads, LtSmem::bytes, pdl, s, a, flag);
 }
 
 template <bool REV>
@@ -218,16 +250,14 @@ static int lin_tc_starts(LinTcArgs &a, const LinLayout &L, char *ws, const float
     }
     p.agg = reinterpret_cast<float *>(ws + L.agg);
     p.segdec = reinterpret_cast<float *>(ws + L.segdec);
-    cudaError_t e;
     int *flag = nullptr;
     if (int rc = timeout_flag_ptr(&flag)) return rc;
-    auto kern = k_linear_agg_tc<REV>;
-    if ((e = set_smem(kern, LaSmem::bytes)) != cudaSuccess) return cuda_fail(e);
     {
         ProfScope ps(prof, s);
-        kern<<<dim3(2, p.BH, L.S), kLtThreads, LaSmem::bytes, s>>>(a.pass[0], flag);
+        if (int rc = launch_after(k_linear_agg_tc<REV>, dim3(2, p.BH, L.S), kLtThreads, LaSmem::bytes, true, s,
+                                  a.pass[0], flag))
+            return rc;
     }
-    if (int rc = check_launch()) return rc;
     ProfScope ps(prof, s);
     k_linear_scan<<<dim3(16, p.BH), 256, 0, s>>>(p.agg, p.segdec, init, L.S, 128 * 128, REV);
     p.start = p.agg;
@@ -246,9 +276,10 @@ static int lin_tc_forward(const LinCall &c, const LinLayout &L) {
     p.log_min = kLogBetaMin;
     p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S;
     p.zy = 1;
+    if (int rc = lin_tc_tables<false>(a, 1, L, c.ws, GKA_KERNEL_LINEAR, c.s)) return rc;
     if (int rc = lin_tc_starts<false>(a, L, c.ws, c.init, GKA_KERNEL_LINEAR, c.s)) return rc;
     p.last = c.last;
-    return lin_tc_launch<false>(a, 1, GKA_KERNEL_LINEAR, c.s);
+    return lin_tc_launch<false>(a, 1, L.S == 1, GKA_KERNEL_LINEAR, c.s);
 }
 
 static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
@@ -271,18 +302,20 @@ static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
     LinTcArgs f = {};
     f.pass[0].x = d_o; f.pass[0].y = v; f.pass[0].z = k;
     f.pass[0].p = p;
+    if (int rc = lin_tc_tables<false>(f, 1, L, c.ws, kProf, c.s)) return rc;
     if (int rc = lin_tc_starts<false>(f, L, c.ws, c.init, kProf, c.s)) return rc;
     LinPass &pf = f.pass[0].p;
     if (int rc = head_map(&f.pass[0].out, c.dq, c.T, c.BH)) return rc;
     pf.xd = c.q;
     pf.dot = const_cast<float *>(w.p.zeta);
     pf.states = reinterpret_cast<float *>(c.ws + L.states);
-    if (int rc = lin_tc_launch<false>(f, 1, kProf, c.s)) return rc;
+    if (int rc = lin_tc_launch<false>(f, 1, L.S == 1, kProf, c.s)) return rc;
     // dv and dk, backwards in time, in one launch
     LinTcArgs r = {};
     r.pass[0].x = k; r.pass[0].y = q; r.pass[0].z = d_o;
     r.pass[0].p = p;
     r.pass[0].p.zy = 1;
+    if (int rc = lin_tc_tables<true>(r, 2, L, c.ws, kProf, c.s)) return rc;
     if (int rc = lin_tc_starts<true>(r, L, c.ws, c.dlast, kProf, c.s)) return rc;
     LinPass &pv = r.pass[0].p, &pk = r.pass[1].p;
     r.pass[1].x = v; r.pass[1].y = d_o; r.pass[1].z = q;
@@ -296,7 +329,7 @@ static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
     pv.xd = c.v;
     pv.dot = const_cast<float *>(w.p.eta);
     pv.last = c.dinit;
-    if (int rc = lin_tc_launch<true>(r, 2, kProf, c.s)) return rc;
+    if (int rc = lin_tc_launch<true>(r, 2, L.S == 1, kProf, c.s)) return rc;
     w.q = q; w.k = k; w.v = v; w.d_o = d_o;
     w.p.beta = c.beta; w.p.gate = c.gate;
     w.p.dbeta = c.dbeta; w.p.dgate = c.dgate;

@@ -56,6 +56,7 @@ constexpr int kLtZN = 64;                       // columns of z a CTA owns
 constexpr int kLtGroup = 256;                   // threads of an arithmetic group (two)
 constexpr int kLtThreads = 2 * kLtGroup + 128;  // + two issuers, the decay warp, the loader
 constexpr int kLtTabs = 4;                      // stages of decay tables
+constexpr int kLtTabF = 8 * kLtC + 4;           // floats of a table
 constexpr int kLtDots = 4, kLtFdots = 16;       // planes of dot and fdot partials per pass
 constexpr uint32_t kLtProbes = 1u << 17;
 constexpr uint32_t kLtHintNs = 2000;            // a probe suspends its warp for up to this long
@@ -71,9 +72,8 @@ struct LtSmem {
     static constexpr uint32_t TAB = SOP + 2 * HALF;       // decay tables of the chunks in flight
     // table floats, 128 tokens each: a, u, l (of the row), ta, c[3], and g (backward) or m (l
     // less log2 of the gate, of the column; forward); then b
-    static constexpr uint32_t TABF = 8 * kLtC + 4;
-    static constexpr uint32_t BARS = TAB + kLtTabs * 4 * TABF;
-    static constexpr uint32_t TBASE = BARS + 8 * (18 + 2 * kLtTabs);      // TMEM base, abort flag
+    static constexpr uint32_t BARS = TAB + kLtTabs * 4 * kLtTabF;
+    static constexpr uint32_t TBASE = BARS + 8 * (20 + 2 * kLtTabs);      // TMEM base, abort flag
     static constexpr uint32_t END = TBASE + 16;
     static constexpr size_t bytes = END + 1024;
 };
@@ -83,6 +83,7 @@ struct LinTcPass {
     // past T read as zeros and are not written
     CUtensorMap x, y, z, out;
     LinPass p;
+    const float *tab;             // decay tables of the pass's direction
 };
 struct LinTcArgs {
     LinTcPass pass[2];
@@ -163,6 +164,12 @@ __device__ __forceinline__ bool lt_wait_warp(uint32_t bar, uint32_t parity, uint
     if (__all_sync(0xffffffffu, lt_try(bar, parity))) return true;
     return __all_sync(0xffffffffu, lt_wait_more(bar, parity, abort)) != 0;
 }
+__device__ __forceinline__ void lt_bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
 // After a time-out: a bounded wait for work in flight.
 __device__ __noinline__ void lt_drain(uint32_t bar, uint32_t parity) {
     for (uint32_t i = 0; i < kLtProbes; ++i)
@@ -216,13 +223,31 @@ __device__ __forceinline__ Log2Sum shfl(Log2Sum x, int src) {
     return {__shfl_sync(0xffffffffu, x.hi, src), __shfl_sync(0xffffffffu, x.lo, src)};
 }
 
-// Inclusive sums of the clamped log2 decays of a chunk's four blocks of 32 tokens, by one
-// warp (lane = token of every block; the blocks' scans run side by side).
-__device__ __forceinline__ void lt_scan(const float *bv, float log2_min, Log2Sum *l) {
+// Decay tables of every chunk, a warp each, into tab [B*H][N][kLtTabF] (LtSmem lists a table's
+// parts).  A kernel of its own: formed by a warp of the passes, chunk by chunk, they took 4500
+// to 6300 cycles a chunk (600 instructions that no cache held) and bounded those.
+// grid ceil(B*H*N / 8), block 256.  Lane l holds tokens 32 j + l.
+template <bool REV>
+__global__ void __launch_bounds__(256)
+k_linear_tables(const float *__restrict__ beta, const float *__restrict__ gate, float *__restrict__ tab,
+                int BH, int N, int T, float scale, float log2_min) {
+    griddep_launch_dependents();   // the pass after this one may set itself up meanwhile
     const int lane = threadIdx.x & 31;
+    const long long c = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (c >= (long long)BH * N) return;
+    const int bh = (int)(c / N), n = (int)(c - (long long)bh * N), t0 = n * kLtC + lane;
+    const Log2Sum zero = {0.f, 0.f};
+    float g[4];
+    Log2Sum l[4], e[4], end = zero;   // e[b]: cumulative log at the end of block b
 #pragma unroll
-    for (int j = 0; j < 4; ++j) l[j] = {fmaxf(log2f(bv[j]), log2_min), 0.f};
-#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+        const bool in = t0 + 32 * j < T;   // past the sequence's end: no decay, no write
+        const size_t at = (size_t)bh * T + t0 + 32 * j;
+        const float b = in ? beta[at] : 1.f;
+        g[j] = in ? (gate ? gate[at] : 1.f) : 0.f;
+        l[j] = {fmaxf(log2f(b), log2_min), 0.f};
+    }
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -230,51 +255,34 @@ __device__ __forceinline__ void lt_scan(const float *bv, float log2_min, Log2Sum
             if (lane >= o) l[j] = l[j] + y;
         }
     }
-}
-
-// Decay tables of one chunk by one warp; lane l holds tokens 32 j + l, whose beta and
-// gate are bv[j] and gv[j] (1 and 0 past the sequence's end).  The second part is a loop:
-// the kernel's hot code has to share the instruction caches.
-template <bool REV>
-__device__ __forceinline__ void lt_tables(float *tab, const float *bv, const float *gv, float scale,
-                                          float log2_min) {
-    const int lane = threadIdx.x & 31;
-    float *ta_a = tab + lane, *ta_u = ta_a + kLtC, *ta_l = ta_u + kLtC, *ta_t = ta_l + kLtC,
-          *ta_c = ta_t + kLtC, *ta_gm = ta_c + 3 * kLtC;
-    const Log2Sum zero = {0.f, 0.f};
-    Log2Sum l[4], e[4], end = zero;   // e[b]: cumulative log at the end of block b
-    lt_scan(bv, log2_min, l);
+    float lb[4];   // from the block's start
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const Log2Sum c = end + l[j];
-        ta_l[32 * j] = l[j].hi + l[j].lo;   // from the block's start
-        ta_a[32 * j] = c.hi;                // parked until the loop
-        ta_u[32 * j] = c.lo;
+        const Log2Sum c2 = end + l[j];
+        lb[j] = l[j].hi + l[j].lo;
         end = end + shfl(l[j], 31);
+        l[j] = c2;
         e[j] = end;
     }
-    float g0 = gv[0], g1 = gv[1], g2 = gv[2], g3 = gv[3];
-#pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
-        const int t = 32 * j;
-        const Log2Sum lt = {ta_a[t], ta_u[t]};
-        const float g = g0, lb = ta_l[t];
-        g0 = g1;
-        g1 = g2;
-        g2 = g3;
-        const float to = exp2_diff(lt, zero), from = exp2_diff(end, lt);
-        ta_a[t] = REV ? from : scale * to;
-        ta_u[t] = REV ? scale * to : g * from;
-        ta_gm[t] = REV ? g : lb - log2f(g);   // closed gate: +inf, whose weight is 0
-        const Log2Sum ej = j == 0 ? e[0] : j == 1 ? e[1] : j == 2 ? e[2] : end;
-        ta_t[t] = REV ? exp2_diff(ej, lt) : ex2(lb);
-        // forward: c[b] serves block row b + 1, the blocks before it; backward: block row
-        // b, the blocks after it (the other entries are not read; their exponents are > 0)
+    float *ta = tab + (size_t)c * kLtTabF + lane;
 #pragma unroll
-        for (int b = 0; b < 3; ++b)
-            ta_c[b * kLtC + t] = REV ? exp2_diff(lt, e[b]) : g * exp2_diff(e[b], lt);
+    for (int j = 0; j < 4; ++j) {
+        const float to = exp2_diff(l[j], zero), from = exp2_diff(end, l[j]);
+        const float v[8] = {
+            REV ? from : scale * to,                       // a
+            REV ? scale * to : g[j] * from,                // u
+            lb[j],                                         // l
+            REV ? exp2_diff(e[j], l[j]) : ex2(lb[j]),      // ta
+            // c: forward, c[b] serves block row b + 1, the blocks before it; backward, block row
+            // b, the blocks after it (0 elsewhere, where it is not read)
+            (REV ? j > 0 : j <= 0) ? (REV ? exp2_diff(l[j], e[0]) : g[j] * exp2_diff(e[0], l[j])) : 0.f,
+            (REV ? j > 1 : j <= 1) ? (REV ? exp2_diff(l[j], e[1]) : g[j] * exp2_diff(e[1], l[j])) : 0.f,
+            (REV ? j > 2 : j <= 2) ? (REV ? exp2_diff(l[j], e[2]) : g[j] * exp2_diff(e[2], l[j])) : 0.f,
+            REV ? g[j] : lb[j] - log2f(g[j])};             // g, or m: a closed gate's +inf weighs 0
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ta[i * kLtC + 32 * j] = v[i];
     }
-    if (lane == 0) tab[8 * kLtC] = ex2(end.hi + end.lo);
+    if (lane < 4) ta[8 * kLtC] = lane ? 0.f : ex2(end.hi + end.lo);   // b
 }
 
 // (u z) of item i (16 bytes of a row) in three bf16 parts, 16 KB apart.
@@ -311,7 +319,8 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                    b_os = bars + 40, b_xfree = bars + 48, b_oi = bars + 56;
     const uint32_t b_xy = bars + 64, b_z = bars + 80, b_o = bars + 96, b_out = bars + 112,
                    b_fin = bars + 128;                                                        // [2]
-    const uint32_t b_w = bars + 144, b_tfree = b_w + 8 * kLtTabs;                             // [kLtTabs]
+    const uint32_t b_zfree = bars + 144;                                                      // [2]
+    const uint32_t b_w = bars + 160, b_tfree = b_w + 8 * kLtTabs;                             // [kLtTabs]
     uint32_t *tbase = reinterpret_cast<uint32_t *>(sm + L::TBASE);
     const uint32_t abort = sb + L::TBASE + 4;
     float *s_tab = reinterpret_cast<float *>(sm + L::TAB);
@@ -328,10 +337,11 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             lt_init(b_z + 8 * i, 1);
             lt_init(b_o + 8 * i, 2);    // both issuers': every product of the chunk is done
             lt_init(b_out + 8 * i, 8);
+            lt_init(b_zfree + 8 * i, 1);
             lt_init(b_fin + 8 * i, 1);
         }
         for (int i = 0; i < kLtTabs; ++i) {
-            lt_init(b_w + 8 * i, 32);
+            lt_init(b_w + 8 * i, 1);
             lt_init(b_tfree + 8 * i, 16);
         }
         lt_init(b_p, 1);
@@ -360,6 +370,9 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         if (warp == 1) tc::tmem_dealloc(*tbase, 512);
         return;
     }
+    // Launched as the tables' programmatic dependent, this kernel may read what was there before
+    // those (x, y, z, beta) at once; the tables, the start states and the other direction's states
+    // only after the wait (loader, state warps).
     // TMEM columns; the bf16 weighted scores of each half of the columns lie over its scores
     constexpr uint32_t kP = 0, kOI = 128, kOS = 192, kDS = 256, kX = 448;
     const int quarter = warp & 3;
@@ -414,7 +427,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             lt_drain(b_fin, 0);
         }
         __syncwarp();
-    } else if (warp == 18) {
+    } else if (warp == 17) {
         // ---- issuer of x's copies to TMEM, of the scores P and of OI ----
         const uint64_t d_x = tc::sdesc(sb + L::X, 16, 1024), d_y = tc::sdesc(sb + L::Y, 16, 1024),
                        d_z = tc::sdesc(sb + L::Z, L::HALF, 1024);
@@ -472,40 +485,10 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             lt_drain(b_fin + 8, 0);
         }
         __syncwarp();
-    } else if (warp == 17) {
-        // ---- decay tables, up to kLtTabs chunks ahead ----
-        const float *beta = p.beta + (size_t)bh * p.T;
-        const float *gate = p.gate ? p.gate + (size_t)bh * p.T : nullptr;
-        const float log2_min = (float)(p.log_min * 1.4426950408889634);
-        float bv[4], gv[4];
-        auto fetch = [&](int it) {
-            const int t0 = chunk(it) * C + lane;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool in = t0 + 32 * j < p.T;
-                bv[j] = in ? beta[t0 + 32 * j] : 1.f;
-                gv[j] = in ? (gate ? gate[t0 + 32 * j] : 1.f) : 0.f;
-            }
-        };
-        fetch(0);
-#pragma unroll 1
-        for (int it = 0; it < NL; ++it) {
-            const int ts = it % kLtTabs;
-            if (it >= kLtTabs && !wait(b_tfree + 8 * ts, (it / kLtTabs - 1) & 1)) break;
-            float cb[4], cg[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                cb[j] = bv[j];
-                cg[j] = gv[j];
-            }
-            if (it + 1 < NL) fetch(it + 1);
-            lt_tables<REV>(s_tab + ts * L::TABF, cb, cg, p.scale, log2_min);
-            lt_arrive(b_w + 8 * ts);
-        }
-    } else if (warp == 19) {
-        // ---- loads into freed stages, rows out ----
+    } else if (warp == 18) {
+        // ---- loads into freed stages ----
         if (lane == 0) {
-            int loads_x = 0, loads_y = 0, loads_z = 0;   // begun
+            int loads_x = 0, loads_y = 0, loads_z = 0, loads_t = 0;   // begun
             auto load_x = [&](int it) {
                 const int t0 = chunk(it) * C;
                 lt_expect(b_xy + 8 * (it & 1), L::TILE);
@@ -526,6 +509,13 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 tma_load_3d(sm + L::Z + st * L::HALF, &A.z, zh * kLtZN, chunk(it) * C, bh, b_z + 8 * st);
                 ++loads_z;
             };
+            auto load_tab = [&](int it) {
+                const int ts = it % kLtTabs;
+                lt_expect(b_w + 8 * ts, 4 * kLtTabF);
+                lt_bulk_load(sb + L::TAB + ts * 4 * kLtTabF, A.tab + ((size_t)bh * p.N + chunk(it)) * kLtTabF,
+                             4 * kLtTabF, b_w + 8 * ts);
+                ++loads_t;
+            };
             load_x(0);
             load_y(0);
             load_z(0);
@@ -533,40 +523,59 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 load_y(1);
                 load_z(1);
             }
+            griddep_wait();   // the tables' kernel is done
+            for (int it = 0; it < kLtTabs && it < NL; ++it) load_tab(it);
             bool ok = true;
             if (NL > 1) {
                 ok = lt_wait(b_xfree, 0, abort);
                 if (ok) load_x(1);
             }
 #pragma unroll 1
-            for (int it = 0; ok && it < NL; ++it) {
-                const int st = it & 1, ph2 = (it >> 1) & 1;
-                if (it + 2 < NL) {
-                    ok = lt_wait(b_xfree, (it + 1) & 1, abort);   // x(it + 1) is in TMEM
-                    if (!ok) break;
-                    load_x(it + 2);
-                    ok = lt_wait(b_o + 8 * st, ph2, abort);       // y's readers are done
-                    if (!ok) break;
-                    load_y(it + 2);
-                }
-                // the rows lie where z did, whose next chunk follows them
-                ok = lt_wait(b_out + 8 * st, ph2, abort);
+            for (int it = 0; ok && it + 2 < NL; ++it) {
+                const int st = it & 1, ph2 = (it >> 1) & 1, ts = it % kLtTabs;
+                ok = lt_wait(b_xfree, (it + 1) & 1, abort);   // x(it + 1) is in TMEM
                 if (!ok) break;
-                tma_store_3d(&A.out, zh * kLtZN, chunk(it) * C, bh, sm + L::Z + st * L::HALF);
-                tc::bulk_commit();
-                tc::bulk_wait_read0();
-                if (it + 2 < NL) load_z(it + 2);
+                load_x(it + 2);
+                ok = lt_wait(b_o + 8 * st, ph2, abort);       // y's readers are done
+                if (!ok) break;
+                load_y(it + 2);
+                ok = lt_wait(b_zfree + 8 * st, ph2, abort);   // the rows that lay in z's place are out
+                if (!ok) break;
+                load_z(it + 2);
+                if (it + kLtTabs < NL) {
+                    ok = lt_wait(b_tfree + 8 * ts, (it / kLtTabs) & 1, abort);
+                    if (!ok) break;
+                    load_tab(it + kLtTabs);
+                }
             }
-            tc::bulk_wait0();
             if (!ok) {   // a wait gave up: drain this thread's copies (chunk i's loads on barrier i & 1)
                 for (int i = 0; i < 2; ++i) {
                     const int n = (min(loads_x, loads_y) + 1 - i) / 2, m = (loads_z + 1 - i) / 2;
                     if (n) lt_drain(b_xy + 8 * i, (n - 1) & 1);
                     if (m) lt_drain(b_z + 8 * i, (m - 1) & 1);
                 }
+                for (int i = 0; i < kLtTabs; ++i) {
+                    const int n = (loads_t + kLtTabs - 1 - i) / kLtTabs;
+                    if (n) lt_drain(b_w + 8 * i, (n - 1) & 1);
+                }
                 // a load whose barrier's other half was never begun: time for it to land
                 if (loads_x != loads_y) __nanosleep(1000000);
             }
+        }
+        __syncwarp();
+    } else if (warp == 19) {
+        // ---- rows out ----
+        if (lane == 0) {
+#pragma unroll 1
+            for (int it = 0; it < NL; ++it) {
+                const int st = it & 1;
+                if (!lt_wait(b_out + 8 * st, (it >> 1) & 1, abort)) break;
+                tma_store_3d(&A.out, zh * kLtZN, chunk(it) * C, bh, sm + L::Z + st * L::HALF);
+                tc::bulk_commit();
+                tc::bulk_wait_read0();
+                lt_arrive(b_zfree + 8 * st);
+            }
+            tc::bulk_wait0();
         }
         __syncwarp();
     } else if (warp < 8) {
@@ -577,7 +586,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
 #pragma unroll 1
             for (int it = 0; it < NL; ++it) {
                 const int sg = it & 1, ph = it & 1, ts = it % kLtTabs;
-                const float *tab = s_tab + ts * L::TABF;
+                const float *tab = s_tab + ts * kLtTabF;
                 if (!wait(b_w + 8 * ts, (it / kLtTabs) & 1) || !wait(b_p, ph)) break;
                 tc::fence_after_sync();
                 // 16 columns at a time, in a loop: straight-line code for all of them would not
@@ -692,6 +701,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         };
 #pragma unroll
         for (int j = 0; j < 32; ++j) st[j] = 0.f;
+        griddep_wait();
         if (p.start) {
             const size_t base = ((size_t)bh * p.S + seg) * D * D;
 #pragma unroll
@@ -700,7 +710,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         bool ok = true;
         for (int it = 0; it < NL; ++it) {
             const int sg = it & 1, ph = it & 1, ts = it % kLtTabs, n = chunk(it);
-            const float *tab = s_tab + ts * L::TABF;
+            const float *tab = s_tab + ts * kLtTabF;
             {
                 // the state before the chunk as the B operand, rows of y, two bf16 parts
 #pragma unroll
@@ -779,15 +789,15 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
 // the state leaves by (the last chunk first, or in a backward pass the first), so that every
 // weight is a product of decays down from one, A = sum u_i y_i z_i^T with
 //   u_i = g_i prod_{m > i} beta_m   (backward: c prod_{m <= i} beta_m)
-// over the segment: one product per chunk into the same accumulators, with nothing of the
-// state in between.  Warps 0-15 form the weighted rows (as in k_linear_tc), warp 16 issues,
-// warp 17 forms the weights, warp 18 loads.
+// over the segment (a chunk's u times the decay of the chunks between it and that end): one
+// product per chunk into the same accumulators, with nothing of the state in between.  Warps
+// 0-15 form the weighted rows (as in k_linear_tc), warp 16 issues, warp 18 loads.
 struct LaSmem {
     static constexpr uint32_t Y = 0;                             // 2 stages
     static constexpr uint32_t Z = Y + 2 * LtSmem::TILE;          // 2 stages
     static constexpr uint32_t PARTS = Z + 2 * LtSmem::HALF;      // 2 x hi, mid, lo
-    static constexpr uint32_t U = PARTS + 6 * LtSmem::HALF;      // [2][128]
-    static constexpr uint32_t BARS = U + 2 * 4 * kLtC;
+    static constexpr uint32_t U = PARTS + 6 * LtSmem::HALF;      // 2 x (u, b)
+    static constexpr uint32_t BARS = U + 2 * (4 * kLtC + 16);
     static constexpr uint32_t TBASE = BARS + 8 * (8 + 2);
     static constexpr uint32_t END = TBASE + 16;
     static constexpr size_t bytes = END + 1024;
@@ -802,7 +812,7 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smem_align1024(smraw);
     const uint32_t sb = smem_u32(sm), bars = sb + L::BARS;
-    const uint32_t b_yz = bars, b_parts = bars + 16, b_ds = bars + 32, b_fin = bars + 48, b_w = bars + 56;
+    const uint32_t b_yz = bars, b_parts = bars + 16, b_ds = bars + 32, b_fin = bars + 48;
     uint32_t *tbase = reinterpret_cast<uint32_t *>(sm + L::TBASE);
     const uint32_t abort = sb + L::TBASE + 4;
     float *s_u = reinterpret_cast<float *>(sm + L::U);
@@ -818,7 +828,6 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
             lt_init(b_parts + 8 * i, 16);
             lt_init(b_ds + 8 * i, 1);
         }
-        for (int i = 0; i < 2; ++i) lt_init(b_w + 8 * i, 32);
         lt_init(b_fin, 1);
         asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(0u) : "memory");
         fence_mbar_init();
@@ -860,41 +869,6 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
             lt_drain(b_fin, 0);
         }
         __syncwarp();
-    } else if (warp == 17) {
-        const float *beta = p.beta + (size_t)bh * p.T;
-        const float *gate = p.gate ? p.gate + (size_t)bh * p.T : nullptr;
-        const float log2_min = (float)(p.log_min * 1.4426950408889634);
-        const Log2Sum zero = {0.f, 0.f};
-        Log2Sum far = zero;   // log decay of the chunks between this one and the segment's end
-#pragma unroll 1
-        for (int it = 0; it < NL; ++it) {
-            const int ts = it & 1, t0 = chunk(it) * C + lane;
-            float bv[4], gv[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool in = t0 + 32 * j < p.T;
-                bv[j] = in ? beta[t0 + 32 * j] : 1.f;
-                gv[j] = in ? (gate ? gate[t0 + 32 * j] : 1.f) : 0.f;
-            }
-            // the weights' last readers, chunk it - 2, are done
-            if (it >= 2) ok = done(it - 2);
-            if (!ok) break;
-            Log2Sum l[4], end = zero;
-            lt_scan(bv, log2_min, l);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const Log2Sum c = end + l[j];
-                end = end + shfl(l[j], 31);
-                l[j] = c;
-            }
-            const Log2Sum all = end + far;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                s_u[ts * C + 32 * j + lane] = REV ? p.scale * exp2_diff(far + l[j], zero) : gv[j] * exp2_diff(all, l[j]);
-            far = all;
-            lt_arrive(b_w + 8 * ts);
-        }
-        if (ok && lane == 0 && zh == 0) p.segdec[(size_t)bh * p.S + seg] = exp2_diff(far, zero);
     } else if (warp == 18) {
         if (lane == 0) {
             int loads = 0;
@@ -903,10 +877,14 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
                 const int st = it & 1, t0 = chunk(it) * C;
                 if (it >= 2) ok = lt_wait(b_ds + 8 * st, ((it >> 1) - 1) & 1, abort);
                 if (!ok) break;
-                lt_expect(b_yz + 8 * st, LtSmem::TILE + LtSmem::HALF);
+                lt_expect(b_yz + 8 * st, LtSmem::TILE + LtSmem::HALF + 4 * kLtC + 16);
                 tma_load_3d(sm + L::Z + st * LtSmem::HALF, &A.z, zh * kLtZN, t0, bh, b_yz + 8 * st);
                 tma_load_3d(sm + L::Y + st * LtSmem::TILE, &A.y, 0, t0, bh, b_yz + 8 * st);
                 tma_load_3d(sm + L::Y + st * LtSmem::TILE + LtSmem::HALF, &A.y, 64, t0, bh, b_yz + 8 * st);
+                if (it == 0) griddep_wait();   // the tables' kernel is done
+                const float *tab = A.tab + ((size_t)bh * p.N + chunk(it)) * kLtTabF;
+                lt_bulk_load(sb + L::U + st * (4 * kLtC + 16), tab + kLtC, 4 * kLtC, b_yz + 8 * st);
+                lt_bulk_load(sb + L::U + st * (4 * kLtC + 16) + 4 * kLtC, tab + 8 * kLtC, 16, b_yz + 8 * st);
                 ++loads;
             }
             if (!ok)
@@ -915,23 +893,26 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
         }
         __syncwarp();
     } else if (warp < 16) {
+        float far = 1.f;   // decay of the chunks between this one and the segment's end
 #pragma unroll 1
         for (int it = 0; it < NL; ++it) {
-            const int st = it & 1, ts = st;
-            ok = wait(b_w + 8 * ts, (it >> 1) & 1) && wait(b_yz + 8 * st, (it >> 1) & 1) &&
-                 (it < 2 || done(it - 2));
+            const int st = it & 1;
+            const float *u = s_u + st * (kLtC + 4);
+            ok = wait(b_yz + 8 * st, (it >> 1) & 1) && (it < 2 || done(it - 2));
             if (!ok) break;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int item = tid + i * 512;   // row item / 8
                 lt_parts(sm + L::Z + st * LtSmem::HALF + item * 16, sm + L::PARTS + st * PARTB + item * 16,
-                         s_u[ts * C + (item >> 3)]);
+                         u[item >> 3] * far);
             }
+            far *= u[kLtC];
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) lt_arrive(b_parts + 8 * st);
         }
         if (ok) ok = done(NL - 1);
+        if (ok && tid == 0 && zh == 0) p.segdec[(size_t)bh * p.S + seg] = far;
         if (ok) {
             tc::fence_after_sync();
             const int quarter = warp & 3, cg = warp >> 2, row = quarter * 32 + lane, z0 = zh * kLtZN + cg * 16;
