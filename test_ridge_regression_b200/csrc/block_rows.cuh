@@ -43,19 +43,29 @@ struct Vec16;
 template <>
 struct Vec16<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const float *p, float *x) {
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    static __device__ __forceinline__ void unpack(uint4 v, float *x) {
+        x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
+        x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ void load(const float *p, float *x) { unpack(raw(p), x); }
+    static __device__ __forceinline__ uint4 raw(const float *p) {
+        return __ldg(reinterpret_cast<const uint4 *>(p));
+    }
+    static __device__ __forceinline__ uint4 pack(const float *x) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                          __float_as_uint(x[3]));
     }
     static __device__ __forceinline__ void store(float *p, const float *x) {
-        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<uint4 *>(p) = pack(x);
     }
 };
 template <>
 struct Vec16<__nv_bfloat16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float *x) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+    static __device__ __forceinline__ uint4 raw(const __nv_bfloat16 *p) {
+        return __ldg(reinterpret_cast<const uint4 *>(p));
+    }
+    static __device__ __forceinline__ void unpack(uint4 v, float *x) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -63,14 +73,18 @@ struct Vec16<__nv_bfloat16> {
             x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
+    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float *x) { unpack(raw(p), x); }
     static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *x) {
+        *reinterpret_cast<uint4 *>(p) = pack(x);
+    }
+    static __device__ __forceinline__ uint4 pack(const float *x) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 
@@ -106,9 +120,9 @@ struct TileAt {
     int b, s0, t0;
 };
 template <int R>
-__device__ __forceinline__ TileAt tile_at(const RowTile &g) {
-    const unsigned q = blockIdx.x / g.tcount, b = q / g.scount;
-    return {(int)b, (int)((q - b * g.scount) * (R >> g.tb)), (int)((blockIdx.x - q * g.tcount) << g.tb)};
+__device__ __forceinline__ TileAt tile_at(const RowTile &g, unsigned blk) {
+    const unsigned q = blk / g.tcount, b = q / g.scount;
+    return {(int)b, (int)((q - b * g.scount) * (R >> g.tb)), (int)((blk - q * g.tcount) << g.tb)};
 }
 __device__ __forceinline__ SlotRow tile_row(const RowTile &g, const TileAt &a, int i, int T, int slots) {
     SlotRow s;
@@ -129,10 +143,26 @@ struct BlockInArgs {
     int B, T, H, Hk;
     float eps;
     unsigned row_blocks;   // blocks of the row part; the rest do the gates
-    RowTile tile;
+    RowTile qtile, ktile;
 };
 
-// Slots: 0..H-1 queries, then Hk keys, then Hk values.
+// The block's rows are of one kind, queries, keys or values, each with its own tiles.
+struct KindAt {
+    int kind, heads;   // 0 q, 1 k, 2 v
+    TileAt at;
+};
+template <int R>
+__device__ __forceinline__ KindAt kind_at(const BlockInArgs &a) {
+    KindAt k;
+    unsigned blk = blockIdx.x;
+    const unsigned nq = a.qtile.tcount * a.qtile.scount * a.B, nk = a.ktile.tcount * a.ktile.scount * a.B;
+    k.kind = blk < nq ? 0 : blk < nq + nk ? 1 : 2;
+    blk -= k.kind == 0 ? 0 : k.kind == 1 ? nq : nq + nk;
+    k.heads = k.kind ? a.Hk : a.H;
+    k.at = tile_at<R>(k.kind ? a.ktile : a.qtile, blk);
+    return k;
+}
+
 // grid: row_blocks blocks of rows (RPT rows a lane group), then ceil(B*H*T / 256)
 // blocks of gates.
 template <typename T, int D, int RPT>
@@ -141,7 +171,6 @@ k_block_in(const BlockInArgs a, T *__restrict__ qo, T *__restrict__ ko, T *__res
            float *__restrict__ beta, float *__restrict__ gate) {
     using V = Vec16<T>;
     constexpr int LPR = D / V::N, GROUPS = kRowThreads / LPR;
-    const int slots = a.H + 2 * a.Hk;
     if (blockIdx.x >= a.row_blocks) {
         // gates: beta = sigmoid(logit + bias), padding keeps the state (beta 1, gate 0)
         const size_t n = (size_t)a.B * a.H * a.T;
@@ -165,40 +194,39 @@ k_block_in(const BlockInArgs a, T *__restrict__ qo, T *__restrict__ ko, T *__res
         }
         return;
     }
-    const int lane = threadIdx.x % LPR, rep = a.H / a.Hk, grp = threadIdx.x / LPR;
-    const TileAt at = tile_at<GROUPS * RPT>(a.tile);
-    const int len = a.lengths ? min(a.lengths[at.b], a.T) : a.T;
-    float x[RPT][V::N];
+    const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+    const KindAt k = kind_at<GROUPS * RPT>(a);
+    const RowTile &tile = k.kind ? a.ktile : a.qtile;
+    const StridedRows &in = k.kind == 0 ? a.q : k.kind == 1 ? a.k : a.v;
+    T *out = k.kind == 0 ? qo : k.kind == 1 ? ko : vo;
+    const T *src = static_cast<const T *>(in.ptr) + k.at.b * in.sb + lane * V::N;
+    const int rep = k.kind ? a.H / a.Hk : 1;
+    const int len = a.lengths ? min(a.lengths[k.at.b], a.T) : a.T;
+    uint4 x[RPT];
     // every load of the group's rows goes out before the first sum
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
-        const SlotRow s = tile_row(a.tile, at, grp + j * GROUPS, a.T, slots);
-#pragma unroll
-        for (int i = 0; i < V::N; ++i) x[j][i] = 0.f;
-        if (!s.in || s.t >= len) continue;
-        const StridedRows &in = s.slot < a.H ? a.q : s.slot < a.H + a.Hk ? a.k : a.v;
-        const int h = s.slot < a.H ? s.slot : (s.slot - a.H) % a.Hk;
-        V::load(static_cast<const T *>(in.ptr) + s.b * in.sb + s.t * in.st + h * in.sh +
-                    lane * V::N, x[j]);
+        const SlotRow s = tile_row(tile, k.at, grp + j * GROUPS, len, k.heads);
+        x[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (s.in) x[j] = V::raw(src + s.t * in.st + s.slot * in.sh);
     }
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
-        const SlotRow s = tile_row(a.tile, at, grp + j * GROUPS, a.T, slots);
-        float ss = 0.f;
+        const SlotRow s = tile_row(tile, k.at, grp + j * GROUPS, a.T, k.heads);
+        uint4 y = x[j];
+        if (k.kind < 2) {   // values pass as they are
+            float f[V::N], ss = 0.f;
+            V::unpack(y, f);
 #pragma unroll
-        for (int i = 0; i < V::N; ++i) ss = fmaf(x[j][i], x[j][i], ss);
-        ss = row_sum<LPR>(ss);
-        if (!s.in) continue;
-        if (s.slot < a.H + a.Hk) {
-            const float rn = rsqrtf(ss + a.eps);
+            for (int i = 0; i < V::N; ++i) ss = fmaf(f[i], f[i], ss);
+            const float rn = rsqrtf(row_sum<LPR>(ss) + a.eps);
 #pragma unroll
-            for (int i = 0; i < V::N; ++i) x[j][i] *= rn;
+            for (int i = 0; i < V::N; ++i) f[i] *= rn;
+            y = V::pack(f);
         }
-        const bool is_q = s.slot < a.H;
-        T *out = is_q ? qo : s.slot < a.H + a.Hk ? ko : vo;
-        const int h0 = is_q ? s.slot : ((s.slot - a.H) % a.Hk) * rep, nh = is_q ? 1 : rep;
-        for (int h = h0; h < h0 + nh; ++h)
-            V::store(out + (((size_t)s.b * a.H + h) * a.T + s.t) * D + lane * V::N, x[j]);
+        if (!s.in) continue;
+        T *dst = out + (((size_t)k.at.b * a.H + s.slot * rep) * a.T + s.t) * D + lane * V::N;
+        for (int h = 0; h < rep; ++h, dst += (size_t)a.T * D) *reinterpret_cast<uint4 *>(dst) = y;
     }
 }
 
@@ -218,7 +246,7 @@ __global__ void __launch_bounds__(kRowThreads)
 k_block_in_grad(const BlockInArgs a, const BlockInGrad g) {
     using V = Vec16<T>;
     constexpr int LPR = D / V::N, GROUPS = kRowThreads / LPR;
-    const int slots = a.H + 2 * a.Hk, lane = threadIdx.x % LPR;
+    const int lane = threadIdx.x % LPR;
     if (blockIdx.x >= a.row_blocks) {
         const unsigned id = blockIdx.x - a.row_blocks;
         const int h = (int)(id / (unsigned)g.gblk), part = (int)(id % (unsigned)g.gblk);
@@ -273,54 +301,52 @@ k_block_in_grad(const BlockInArgs a, const BlockInGrad g) {
         }
         return;
     }
-    const int rep = a.H / a.Hk, grp = threadIdx.x / LPR;
-    const TileAt at = tile_at<GROUPS * RPT>(a.tile);
-    const int len = a.lengths ? min(a.lengths[at.b], a.T) : a.T;
-    float x[RPT][V::N], dy[RPT][V::N];
+    const int grp = threadIdx.x / LPR;
+    const KindAt k = kind_at<GROUPS * RPT>(a);
+    const RowTile &tile = k.kind ? a.ktile : a.qtile;
+    const StridedRows &in = k.kind ? a.k : a.q;
+    const T *src = static_cast<const T *>(in.ptr) + k.at.b * in.sb + lane * V::N;
+    const T *up = static_cast<const T *>(k.kind == 0 ? g.dq : k.kind == 1 ? g.dk : g.dv) + lane * V::N;
+    T *out = static_cast<T *>(k.kind == 0 ? g.xq : k.kind == 1 ? g.xk : g.xv) + lane * V::N;
+    const int rep = k.kind ? a.H / a.Hk : 1;
+    const int len = a.lengths ? min(a.lengths[k.at.b], a.T) : a.T;
+    uint4 x[RPT];
+    float dy[RPT][V::N];
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
-        const SlotRow s = tile_row(a.tile, at, grp + j * GROUPS, a.T, slots);
+        const SlotRow s = tile_row(tile, k.at, grp + j * GROUPS, len, k.heads);
+        x[j] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int i = 0; i < V::N; ++i) x[j][i] = dy[j][i] = 0.f;
-        if (!s.in || s.t >= len) continue;
-        const bool is_q = s.slot < a.H, unit = s.slot < a.H + a.Hk;
-        const int h = is_q ? s.slot : (s.slot - a.H) % a.Hk;
-        if (unit) {
-            const StridedRows &in = is_q ? a.q : a.k;
-            V::load(static_cast<const T *>(in.ptr) + s.b * in.sb + s.t * in.st + h * in.sh +
-                        lane * V::N, x[j]);
-        }
+        for (int i = 0; i < V::N; ++i) dy[j][i] = 0.f;
+        if (!s.in) continue;
+        if (k.kind < 2) x[j] = V::raw(src + s.t * in.st + s.slot * in.sh);
         // a shared key or value head collects the gradients of its group
-        const T *up = static_cast<const T *>(is_q ? g.dq : unit ? g.dk : g.dv);
-        const int h0 = is_q ? h : h * rep, nh = is_q ? 1 : rep;
-        for (int hh = h0; hh < h0 + nh; ++hh) {
+        const T *u = up + (((size_t)k.at.b * a.H + s.slot * rep) * a.T + s.t) * D;
+        for (int h = 0; h < rep; ++h, u += (size_t)a.T * D) {
             float d[V::N];
-            V::load(up + (((size_t)s.b * a.H + hh) * a.T + s.t) * D + lane * V::N, d);
+            V::load(u, d);
 #pragma unroll
             for (int i = 0; i < V::N; ++i) dy[j][i] += d[i];
         }
     }
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
-        const SlotRow s = tile_row(a.tile, at, grp + j * GROUPS, a.T, slots);
-        float ss = 0.f, xd = 0.f;
+        const SlotRow s = tile_row(tile, k.at, grp + j * GROUPS, a.T, k.heads);
+        if (k.kind < 2) {
+            float f[V::N], ss = 0.f, xd = 0.f;
+            V::unpack(x[j], f);
 #pragma unroll
-        for (int i = 0; i < V::N; ++i) {
-            ss = fmaf(x[j][i], x[j][i], ss);
-            xd = fmaf(x[j][i], dy[j][i], xd);
-        }
-        ss = row_sum<LPR>(ss);
-        xd = row_sum<LPR>(xd);
-        if (!s.in) continue;
-        const bool is_q = s.slot < a.H, unit = s.slot < a.H + a.Hk;
-        if (unit) {
+            for (int i = 0; i < V::N; ++i) {
+                ss = fmaf(f[i], f[i], ss);
+                xd = fmaf(f[i], dy[j][i], xd);
+            }
+            ss = row_sum<LPR>(ss);
+            xd = row_sum<LPR>(xd);
             const float rn = rsqrtf(ss + a.eps), c = rn * rn * xd;   // r (dy - r x (r x . dy))
 #pragma unroll
-            for (int i = 0; i < V::N; ++i) dy[j][i] = rn * (dy[j][i] - c * x[j][i]);
+            for (int i = 0; i < V::N; ++i) dy[j][i] = rn * (dy[j][i] - c * f[i]);
         }
-        const int heads = is_q ? a.H : a.Hk, h = is_q ? s.slot : (s.slot - a.H) % a.Hk;
-        T *out = static_cast<T *>(is_q ? g.xq : unit ? g.xk : g.xv);
-        V::store(out + (((size_t)s.b * a.T + s.t) * heads + h) * D + lane * V::N, dy[j]);
+        if (s.in) V::store(out + (((size_t)k.at.b * a.T + s.t) * k.heads + s.slot) * D, dy[j]);
     }
 }
 
@@ -364,7 +390,7 @@ k_block_out(const BlockOutArgs a, T *__restrict__ y) {
     using V = Vec16<T>;
     constexpr int LPR = D / V::N, GROUPS = kRowThreads / LPR;
     const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR;
-    const TileAt at = tile_at<GROUPS * RPT>(a.tile);
+    const TileAt at = tile_at<GROUPS * RPT>(a.tile, blockIdx.x);
     float w[V::N];
 #pragma unroll
     for (int i = 0; i < V::N; ++i) w[i] = a.w[lane * V::N + i];
@@ -437,28 +463,42 @@ k_block_out_grad(const BlockOutArgs a, const BlockOutGrad g) {
     const int rounds = (int)((e1 - e0 + GROUPS - 1) / GROUPS);
     size_t b = (e0 + grp) / (unsigned)a.T;
     unsigned t = (unsigned)(e0 + grp - b * (unsigned)a.T);
-    for (int k = 0; k < rounds; ++k, t += GROUPS) {
+    // the next round's rows are on their way while this one's are worked on
+    struct Rows {
+        uint4 o, v, z, dy;
+    } nx;
+    size_t hm, tm;
+    bool in;
+    auto fetch = [&](int k) {
         if (t >= (unsigned)a.T) {
             const unsigned q = t / (unsigned)a.T;
             b += q;
             t -= q * (unsigned)a.T;
         }
-        const size_t e = e0 + (size_t)k * GROUPS + grp, ec = b * (unsigned)a.T + t;
-        const bool in = e < e1;
-        const size_t hm = ((b * a.H + h) * a.T + t) * D + lane * V::N;
-        const size_t tm = (ec * a.H + h) * D + lane * V::N;
-        float u[V::N], v[V::N], z[V::N], dy[V::N];
+        in = e0 + (size_t)k * GROUPS + grp < e1;
+        hm = ((b * a.H + h) * a.T + t) * D + lane * V::N;
+        tm = ((b * (unsigned)a.T + t) * a.H + h) * D + lane * V::N;
+        nx.o = nx.v = nx.z = nx.dy = make_uint4(0u, 0u, 0u, 0u);
         if (in) {
-            V::load(static_cast<const T *>(a.o) + hm, u);
-            V::load(static_cast<const T *>(g.dy) + tm, dy);
-            if (a.v) V::load(static_cast<const T *>(a.v) + hm, v);
+            nx.o = V::raw(static_cast<const T *>(a.o) + hm);
+            nx.dy = V::raw(static_cast<const T *>(g.dy) + tm);
+            if (a.v) nx.v = V::raw(static_cast<const T *>(a.v) + hm);
             if (a.z.ptr)
-                V::load(static_cast<const T *>(a.z.ptr) + b * a.z.sb + t * a.z.st + h * a.z.sh +
-                            lane * V::N, z);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V::N; ++i) u[i] = v[i] = z[i] = dy[i] = 0.f;
+                nx.z = V::raw(static_cast<const T *>(a.z.ptr) + b * a.z.sb + t * a.z.st + h * a.z.sh +
+                              lane * V::N);
         }
+        t += GROUPS;
+    };
+    if (rounds > 0) fetch(0);
+    for (int k = 0; k < rounds; ++k) {
+        float u[V::N], v[V::N], z[V::N], dy[V::N];
+        V::unpack(nx.o, u);
+        V::unpack(nx.v, v);
+        V::unpack(nx.z, z);
+        V::unpack(nx.dy, dy);
+        const size_t hm0 = hm, tm0 = tm;
+        const bool in0 = in;
+        if (k + 1 < rounds) fetch(k + 1);
         if (a.v) {
 #pragma unroll
             for (int i = 0; i < V::N; ++i) u[i] = fmaf(sk, v[i], u[i]);
@@ -486,16 +526,16 @@ k_block_out_grad(const BlockOutArgs a, const BlockOutGrad g) {
         dot = row_sum<LPR>(dot) * (1.f / D);
 #pragma unroll
         for (int i = 0; i < V::N; ++i) dy[i] = rn * (dy[i] - u[i] * dot);   // du
-        if (!in) continue;
-        V::store(static_cast<T *>(g.d_o) + hm, dy);
-        if (a.z.ptr) V::store(static_cast<T *>(g.dz) + tm, z);
+        if (!in0) continue;
+        V::store(static_cast<T *>(g.d_o) + hm0, dy);
+        if (a.z.ptr) V::store(static_cast<T *>(g.dz) + tm0, z);
         if (a.v) {
 #pragma unroll
             for (int i = 0; i < V::N; ++i) {
                 ds = fmaf(dy[i], v[i], ds);
                 dy[i] *= sk;
             }
-            V::store(static_cast<T *>(g.dv) + hm, dy);
+            V::store(static_cast<T *>(g.dv) + hm0, dy);
         }
     }
     __shared__ float red[GROUPS][D];

@@ -406,6 +406,10 @@ static size_t row_tiles(int R, int B, int T, int slots, RowTile *g) {
     g->scount = (unsigned)((slots + (R >> tb) - 1) / (R >> tb));
     return (size_t)B * g->scount * g->tcount;
 }
+// Blocks of the block_in rows: queries, then keys, then values.
+static unsigned in_blocks(int R, int B, int T, int H, int Hk, BlockInArgs *a) {
+    return (unsigned)(row_tiles(R, B, T, H, &a->qtile) + 2 * row_tiles(R, B, T, Hk, &a->ktile));
+}
 template <typename T, int D>
 constexpr int rows_per_block(int rpt) {
     return kRowThreads / (D / Vec16<T>::N) * rpt;
@@ -556,7 +560,7 @@ int gka_block_in_forward(const gka_strided *q, const gka_strided *k, const gka_s
     return by_type(dt, D, [&](auto tag, auto d) {
         using Tin = decltype(tag);
         constexpr int DD = decltype(d)::value, RPT = 4;
-        a.row_blocks = (unsigned)row_tiles(rows_per_block<Tin, DD>(RPT), B, T, H + 2 * Hk, &a.tile);
+        a.row_blocks = in_blocks(rows_per_block<Tin, DD>(RPT), B, T, H, Hk, &a);
         const size_t gates = (n + kRowThreads - 1) / kRowThreads;
         ProfScope ps(GKA_KERNEL_BLOCK_ROWS, s);
         k_block_in<Tin, DD, RPT><<<(unsigned)(a.row_blocks + gates), kRowThreads, 0, s>>>(
@@ -617,7 +621,7 @@ int gka_block_in_backward(const gka_strided *q, const gka_strided *k,
     return by_type(dt, D, [&](auto tag, auto d) {
         using Tin = decltype(tag);
         constexpr int DD = decltype(d)::value, RPT = 2;
-        a.row_blocks = (unsigned)row_tiles(rows_per_block<Tin, DD>(RPT), B, T, H + 2 * Hk, &a.tile);
+        a.row_blocks = in_blocks(rows_per_block<Tin, DD>(RPT), B, T, H, Hk, &a);
         {
             ProfScope ps(GKA_KERNEL_BLOCK_ROWS, s);
             k_block_in_grad<Tin, DD, RPT>
