@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace gka {
 
@@ -244,6 +245,7 @@ struct BlockInGrad {
 template <typename T, int D, int RPT>
 __global__ void __launch_bounds__(kRowThreads)
 k_block_in_grad(const BlockInArgs a, const BlockInGrad g) {
+    griddep_launch_dependents();
     using V = Vec16<T>;
     constexpr int LPR = D / V::N, GROUPS = kRowThreads / LPR;
     const int lane = threadIdx.x % LPR;
@@ -350,26 +352,27 @@ k_block_in_grad(const BlockInArgs a, const BlockInGrad g) {
     }
 }
 
-// out[i] = sum of part[i][0..n), one block per output, in a fixed order.  The first
-// n0 outputs go to out0, the others to out1 (either nullable).
-__global__ void __launch_bounds__(128)
-k_block_sums(const float *__restrict__ part, int n, int n0, float *__restrict__ out0,
-             float *__restrict__ out1) {
+// out[i] = sum of part[i][0..n), i < count, one block per output, in a fixed order; two such
+// arrays (the second's count may be 0, either's out NULL).  grid count0 + count1, launched as
+// the programmatic dependent of the kernel that writes the parts.
+struct SumsOf {
+    const float *part;
+    int count, n;
+    float *out;
+};
+__global__ void __launch_bounds__(128) k_block_sums(const SumsOf a, const SumsOf b) {
     __shared__ float red[4];
-    float s = 0.f;
-    for (int i = threadIdx.x; i < n; i += 128) s += part[(size_t)blockIdx.x * n + i];
-    s = warp_sum(s);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    griddep_wait();
+    const bool first = (int)blockIdx.x < a.count;
+    const SumsOf &s = first ? a : b;
+    const int i = (int)blockIdx.x - (first ? 0 : a.count);
+    if (!s.out) return;
+    float x = 0.f;
+    for (int e = threadIdx.x; e < s.n; e += 128) x += s.part[(size_t)i * s.n + e];
+    x = warp_sum(x);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        s = red[0] + red[1] + red[2] + red[3];
-        const int i = blockIdx.x;
-        if (i < n0) {
-            if (out0) out0[i] = s;
-        } else if (out1) {
-            out1[i - n0] = s;
-        }
-    }
+    if (threadIdx.x == 0) s.out[i] = red[0] + red[1] + red[2] + red[3];
 }
 
 // ---------------------------------------------------------------------------
@@ -446,6 +449,7 @@ struct BlockOutGrad {
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads)
 k_block_out_grad(const BlockOutArgs a, const BlockOutGrad g) {
+    griddep_launch_dependents();
     using V = Vec16<T>;
     constexpr int LPR = D / V::N, GROUPS = kRowThreads / LPR;
     const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR, h = blockIdx.y;

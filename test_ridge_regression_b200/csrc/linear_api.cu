@@ -19,6 +19,26 @@ constexpr int kSms = 148;   // SMs of the one GPU this library is built for
 
 static bool valid_dtype(gka_dtype dt) { return dt == GKA_F32 || dt == GKA_BF16; }
 
+// Launches `kern` as the programmatic dependent of the kernel before it (`pdl`): it may set
+// itself up while that one ends, and waits for it on the device.
+template <typename K, typename... Args>
+static int launch_after(K kern, dim3 grid, int threads, size_t smem, bool pdl, cudaStream_t s, Args... args) {
+    cudaError_t e;
+    if (smem && (e = set_smem(kern, smem)) != cudaSuccess) return cuda_fail(e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    if ((e = cudaLaunchKernelEx(&cfg, kern, args...)) != cudaSuccess) return cuda_fail(e);
+    return GKA_OK;
+}
+
 // ---------------------------------------------------------------------------
 // Gated linear recurrence
 // ---------------------------------------------------------------------------
@@ -72,12 +92,9 @@ static int lin_layout(int B, int H, int T, int D, gka_dtype dt, bool bwd, LinLay
 
 template <typename T, int D, bool REV, bool OUT>
 static int lin_launch(const LinPass &p, int ZS, int prof, cudaStream_t s) {
-    cudaError_t e;
-    auto kern = k_linear_pass<T, D, REV, OUT>;
-    if ((e = set_smem(kern, LinSmem<D>::bytes)) != cudaSuccess) return cuda_fail(e);
     ProfScope ps(prof, s);
-    kern<<<dim3(ZS, p.BH, p.S), kLinThreads, LinSmem<D>::bytes, s>>>(p);
-    return check_launch();
+    return launch_after(k_linear_pass<T, D, REV, OUT>, dim3(ZS, p.BH, p.S), kLinThreads, LinSmem<D>::bytes, true,
+                        s, p);
 }
 
 // Segment starts for a pass (p.S > 1): aggregates, then their scan from `init`.
@@ -92,10 +109,9 @@ static int lin_starts(LinPass &p, const LinLayout &L, char *ws, const float *ini
     p.segdec = reinterpret_cast<float *>(ws + L.segdec);
     if (int rc = lin_launch<T, D, REV, false>(p, L.ZS, prof, s)) return rc;
     ProfScope ps(prof, s);
-    k_linear_scan<<<dim3((D * D + 1023) / 1024, p.BH), 256, 0, s>>>(p.agg, p.segdec, init, L.S,
-                                                                  D * D, REV);
     p.start = p.agg;
-    return check_launch();
+    return launch_after(k_linear_scan, dim3((D * D + 1023) / 1024, p.BH), 256, 0, true, s, p.agg,
+                        (const float *)p.segdec, init, L.S, D * D, (int)REV);
 }
 
 struct LinCall {
@@ -116,7 +132,7 @@ static int lin_forward(const LinCall &c, const LinLayout &L) {
     p.out = c.o;
     p.beta = c.beta; p.gate = c.gate;
     p.scale = c.scale;
-    p.log_min = kLogBetaMin;
+    p.log2_min = kLinLog2Min;
     p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S;
     p.zy = 1;
     if (int rc = lin_starts<T, D, false>(p, L, c.ws, c.init, GKA_KERNEL_LINEAR, c.s)) return rc;
@@ -134,7 +150,7 @@ static int lin_backward(const LinCall &c, const LinLayout &L) {
     LinPass p = {};
     p.beta = c.beta; p.gate = c.gate;
     p.scale = c.scale;
-    p.log_min = kLinLogMinBwd;
+    p.log2_min = kLinLog2MinBwd;
     p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S;
     // dq, forwards in time; M before every chunk stays for F
     LinPass f = p;
@@ -171,12 +187,8 @@ static int lin_backward(const LinCall &c, const LinLayout &L) {
     w.dbeta = c.dbeta; w.dgate = c.dgate;
     w.scale = c.scale;
     w.BH = c.BH; w.T = c.T; w.N = L.N; w.ZS = L.ZS;
-    cudaError_t e;
-    auto kern = k_linear_pairs<T, D>;
-    if ((e = set_smem(kern, lin_pairs_smem<D>())) != cudaSuccess) return cuda_fail(e);
     ProfScope ps(kProf, c.s);
-    kern<<<dim3(L.N, c.BH), kLinThreads, lin_pairs_smem<D>(), c.s>>>(w);
-    return check_launch();
+    return launch_after(k_linear_pairs<T, D>, dim3(L.N, c.BH), kLinThreads, lin_pairs_smem<D>(), true, c.s, w);
 }
 
 // ---------------------------------------------------------------------------
@@ -197,26 +209,6 @@ static int head_map(CUtensorMap *m, const void *base, int T, int BH) {
     return r == CUDA_SUCCESS ? GKA_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
-// Launches `kern` as the programmatic dependent of the kernel before it (`pdl`): it may set
-// itself up while that one ends, and waits for it on the device.
-template <typename K, typename... Args>
-static int launch_after(K kern, dim3 grid, int threads, size_t smem, bool pdl, cudaStream_t s, Args... args) {
-    cudaError_t e;
-    if ((e = set_smem(kern, smem)) != cudaSuccess) return cuda_fail(e);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
-    if ((e = cudaLaunchKernelEx(&cfg, kern, args...)) != cudaSuccess) return cuda_fail(e);
-    return GKA_OK;
-}
-
 // Every chunk's decay tables for one direction, into the workspace.
 template <bool REV>
 static int lin_tc_tables(LinTcArgs &a, int passes, const LinLayout &L, char *ws, int prof, cudaStream_t s) {
@@ -225,9 +217,8 @@ static int lin_tc_tables(LinTcArgs &a, int passes, const LinLayout &L, char *ws,
     for (int i = 0; i < passes; ++i) a.pass[i].tab = tab;
     const long long chunks = (long long)p.BH * L.N;
     ProfScope ps(prof, s);
-    k_linear_tables<REV><<<(unsigned)((chunks + 7) / 8), 256, 0, s>>>(
-        p.beta, p.gate, tab, p.BH, L.N, p.T, p.scale, (float)(p.log_min * 1.4426950408889634));
-    return check_launch();
+    return launch_after(k_linear_tables<REV>, dim3((unsigned)((chunks + 7) / 8)), 256, 0, true, s, p.beta, p.gate,
+                        tab, p.BH, L.N, p.T, p.scale, p.log2_min);
 }
 
 // `pdl`: the kernel before is the tables'.
@@ -259,9 +250,9 @@ static int lin_tc_starts(LinTcArgs &a, const LinLayout &L, char *ws, const float
             return rc;
     }
     ProfScope ps(prof, s);
-    k_linear_scan<<<dim3(16, p.BH), 256, 0, s>>>(p.agg, p.segdec, init, L.S, 128 * 128, REV);
     p.start = p.agg;
-    return check_launch();
+    return launch_after(k_linear_scan, dim3(16, p.BH), 256, 0, false, s, p.agg, (const float *)p.segdec, init,
+                        L.S, 128 * 128, (int)REV);
 }
 
 static int lin_tc_forward(const LinCall &c, const LinLayout &L) {
@@ -273,7 +264,7 @@ static int lin_tc_forward(const LinCall &c, const LinLayout &L) {
     LinPass &p = a.pass[0].p;
     p.beta = c.beta; p.gate = c.gate;
     p.scale = c.scale;
-    p.log_min = kLogBetaMin;
+    p.log2_min = kLinLog2Min;
     p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S;
     p.zy = 1;
     if (int rc = lin_tc_tables<false>(a, 1, L, c.ws, GKA_KERNEL_LINEAR, c.s)) return rc;
@@ -292,7 +283,7 @@ static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
     LinPass p = {};
     p.beta = c.beta; p.gate = c.gate;
     p.scale = c.scale;
-    p.log_min = kLinLogMinBwd;
+    p.log2_min = kLinLog2MinBwd;
     p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S;
     LinPairsTc w = {};
     w.p.zeta = reinterpret_cast<float *>(c.ws + L.zeta);
@@ -336,13 +327,10 @@ static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
     w.p.scale = c.scale;
     w.p.BH = c.BH; w.p.T = c.T; w.p.N = L.N; w.p.ZS = L.dots;
     w.FS = L.fdots;
-    cudaError_t e;
     int *flag = nullptr;
     if (int rc = timeout_flag_ptr(&flag)) return rc;
-    if ((e = set_smem(k_linear_pairs_tc, LpSmem::bytes)) != cudaSuccess) return cuda_fail(e);
     ProfScope ps(kProf, c.s);
-    k_linear_pairs_tc<<<dim3(L.N, c.BH), kLpThreads, LpSmem::bytes, c.s>>>(w, flag);
-    return check_launch();
+    return launch_after(k_linear_pairs_tc, dim3(L.N, c.BH), kLpThreads, LpSmem::bytes, true, c.s, w, flag);
 }
 
 // f(type tag, size tag) for the call's type and head size.
@@ -630,8 +618,9 @@ int gka_block_in_backward(const gka_strided *q, const gka_strided *k,
         if (int rc = check_launch()) return rc;
         if (!dbeta_bias && !dgate_bias) return (int)GKA_OK;
         ProfScope ps(GKA_KERNEL_BLOCK_ROWS, s);
-        k_block_sums<<<dgate_bias ? 2 * H : H, 128, 0, s>>>(g.part, g.gblk, H, dbeta_bias, dgate_bias);
-        return check_launch();
+        const SumsOf db = {g.part, H, g.gblk, dbeta_bias};
+        const SumsOf dg = {g.part + (size_t)H * g.gblk, dgate_bias ? H : 0, g.gblk, dgate_bias};
+        return launch_after(k_block_sums, dim3(db.count + dg.count), 128, 0, true, s, db, dg);
     });
 }
 
@@ -711,9 +700,8 @@ int gka_block_out_backward(const void *o, const void *v, const gka_strided *z, c
         }
         if (int rc = check_launch()) return rc;
         ProfScope ps(GKA_KERNEL_BLOCK_ROWS, s);
-        k_block_sums<<<D, 128, 0, s>>>(g.wpart, H * g.blk, D, dw, nullptr);
-        if (v) k_block_sums<<<H, 128, 0, s>>>(g.spart, g.blk, H, dskip, nullptr);
-        return check_launch();
+        const SumsOf sw = {g.wpart, D, H * g.blk, dw}, ss = {g.spart, v ? H : 0, g.blk, dskip};
+        return launch_after(k_block_sums, dim3(sw.count + ss.count), 128, 0, true, s, sw, ss);
     });
 }
 

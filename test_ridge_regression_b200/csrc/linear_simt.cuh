@@ -18,7 +18,7 @@
 //     dq      do  v   k   forward   e^{l_t}          e^{l_t - l_i} g_i    e^{l_C - l_i} g_i
 //     dv      k   q   do  backward  e^{l_C - l_t}    e^{l_i - l_t} c      e^{l_i} c
 //     dk      v   do  q   backward  e^{l_C - l_t}    e^{l_i - l_t} c      e^{l_i} c
-// with l the cumulative log decay inside the chunk (summed in double, so that a
+// with l the cumulative log decay inside the chunk (a sum of two floats, so that a
 // difference keeps fp32 precision after a reset) and the sum over i <= t
 // (forward) or i >= t (backward).  o and dq are scaled by c at the end, dk and dv
 // by g_t.  S runs along the sequence in fp32; a CTA owns ZN columns of z for one
@@ -30,7 +30,7 @@
 // over the chunk of t, where F = e^{l_C} <E, M_s> (write before, read behind the
 // chunk), zeta_s = q_s . (state part of dq_s) and eta_i = v_i . (state part of
 // dv_i / g_i).  No term cancels another, and every one holds the factor beta_t, so
-// the quotient is as exact as the terms; log beta is clamped at kLinLogMinBwd in
+// the quotient is as exact as the terms; log beta is clamped at 2^-60 in
 // the backward for that quotient to exist at beta = 0 (a reset), where what the
 // clamp lets through is below 2^-60 of what was written.  dg_i = eta_i plus the
 // pair terms' column sums.  The passes leave zeta, eta and F in the workspace and
@@ -41,14 +41,41 @@
 
 #include "block_rows.cuh"
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace gka {
 
 constexpr int kLinC = 32;         // tokens per chunk of the CUDA-core pass
 constexpr int kLinZN = 32;        // columns of z a CTA owns
 constexpr int kLinThreads = 256;
-// exp(-41.59) = 2^-60: the smallest decay the backward tells from zero
-constexpr double kLinLogMinBwd = -41.588830833596715;
+// Clamps of log2 beta: in the forward, below every fp32 product (a reset passes exactly
+// nothing); 2^-60 is the smallest decay the backward tells from zero.
+constexpr float kLinLog2Min = -216.f, kLinLog2MinBwd = -60.f;
+
+// A sum of log decays as an unevaluated pair of floats (about 45 bits): differences of
+// cumulative logs keep fp32 precision after a reset, at a fraction of doubles' latency.
+struct Log2Sum {
+    float hi, lo;
+};
+__device__ __forceinline__ Log2Sum operator+(Log2Sum a, Log2Sum b) {
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
+    const float h = s + e;
+    return {h, e - (h - s)};
+}
+// 2^x, results below 2^-126 as zero (relative error 2^-22: the hardware's function)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 2^(a - b)
+__device__ __forceinline__ float exp2_diff(Log2Sum a, Log2Sum b) {
+    return ex2((a.hi - b.hi) + (a.lo - b.lo));
+}
+__device__ __forceinline__ Log2Sum shfl(Log2Sum x, int src) {
+    return {__shfl_sync(0xffffffffu, x.hi, src), __shfl_sync(0xffffffffu, x.lo, src)};
+}
 
 struct LinPass {
     const void *x, *y, *z;        // [B*H, T, D]
@@ -63,7 +90,7 @@ struct LinPass {
     float *dot;                   // [ZS][B*H*T]
     float *fdot;                  // [ZS][B*H*N]
     float scale;
-    double log_min;               // clamp of log beta
+    float log2_min;               // clamp of log2 beta
     int BH, T, N, S;
     int zy;                       // a state's memory is [z][y] (else [y][z])
 };
@@ -79,42 +106,51 @@ struct LinSmem {
     static constexpr int LD = D + 4;
     static constexpr int floats = 2 * kLinC * LD + 2 * kLinC * kLinZN + D * kLinZN +
                                   kLinC * (kLinC + 1) + 3 * kLinC + 8;
-    static constexpr size_t bytes = sizeof(double) * kLinC + sizeof(float) * floats;
+    static constexpr size_t bytes = sizeof(Log2Sum) * kLinC + sizeof(float) * floats;
 };
 
-// Chunk n's tile of rows as floats (rows past T: zeros): [kLinC][ld] from [T][D] at
-// column c0, `cols` columns.
-template <typename T>
-__device__ __forceinline__ void lin_load(const T *src, int t0, int Ttot, int D, int c0, int cols,
-                                         float *dst, int ld) {
+// A chunk's tile of rows [kLinC][COLS] (from [T][D] at column c0; rows past T: zeros) into
+// registers, and from there as floats into shared memory: every load of a chunk goes out
+// before the first store.
+template <typename T, int COLS>
+struct LinTile {
     using V = Vec16<T>;
-    const int per = cols / V::N;
-    for (int i = threadIdx.x; i < kLinC * per; i += kLinThreads) {
-        const int r = i / per, c = (i - r * per) * V::N;
-        float v[V::N];
-        if (t0 + r < Ttot) {
-            V::load(src + (size_t)(t0 + r) * D + c0 + c, v);
-        } else {
+    static constexpr int PER = COLS / V::N, ITEMS = kLinC * PER, N = (ITEMS + kLinThreads - 1) / kLinThreads;
+    uint4 v[N];
+    __device__ __forceinline__ void load(const T *src, int t0, int Ttot, int D, int c0) {
 #pragma unroll
-            for (int e = 0; e < V::N; ++e) v[e] = 0.f;
+        for (int k = 0; k < N; ++k) {
+            const int i = threadIdx.x + k * kLinThreads, r = i / PER;
+            v[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < ITEMS && t0 + r < Ttot)
+                v[k] = V::raw(src + (size_t)(t0 + r) * D + c0 + (i - r * PER) * V::N);
         }
-#pragma unroll
-        for (int e = 0; e < V::N; e += 4)
-            *reinterpret_cast<float4 *>(dst + r * ld + c + e) =
-                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
     }
-}
+    __device__ __forceinline__ void store(float *dst, int ld) const {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int i = threadIdx.x + k * kLinThreads, r = i / PER;
+            if (i >= ITEMS) continue;
+            float f[V::N];
+            V::unpack(v[k], f);
+#pragma unroll
+            for (int e = 0; e < V::N; e += 4)
+                *reinterpret_cast<float4 *>(dst + r * ld + (i - r * PER) * V::N + e) =
+                    make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        }
+    }
+};
 
-// Inclusive prefix of the clamped log decays of one chunk by one warp (lane =
+// Inclusive prefix of the clamped log2 decays of one chunk by one warp (lane =
 // token; past T: no decay).
-__device__ __forceinline__ double lin_log_prefix(const float *beta, int t0, int T, double log_min) {
+__device__ __forceinline__ Log2Sum lin_log_prefix(const float *beta, int t0, int T, float log2_min) {
     const int lane = threadIdx.x & 31;
-    double x = 0.0;
-    if (t0 + lane < T) x = fmax(log((double)beta[t0 + lane]), log_min);
+    Log2Sum x = {0.f, 0.f};
+    if (t0 + lane < T) x.hi = fmaxf(log2f(beta[t0 + lane]), log2_min);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const Log2Sum y = {__shfl_up_sync(0xffffffffu, x.hi, o), __shfl_up_sync(0xffffffffu, x.lo, o)};
+        if (lane >= o) x = x + y;
     }
     return x;
 }
@@ -125,8 +161,8 @@ template <typename T, int D, bool REV, bool OUT>
 __global__ void __launch_bounds__(kLinThreads) k_linear_pass(const LinPass p) {
     using L = LinSmem<D>;
     constexpr int C = kLinC, ZN = kLinZN, LD = L::LD;
-    extern __shared__ double lin_smem[];
-    double *s_l = lin_smem;                                   // [C]
+    extern __shared__ float4 lin_smem[];
+    Log2Sum *s_l = reinterpret_cast<Log2Sum *>(lin_smem);     // [C]
     float *xs = reinterpret_cast<float *>(s_l + C);           // [C][LD]
     float *ys = xs + C * LD;                                  // [C][LD]
     float *zs = ys + C * LD;                                  // [C][ZN]
@@ -134,6 +170,8 @@ __global__ void __launch_bounds__(kLinThreads) k_linear_pass(const LinPass p) {
     float *St = wz + C * ZN;                                  // [D][ZN]
     float *Ps = St + D * ZN;                                  // [C][C + 1]
     float *s_a = Ps + C * (C + 1), *s_u = s_a + C, *s_g = s_u + C, *s_red = s_g + C;   // s_red [8]
+    griddep_launch_dependents();
+    griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int zsp = blockIdx.x, z0 = zsp * ZN, bh = blockIdx.y, seg = blockIdx.z;
     const int n0 = lin_seg(seg, p.S, p.N), n1 = lin_seg(seg + 1, p.S, p.N);
@@ -163,8 +201,19 @@ __global__ void __launch_bounds__(kLinThreads) k_linear_pass(const LinPass p) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) st[i][j] = p.start[state_at(base, i, j)];
     }
-    double seglog = 0.0;
+    const Log2Sum zero = {0.f, 0.f};
+    Log2Sum seglog = zero;
 
+    // a chunk's tiles are on their way while the one before is worked on
+    LinTile<T, D> tx, ty;
+    LinTile<T, ZN> tz;
+    auto fetch = [&](int it) {
+        const int t0 = (REV ? n1 - 1 - it : n0 + it) * C;
+        if (OUT) tx.load(X, t0, p.T, D, 0);
+        ty.load(Y, t0, p.T, D, 0);
+        tz.load(Z, t0, p.T, D, z0);
+    };
+    fetch(0);
     for (int it = 0; it < n1 - n0; ++it) {
         const int n = REV ? n1 - 1 - it : n0 + it, t0 = n * C;
         __syncthreads();
@@ -181,22 +230,23 @@ __global__ void __launch_bounds__(kLinThreads) k_linear_pass(const LinPass p) {
                     for (int j = 0; j < 4; ++j) p.states[state_at(base, i, j)] = st[i][j];
             }
         }
-        if (OUT) lin_load<T>(X, t0, p.T, D, 0, D, xs, LD);
-        lin_load<T>(Y, t0, p.T, D, 0, D, ys, LD);
-        lin_load<T>(Z, t0, p.T, D, z0, ZN, zs, ZN);
+        if (OUT) tx.store(xs, LD);
+        ty.store(ys, LD);
+        tz.store(zs, ZN);
         if (warp == 0) {
-            const double l = lin_log_prefix(beta, t0, p.T, p.log_min);
-            const double lC = __shfl_sync(0xffffffffu, l, 31);
+            const Log2Sum l = lin_log_prefix(beta, t0, p.T, p.log2_min), lC = shfl(l, 31);
             const float g = t0 + lane < p.T ? (gate ? gate[t0 + lane] : 1.f) : 0.f;
             s_l[lane] = l;
             s_g[lane] = g;
-            s_a[lane] = decay_exp(REV ? lC - l : l);
-            s_u[lane] = REV ? p.scale * decay_exp(l) : g * decay_exp(lC - l);
+            const float to = exp2_diff(l, zero), from = exp2_diff(lC, l);
+            s_a[lane] = REV ? from : to;
+            s_u[lane] = REV ? p.scale * to : g * from;
         }
         __syncthreads();
-        const double lC = s_l[C - 1];
-        const float b = decay_exp(lC);
-        seglog += lC;
+        if (it + 1 < n1 - n0) fetch(it + 1);
+        const Log2Sum lC = s_l[C - 1];
+        const float b = exp2_diff(lC, zero);
+        seglog = seglog + lC;
         // F: the state of the other direction against this one's, before the chunk
         if (OUT && p.states_in) {
             float f = 0.f;
@@ -242,7 +292,7 @@ __global__ void __launch_bounds__(kLinThreads) k_linear_pass(const LinPass p) {
                     const bool in = REV ? c >= t : c <= t;
                     const float w = REV ? p.scale : s_g[c];
                     Ps[t * (C + 1) + c] =
-                        in ? acc[i][j] * w * decay_exp(REV ? s_l[c] - s_l[t] : s_l[t] - s_l[c]) : 0.f;
+                        in ? acc[i][j] * w * (REV ? exp2_diff(s_l[c], s_l[t]) : exp2_diff(s_l[t], s_l[c])) : 0.f;
                 }
         }
         __syncthreads();
@@ -325,7 +375,7 @@ __global__ void __launch_bounds__(kLinThreads) k_linear_pass(const LinPass p) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) dst[state_at(base, i, j)] = st[i][j];
     }
-    if (!OUT && tid == 0 && zsp == 0) p.segdec[(size_t)bh * p.S + seg] = decay_exp(seglog);
+    if (!OUT && tid == 0 && zsp == 0) p.segdec[(size_t)bh * p.S + seg] = exp2_diff(seglog, zero);
 }
 
 // Segment starts in place of the segments' aggregates: the carry over a segment is
@@ -337,6 +387,8 @@ __global__ void __launch_bounds__(kLinThreads) k_linear_pass(const LinPass p) {
 __global__ void __launch_bounds__(256)
 k_linear_scan(float *__restrict__ agg, const float *__restrict__ segdec,
               const float *__restrict__ init, int S, int D2, int rev) {
+    griddep_launch_dependents();
+    griddep_wait();
     const int bh = blockIdx.y, e = (blockIdx.x * 256 + threadIdx.x) * 4;
     if (e >= D2) return;
     float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -380,22 +432,30 @@ struct LinPairs {
 template <typename T, int D>
 __global__ void __launch_bounds__(kLinThreads) k_linear_pairs(const LinPairs p) {
     constexpr int C = kLinC, LD = D + 4;
-    extern __shared__ double lin_smem[];
-    double *s_l = lin_smem;
+    extern __shared__ float4 lin_smem[];
+    Log2Sum *s_l = reinterpret_cast<Log2Sum *>(lin_smem);
     float *qs = reinterpret_cast<float *>(s_l + C), *ks = qs + C * LD, *vs = ks + C * LD,
           *os = vs + C * LD;
     float *As = os + C * LD;                       // [C][C + 1]
     float *s_g = As + C * (C + 1), *s_ze = s_g + C, *s_ge = s_ze + C;
+    griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = blockIdx.x, bh = blockIdx.y, t0 = n * C;
     const size_t head = (size_t)bh * p.T, rowsall = (size_t)p.BH * p.T;
-    lin_load<T>(static_cast<const T *>(p.q) + head * D, t0, p.T, D, 0, D, qs, LD);
-    lin_load<T>(static_cast<const T *>(p.k) + head * D, t0, p.T, D, 0, D, ks, LD);
-    lin_load<T>(static_cast<const T *>(p.v) + head * D, t0, p.T, D, 0, D, vs, LD);
-    lin_load<T>(static_cast<const T *>(p.d_o) + head * D, t0, p.T, D, 0, D, os, LD);
+    {
+        LinTile<T, D> tq, tk, tv, to;
+        tq.load(static_cast<const T *>(p.q) + head * D, t0, p.T, D, 0);
+        tk.load(static_cast<const T *>(p.k) + head * D, t0, p.T, D, 0);
+        tv.load(static_cast<const T *>(p.v) + head * D, t0, p.T, D, 0);
+        to.load(static_cast<const T *>(p.d_o) + head * D, t0, p.T, D, 0);
+        tq.store(qs, LD);
+        tk.store(ks, LD);
+        tv.store(vs, LD);
+        to.store(os, LD);
+    }
     float eta = 0.f;
     if (warp == 0) {
-        s_l[lane] = lin_log_prefix(p.beta + head, t0, p.T, kLinLogMinBwd);
+        s_l[lane] = lin_log_prefix(p.beta + head, t0, p.T, kLinLog2MinBwd);
         float zeta = 0.f, g = 0.f;
         if (t0 + lane < p.T) {
             g = p.gate ? p.gate[head + t0 + lane] : 1.f;
@@ -451,7 +511,7 @@ __global__ void __launch_bounds__(kLinThreads) k_linear_pairs(const LinPairs p) 
             for (int j = 0; j < 2; ++j) {
                 const int s = tr + 16 * i, c = tc + 16 * j;
                 As[s * (C + 1) + c] =
-                    c <= s ? p.scale * decay_exp(s_l[s] - s_l[c]) * aq[i][j] * av[i][j] : 0.f;
+                    c <= s ? p.scale * exp2_diff(s_l[s], s_l[c]) * aq[i][j] * av[i][j] : 0.f;
             }
     }
     __syncthreads();
@@ -484,7 +544,7 @@ __global__ void __launch_bounds__(kLinThreads) k_linear_pairs(const LinPairs p) 
 
 template <int D>
 constexpr size_t lin_pairs_smem() {
-    return sizeof(double) * kLinC +
+    return sizeof(Log2Sum) * kLinC +
            sizeof(float) * (4 * kLinC * (D + 4) + kLinC * (kLinC + 1) + 3 * kLinC);
 }
 

@@ -191,38 +191,12 @@ __device__ __forceinline__ void lt_commit(uint32_t bar) {
         : "memory");
 }
 
-// A sum of log decays as an unevaluated pair of floats (about 45 bits): differences of
-// cumulative logs keep fp32 precision after a reset, at a fraction of the latency that
-// doubles have on the one warp that forms the tables (1200 against 5400 cycles a chunk).
-struct Log2Sum {
-    float hi, lo;
-};
-__device__ __forceinline__ Log2Sum operator+(Log2Sum a, Log2Sum b) {
-    const float s = a.hi + b.hi, t = s - a.hi;
-    const float e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
-    const float h = s + e;
-    return {h, e - (h - s)};
-}
-// 2^x, results below 2^-126 as zero (relative error 2^-22: the hardware's function)
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// 2^(a - b)
-__device__ __forceinline__ float exp2_diff(Log2Sum a, Log2Sum b) {
-    return ex2((a.hi - b.hi) + (a.lo - b.lo));
-}
 // Two bf16 as a pair of floats, a pair as two bf16, and what the rounding left.
 __device__ __forceinline__ float2 bf16x2_f2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 __device__ __forceinline__ uint32_t f2_bf16x2(float2 y) { return bf16x2_bits(y.x, y.y); }
 __device__ __forceinline__ float2 f2_rest(float2 y, uint32_t w) {
     return __ffma2_rn(bf16x2_f2(w), make_float2(-1.f, -1.f), y);
 }
-__device__ __forceinline__ Log2Sum shfl(Log2Sum x, int src) {
-    return {__shfl_sync(0xffffffffu, x.hi, src), __shfl_sync(0xffffffffu, x.lo, src)};
-}
-
 // Decay tables of every chunk, a warp each, into tab [B*H][N][kLtTabF] (LtSmem lists a table's
 // parts).  A kernel of its own: formed by a warp of the passes, chunk by chunk, they took 4500
 // to 6300 cycles a chunk (600 instructions that no cache held) and bounded those.
@@ -231,7 +205,9 @@ template <bool REV>
 __global__ void __launch_bounds__(256)
 k_linear_tables(const float *__restrict__ beta, const float *__restrict__ gate, float *__restrict__ tab,
                 int BH, int N, int T, float scale, float log2_min) {
-    griddep_launch_dependents();   // the pass after this one may set itself up meanwhile
+    // once what came before is done, the pass after this one may begin: it reads that at once
+    griddep_wait();
+    griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
     const long long c = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (c >= (long long)BH * N) return;
@@ -373,6 +349,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     // Launched as the tables' programmatic dependent, this kernel may read what was there before
     // those (x, y, z, beta) at once; the tables, the start states and the other direction's states
     // only after the wait (loader, state warps).
+    griddep_launch_dependents();
     // TMEM columns; the bf16 weighted scores of each half of the columns lie over its scores
     constexpr uint32_t kP = 0, kOI = 128, kOS = 192, kDS = 256, kX = 448;
     const int quarter = warp & 3;
@@ -1020,6 +997,7 @@ k_linear_pairs_tc(const __grid_constant__ LinPairsTc args, int *__restrict__ tim
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tbase;
+    griddep_wait();
     bool ok = true;
     if (tid == kLpThreads - 32) {   // warps 0-3 prepare the tokens meanwhile
         auto load = [&](const CUtensorMap *a, const CUtensorMap *b, uint32_t bar) {
@@ -1066,7 +1044,7 @@ k_linear_pairs_tc(const __grid_constant__ LinPairsTc args, int *__restrict__ tim
         float g = 0.f;
         double l = 0.0;
         if (t < p.T) {
-            l = (double)fmaxf(log2f(p.beta[head + t]), -60.f);
+            l = (double)fmaxf(log2f(p.beta[head + t]), kLinLog2MinBwd);
             g = p.gate ? p.gate[head + t] : 1.f;
             for (int z = 0; z < p.ZS; ++z) {
                 zeta += p.zeta[z * all + head + t];
@@ -1127,7 +1105,7 @@ k_linear_pairs_tc(const __grid_constant__ LinPairsTc args, int *__restrict__ tim
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const int c = cb * 32 + h * 16 + j;
-                        const float w = exp2f((lh - s_lh[c]) + (ll - s_ll[c]));
+                        const float w = ex2((lh - s_lh[c]) + (ll - s_ll[c]));
                         float &x = a[h * 16 + j];
                         x = c <= s ? p.scale * w * x * v[j] : 0.f;
                         rs = fmaf(x, s_g[c], rs);
