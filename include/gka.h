@@ -307,8 +307,10 @@ int gka_solver_study(const void *q, const void *k, const float *beta, const floa
  *               and may be initial_state itself; T = 0 copies the one to the other
  *   workspace   at least gka_linear_forward_workspace_bytes(), 256-byte aligned
  *               (0 bytes for some sizes: then NULL will do)
- * B*H is at most 65535.  The fp32 state is carried in fp32; with bf16 inputs and
- * D = 128 the products run on the tensor cores.
+ * B*H is at most 65535.  The state is carried in fp32.  With bf16 inputs and D = 128
+ * the products run on the tensor cores (fp32 accumulation): inputs enter exactly, the
+ * state and its increments in two and three bf16 parts (16 and 24 bits), the decayed
+ * scores rounded once to bf16.  Every other case runs on CUDA cores in fp32.
  */
 size_t gka_linear_forward_workspace_bytes(int B, int H, int T, int D, gka_dtype dt);
 int gka_linear_forward(const void *q, const void *k, const void *v, const float *beta,
@@ -333,7 +335,7 @@ int gka_linear_decode_step(float *state, const void *q, const void *k, const voi
  *   initial_state, dfinal_state   nullable fp32 [B, H, D, D]
  *   dq, dk, dv    [B, H, T, D] in `dt`; dbeta [B, H, T] fp32 (written)
  *   dgate         [B, H, T] fp32 (written); non-NULL exactly when gate is
- *   dinitial_state  nullable fp32 [B, H, D, D] (written); may be dfinal_state itself
+ *   dinitial_state  nullable fp32 [B, H, D, D] (written); no input's memory
  *   workspace     at least gka_linear_backward_workspace_bytes(), 256-byte aligned
  * Decays below 2^-60 (a reset's 0 among them) count as 2^-60: dbeta stays exact
  * there, and every other gradient is off by less than 2^-60 of what was written.

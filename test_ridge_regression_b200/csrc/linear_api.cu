@@ -476,6 +476,8 @@ int gka_linear_backward(const void *q, const void *k, const void *v, const float
         if (p && !aligned16(p)) return GKA_ERR_MISALIGNED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) return pass_state(dinitial_state, dfinal_state, BH * D * D, s);
+    // dk's pass still reads the one while dv's writes the other
+    if (dinitial_state && dinitial_state == dfinal_state) return GKA_ERR_INVALID_ARG;
     if (!q || !k || !v || !beta || !dout || !dq || !dk || !dv || !dbeta || !workspace)
         return GKA_ERR_INVALID_ARG;
     if ((uintptr_t)workspace & 255u) return GKA_ERR_MISALIGNED;

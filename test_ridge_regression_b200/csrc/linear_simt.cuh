@@ -63,6 +63,11 @@ __device__ __forceinline__ Log2Sum operator+(Log2Sum a, Log2Sum b) {
     const float h = s + e;
     return {h, e - (h - s)};
 }
+// log2 beta, not below `least` (a NaN stays one)
+__device__ __forceinline__ float log2_decay(float beta, float least) {
+    const float l = log2f(beta);
+    return l < least ? least : l;
+}
 // 2^x, results below 2^-126 as zero (relative error 2^-22: the hardware's function)
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -146,7 +151,7 @@ struct LinTile {
 __device__ __forceinline__ Log2Sum lin_log_prefix(const float *beta, int t0, int T, float log2_min) {
     const int lane = threadIdx.x & 31;
     Log2Sum x = {0.f, 0.f};
-    if (t0 + lane < T) x.hi = fmaxf(log2f(beta[t0 + lane]), log2_min);
+    if (t0 + lane < T) x.hi = log2_decay(beta[t0 + lane], log2_min);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const Log2Sum y = {__shfl_up_sync(0xffffffffu, x.hi, o), __shfl_up_sync(0xffffffffu, x.lo, o)};

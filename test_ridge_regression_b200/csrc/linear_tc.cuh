@@ -58,7 +58,7 @@ constexpr int kLtThreads = 2 * kLtGroup + 128;  // + two issuers, the decay warp
 constexpr int kLtTabs = 4;                      // stages of decay tables
 constexpr int kLtTabF = 8 * kLtC + 4;           // floats of a table
 constexpr int kLtDots = 4, kLtFdots = 16;       // planes of dot and fdot partials per pass
-constexpr uint32_t kLtProbes = 1u << 17;
+constexpr uint32_t kLtProbes = 1u << 20;
 constexpr uint32_t kLtHintNs = 2000;            // a probe suspends its warp for up to this long
 
 struct LtSmem {
@@ -221,7 +221,7 @@ k_linear_tables(const float *__restrict__ beta, const float *__restrict__ gate, 
         const size_t at = (size_t)bh * T + t0 + 32 * j;
         const float b = in ? beta[at] : 1.f;
         g[j] = in ? (gate ? gate[at] : 1.f) : 0.f;
-        l[j] = {fmaxf(log2f(b), log2_min), 0.f};
+        l[j] = {log2_decay(b, log2_min), 0.f};
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -624,9 +624,14 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 const int t = chunk(it) * C + row;
                 const size_t grow = (size_t)bh * p.T + t;
                 const bool in = t < p.T;
-                const uint4 *xd = reinterpret_cast<const uint4 *>(
-                    static_cast<const __nv_bfloat16 *>(p.xd) + grow * D + z0);
                 const bool dots = p.dot && in;
+                uint4 xd[4] = {};   // (in flight while the products run)
+                if (dots) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        static_cast<const __nv_bfloat16 *>(p.xd) + grow * D + z0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) xd[j] = __ldg(src + j);
+                }
                 const float a = tab[row], g = REV ? tab[7 * C + row] : 1.f;
                 float d = 0.f;
                 if (!wait(b_o + 8 * sg, (it >> 1) & 1)) break;
@@ -644,7 +649,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
 #pragma unroll
                     for (int j = 0; j < 16; ++j) vs[j] *= a;
                     if (dots) {
-                        const uint4 x0 = __ldg(xd + 2 * h), x1 = __ldg(xd + 2 * h + 1);
+                        const uint4 x0 = h ? xd[2] : xd[0], x1 = h ? xd[3] : xd[1];
                         const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
@@ -946,7 +951,7 @@ struct LpSmem {
 struct LinPairsTc {
     CUtensorMap q, k, v, d_o;
     LinPairs p;
-    int FS;          // planes of fdot
+    int FS;          // planes of fdot (at most 32)
 };
 
 // x[j] over the 32 lanes of a warp: lane j returns the sum of every lane's x[j].
@@ -1038,13 +1043,15 @@ k_linear_pairs_tc(const __grid_constant__ LinPairsTc args, int *__restrict__ tim
     }
     __syncwarp();
     // tokens by threads 0..127: logs, gates, and the sums of zeta from and g eta before a token
-    float eta = 0.f, zeta = 0.f, ge = 0.f;
+    float eta = 0.f, zeta = 0.f, ge = 0.f, through = 0.f;
     if (tid < C) {
+        if (lane < args.FS) through = p.fdot[((size_t)lane * p.BH + bh) * p.N + n];   // FS <= 32
+        through = warp_sum(through);
         const int t = t0 + tid;
         float g = 0.f;
         double l = 0.0;
         if (t < p.T) {
-            l = (double)fmaxf(log2f(p.beta[head + t]), kLinLog2MinBwd);
+            l = (double)log2_decay(p.beta[head + t], kLinLog2MinBwd);
             g = p.gate ? p.gate[head + t] : 1.f;
             for (int z = 0; z < p.ZS; ++z) {
                 zeta += p.zeta[z * all + head + t];
@@ -1146,8 +1153,7 @@ k_linear_pairs_tc(const __grid_constant__ LinPairsTc args, int *__restrict__ tim
     }
     __syncthreads();
     if (ok && tid < C && t0 + tid < p.T) {
-        float d = zeta + ge, dg = eta;
-        for (int f = 0; f < args.FS; ++f) d += p.fdot[((size_t)f * p.BH + bh) * p.N + n];
+        float d = zeta + ge + through, dg = eta;
         for (int q = 0; q < 4; ++q) {
             d += s_cx[q * C + tid];
             dg += s_cg[q * C + tid];

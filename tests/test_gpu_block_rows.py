@@ -250,3 +250,31 @@ def test_block_in_feeds_the_ridge_layer():
     assert rel(o, torch.from_numpy(want)) <= 2e-2   # the layer's own bar for bf16
     y = gka.gka_block_out(o, torch.ones(128, device="cuda"))
     assert rel(y, ref.block_out(o, torch.ones(128, device="cuda"))) <= TOL[torch.bfloat16]
+
+
+def test_refusals():
+    args, kw, g = make_in(2, 8, 4, 2, 64, torch.bfloat16, 12)
+    q, k, v, bl = args
+    wide = torch.zeros(2, 8, 4, 128, device="cuda", dtype=torch.bfloat16)
+    for bad in ((wide[..., ::2], k, v, bl), (q.float(), k, v, bl), (q, k[:, :, :1], v, bl), (q, k, v, bl[:1]),
+                (q.cpu(), k, v, bl), (q, wide[:, :, :3, :64], wide[:, :, :3, :64], bl)):
+        with pytest.raises((ValueError, TypeError, gka.GkaError)):
+            gka.gka_block_in(*bad, gate_logit=kw["gate_logit"])
+    odd = torch.zeros(2, 8, 4 * 64 + 3, device="cuda", dtype=torch.bfloat16)[..., 3:].unflatten(-1, (4, 64))
+    with pytest.raises(gka.GkaError):   # rows off the 16-byte grid
+        gka.gka_block_in(odd, k, v, bl)
+    with pytest.raises(ValueError):
+        gka.gka_block_in(*args, gate_bias=torch.zeros(4, device="cuda"))
+    with pytest.raises(ValueError):
+        gka.gka_block_in(*args, lengths=torch.tensor([8, 8], device="cuda"))   # int64
+    with pytest.raises(gka.GkaError):
+        gka.gka_block_in(*args, eps=float("nan"))
+    o, w, okw, _ = make_out(2, 8, 4, 64, torch.bfloat16, 13, True, True)
+    with pytest.raises(ValueError):
+        gka.gka_block_out(o, w, v=okw["v"])
+    with pytest.raises(ValueError):
+        gka.gka_block_out(o, w[:32])
+    with pytest.raises(ValueError):
+        gka.gka_block_out(o, w, y=o.view(2, 8, 4, 64))
+    with pytest.raises(ValueError):
+        gka.gka_block_out_backward(o, w, o)

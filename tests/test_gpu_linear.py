@@ -290,3 +290,61 @@ def test_offsets_past_two_to_the_31():
         # the head alone runs in segments: the same up to fp32 order, then one rounding
         assert rel(o[:, h, -4096:], o1[:, 0, -4096:]) <= TOL16
         assert rel(last[:, h], l1[:, 0]) <= TOL32
+
+
+def test_two_streams_at_once():
+    """Independent calls in flight together, each with its own workspace."""
+    sets = [linear_inputs(1, 3 + 40 * (i % 2), 600 + i, 128, torch.bfloat16, 20 + i, gate=True, state=True)
+            for i in range(4)]
+    want = [(run_forward(a, kw), run_backward(a, kw, a["v"])) for a, kw, _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = []
+    for s, (a, kw, _) in zip(streams, sets):
+        with torch.cuda.stream(s):
+            got.append((run_forward(a, kw), run_backward(a, kw, a["v"])))
+    torch.cuda.synchronize()
+    assert gka.device_status() == 0
+    for ((o, l), g), ((ro, rl), rg) in zip(got, want):
+        assert torch.equal(o, ro) and torch.equal(l, rl)
+        assert all(torch.equal(g[n], rg[n]) for n in rg)
+
+
+def test_nan_decay_shows():
+    """A NaN among the decays is not taken for a reset."""
+    for dtype, D in ((torch.float32, 64), (torch.bfloat16, 128)):
+        a, kw, _ = linear_inputs(1, 2, 200, D, dtype, 24)
+        a["beta"][0, 1, 50] = float("nan")
+        o, last = run_forward(a, kw)
+        assert torch.isfinite(o[0, 0]).all() and torch.isfinite(last[0, 0]).all()
+        assert torch.isnan(last[0, 1]).any() and torch.isnan(o[0, 1, 51:]).any()
+
+
+def test_refusals():
+    """What the binding does not take, with nothing launched or written."""
+    a, kw, _ = linear_inputs(1, 2, 40, 64, torch.float32, 25, gate=True, state=True)
+    q, k, v, b = (a[n] for n in ("q", "k", "v", "beta"))
+    bad = [dict(q=q[..., ::2]), dict(k=k.half()), dict(beta=b.double()), dict(beta=b[:, :, 1:]),
+           dict(v=v.cpu()), dict(q=q.transpose(1, 2))]
+    for kw2 in bad:
+        with pytest.raises((ValueError, TypeError, RuntimeError)):
+            gka.gka_linear_forward(**{**a, **kw2})
+    for kw2 in (dict(gate=kw["gate"].half()), dict(initial_state=kw["state"][:, :1]),
+                dict(final_state=kw["state"].bfloat16()), dict(o=v), dict(o=q[:, :, :20]),
+                dict(workspace=torch.empty(0, dtype=torch.uint8))):
+        with pytest.raises((ValueError, TypeError, RuntimeError)):
+            gka.gka_linear_forward(**a, **kw2)
+    with pytest.raises(gka.GkaError):
+        gka.gka_linear_forward(**a, scale=float("nan"))
+    big, _, _ = linear_inputs(1, 1, 4000, 128, torch.bfloat16, 26)
+    n = gka.linear_workspace_bytes(1, 1, 4000, 128)
+    with pytest.raises(gka.GkaError):
+        gka.gka_linear_forward(**big, workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
+    with pytest.raises((ValueError, TypeError)):
+        gka.gka_linear_backward(**a, dout=v[:, :, 1:])
+    with pytest.raises((ValueError, TypeError)):
+        gka.gka_linear_decode_step(kw["state"], q[:, :, 0], k[:, :, 0].contiguous(),
+                                   v[:, :, 0].contiguous(), b[:, :, 0].contiguous())
+    x = {n: y[:, :, 0].contiguous() for n, y in a.items()}
+    with pytest.raises(ValueError):
+        gka.gka_linear_decode_step(kw["state"], **x, o=x["v"])

@@ -119,6 +119,7 @@ def test_linear_backward_refusals(lib):
     for n in ("init", "dlast", "dinit"):
         assert call(**{n: ODD}) == MISALIGNED
     assert call(gate=P) == INVALID and call(dgate=P) == INVALID
+    assert call(dlast=P, dinit=P) == INVALID   # one is read while the other is written
     assert call(n=0) == SMALL and call(scale=math.nan) == INVALID
     assert call(D=16) == UNSUPPORTED and call(B=-1) == INVALID and call(B=0) == OK
 
