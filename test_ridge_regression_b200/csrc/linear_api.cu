@@ -63,13 +63,13 @@ static int lin_layout(int B, int H, int T, int D, gka_dtype dt, bool bwd, LinLay
     if (!supported_d(D)) return GKA_ERR_UNSUPPORTED;
     if ((size_t)B * H > 65535) return GKA_ERR_UNSUPPORTED;   // grid limit
     const size_t BH = (size_t)B * H, st = sizeof(float) * (size_t)D * D;
-    L->tc = dt == GKA_BF16 && D == 128;
+    L->tc = dt == GKA_BF16;
     const int C = L->tc ? kLtC : kLinC;
-    L->ZS = D / (L->tc ? kLtZN : kLinZN);
+    L->ZS = lt_splits(D);   // of 64 columns, in both forms
     L->N = (int)(((long long)T + C - 1) / C);
-    L->S = lin_segments((int)BH * L->ZS, L->N, L->tc ? 1 : 3);
-    L->dots = L->tc ? kLtDots : L->ZS;
-    L->fdots = L->tc ? kLtFdots : L->ZS;
+    L->S = lin_segments((int)BH * L->ZS, L->N, L->tc ? 1 : lin_per_sm(D));
+    L->dots = L->tc ? kLtDots * L->ZS : D / 32;
+    L->fdots = L->tc ? kLtFdots * L->ZS : L->ZS;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -90,24 +90,26 @@ static int lin_layout(int B, int H, int T, int D, gka_dtype dt, bool bwd, LinLay
     return GKA_OK;
 }
 
-template <typename T, int D, bool REV, bool OUT>
-static int lin_launch(const LinPass &p, int ZS, int prof, cudaStream_t s) {
+template <int D, bool REV, bool OUT>
+static int lin_launch(const LinPasses &a, int passes, int prof, cudaStream_t s) {
+    const LinPass &p = a.pass[0];
     ProfScope ps(prof, s);
-    return launch_after(k_linear_pass<T, D, REV, OUT>, dim3(ZS, p.BH, p.S), kLinThreads, LinSmem<D>::bytes, true,
-                        s, p);
+    return launch_after(k_linear_pass<D, REV, OUT>, dim3(passes * (D / LinSmem<D>::ZN), p.BH, p.S), kLinThreads,
+                        LinSmem<D>::bytes, true, s, a);
 }
 
-// Segment starts for a pass (p.S > 1): aggregates, then their scan from `init`.
-template <typename T, int D, bool REV>
-static int lin_starts(LinPass &p, const LinLayout &L, char *ws, const float *init, int prof,
+// Segment starts for the first pass (S > 1): aggregates, then their scan from `init`.
+template <int D, bool REV>
+static int lin_starts(LinPasses &a, const LinLayout &L, char *ws, const float *init, int prof,
                       cudaStream_t s) {
+    LinPass &p = a.pass[0];
     if (L.S == 1) {
         p.start = init;
         return GKA_OK;
     }
     p.agg = reinterpret_cast<float *>(ws + L.agg);
     p.segdec = reinterpret_cast<float *>(ws + L.segdec);
-    if (int rc = lin_launch<T, D, REV, false>(p, L.ZS, prof, s)) return rc;
+    if (int rc = lin_launch<D, REV, false>(a, 1, prof, s)) return rc;
     ProfScope ps(prof, s);
     p.start = p.agg;
     return launch_after(k_linear_scan, dim3((D * D + 1023) / 1024, p.BH), 256, 0, true, s, p.agg,
@@ -119,28 +121,29 @@ struct LinCall {
     const float *beta, *gate, *init, *dlast;
     void *o, *dq, *dk, *dv;
     float *last, *dbeta, *dgate, *dinit;
-    int BH, T;
+    int BH, T, D;
     float scale;
     char *ws;
     cudaStream_t s;
 };
 
-template <typename T, int D>
+template <int D>
 static int lin_forward(const LinCall &c, const LinLayout &L) {
-    LinPass p = {};
+    LinPasses a = {};
+    LinPass &p = a.pass[0];
     p.x = c.q; p.y = c.k; p.z = c.v;
     p.out = c.o;
     p.beta = c.beta; p.gate = c.gate;
     p.scale = c.scale;
     p.log2_min = kLinLog2Min;
-    p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S;
+    p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S; p.D = c.D;
     p.zy = 1;
-    if (int rc = lin_starts<T, D, false>(p, L, c.ws, c.init, GKA_KERNEL_LINEAR, c.s)) return rc;
+    if (int rc = lin_starts<D, false>(a, L, c.ws, c.init, GKA_KERNEL_LINEAR, c.s)) return rc;
     p.last = c.last;
-    return lin_launch<T, D, false, true>(p, L.ZS, GKA_KERNEL_LINEAR, c.s);
+    return lin_launch<D, false, true>(a, 1, GKA_KERNEL_LINEAR, c.s);
 }
 
-template <typename T, int D>
+template <int D>
 static int lin_backward(const LinCall &c, const LinLayout &L) {
     constexpr int kProf = GKA_KERNEL_LINEAR_GRAD;
     float *states = reinterpret_cast<float *>(c.ws + L.states);
@@ -151,56 +154,58 @@ static int lin_backward(const LinCall &c, const LinLayout &L) {
     p.beta = c.beta; p.gate = c.gate;
     p.scale = c.scale;
     p.log2_min = kLinLog2MinBwd;
-    p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S;
+    p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S; p.D = c.D;
     // dq, forwards in time; M before every chunk stays for F
-    LinPass f = p;
+    LinPasses a = {};
+    LinPass &f = a.pass[0];
+    f = p;
     f.x = c.d_o; f.y = c.v; f.z = c.k;
-    f.zy = 0;
-    if (int rc = lin_starts<T, D, false>(f, L, c.ws, c.init, kProf, c.s)) return rc;
+    if (int rc = lin_starts<D, false>(a, L, c.ws, c.init, kProf, c.s)) return rc;
     f.out = c.dq;
     f.xd = c.q;
     f.dot = zeta;
     f.states = states;
-    if (int rc = lin_launch<T, D, false, true>(f, L.ZS, kProf, c.s)) return rc;
-    // dv and dk, backwards in time
-    LinPass r = p;
+    if (int rc = lin_launch<D, false, true>(a, 1, kProf, c.s)) return rc;
+    // dv and dk, backwards in time, in one launch
+    a = {};
+    LinPass &r = a.pass[0], &d = a.pass[1];
+    r = p;
     r.x = c.k; r.y = c.q; r.z = c.d_o;
     r.zy = 1;
-    if (int rc = lin_starts<T, D, true>(r, L, c.ws, c.dlast, kProf, c.s)) return rc;
+    if (int rc = lin_starts<D, true>(a, L, c.ws, c.dlast, kProf, c.s)) return rc;
     r.out = c.dv;
     r.xd = c.v;
     r.dot = eta;
-    r.states_in = states;
-    r.fdot = fdot;
     r.last = c.dinit;
-    if (int rc = lin_launch<T, D, true, true>(r, L.ZS, kProf, c.s)) return rc;
-    LinPass d = p;
+    d = p;
     d.x = c.v; d.y = c.d_o; d.z = c.q;
-    d.zy = 0;
     d.start = r.start;
     d.out = c.dk;
-    if (int rc = lin_launch<T, D, true, true>(d, L.ZS, kProf, c.s)) return rc;
+    // dk's state has dq's orientation: F there reads what dq's pass wrote, as it wrote it
+    d.states_in = states;
+    d.fdot = fdot;
+    if (int rc = lin_launch<D, true, true>(a, 2, kProf, c.s)) return rc;
     LinPairs w = {};
     w.q = c.q; w.k = c.k; w.v = c.v; w.d_o = c.d_o;
     w.beta = c.beta; w.gate = c.gate;
     w.zeta = zeta; w.eta = eta; w.fdot = fdot;
     w.dbeta = c.dbeta; w.dgate = c.dgate;
     w.scale = c.scale;
-    w.BH = c.BH; w.T = c.T; w.N = L.N; w.ZS = L.ZS;
+    w.BH = c.BH; w.T = c.T; w.N = L.N; w.ZS = L.dots; w.FS = L.fdots;
     ProfScope ps(kProf, c.s);
-    return launch_after(k_linear_pairs<T, D>, dim3(L.N, c.BH), kLinThreads, lin_pairs_smem<D>(), true, c.s, w);
+    return launch_after(k_linear_pairs<D>, dim3(L.N, c.BH), kLinThreads, lin_pairs_smem<D>(), true, c.s, w);
 }
 
 // ---------------------------------------------------------------------------
 // The same calls on the tensor cores
 // ---------------------------------------------------------------------------
-// [B*H][T][128] bf16 in boxes of 64 columns x 128 tokens of one head, 128-byte
-// swizzle; tokens past T read as zeros.
-static int head_map(CUtensorMap *m, const void *base, int T, int BH) {
+// [B*H][T][D] bf16 in boxes of 64 columns x 128 tokens of one head, 128-byte
+// swizzle; tokens past T and columns past D read as zeros and are not written.
+static int head_map(CUtensorMap *m, const void *base, int T, int BH, int D) {
     auto enc = tensor_map_encoder();
     if (!enc) return cuda_fail(cudaErrorNotSupported);
-    cuuint64_t dims[3] = {128, (cuuint64_t)T, (cuuint64_t)BH};
-    cuuint64_t strides[2] = {256, (cuuint64_t)T * 256};
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)BH};
+    cuuint64_t strides[2] = {2 * (cuuint64_t)D, 2 * (cuuint64_t)D * T};
     cuuint32_t box[3] = {64, kLtC, 1}, es[3] = {1, 1, 1};
     const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
                            strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -222,13 +227,13 @@ static int lin_tc_tables(LinTcArgs &a, int passes, const LinLayout &L, char *ws,
 }
 
 // `pdl`: the kernel before is the tables'.
-template <bool REV>
+template <bool REV, bool GRAD>
 static int lin_tc_launch(const LinTcArgs &a, int passes, bool pdl, int prof, cudaStream_t s) {
     int *flag = nullptr;
     if (int rc = timeout_flag_ptr(&flag)) return rc;
     const LinPass &p = a.pass[0].p;
     ProfScope ps(prof, s);
-    return launch_after(k_linear_tc<REV>, dim3(2 * passes, p.BH, p.S), kLtThreads, LtSmem::bytes, pdl, s, a, flag);
+    return launch_after(k_linear_tc<REV, GRAD>, dim3(lt_splits(p.D) * passes, p.BH, p.S), kLtThreads, LtSmem::bytes, pdl, s, a, flag);
 }
 
 template <bool REV>
@@ -245,46 +250,46 @@ static int lin_tc_starts(LinTcArgs &a, const LinLayout &L, char *ws, const float
     if (int rc = timeout_flag_ptr(&flag)) return rc;
     {
         ProfScope ps(prof, s);
-        if (int rc = launch_after(k_linear_agg_tc<REV>, dim3(2, p.BH, L.S), kLtThreads, LaSmem::bytes, true, s,
+        if (int rc = launch_after(k_linear_agg_tc<REV>, dim3(L.ZS, p.BH, L.S), kLtThreads, LaSmem::bytes, true, s,
                                   a.pass[0], flag))
             return rc;
     }
     ProfScope ps(prof, s);
     p.start = p.agg;
-    return launch_after(k_linear_scan, dim3(16, p.BH), 256, 0, false, s, p.agg, (const float *)p.segdec, init,
-                        L.S, 128 * 128, (int)REV);
+    return launch_after(k_linear_scan, dim3((p.D * p.D + 1023) / 1024, p.BH), 256, 0, false, s, p.agg,
+                        (const float *)p.segdec, init, L.S, p.D * p.D, (int)REV);
 }
 
 static int lin_tc_forward(const LinCall &c, const LinLayout &L) {
     LinTcArgs a = {};
-    if (int rc = head_map(&a.pass[0].x, c.q, c.T, c.BH)) return rc;
-    if (int rc = head_map(&a.pass[0].y, c.k, c.T, c.BH)) return rc;
-    if (int rc = head_map(&a.pass[0].z, c.v, c.T, c.BH)) return rc;
-    if (int rc = head_map(&a.pass[0].out, c.o, c.T, c.BH)) return rc;
+    if (int rc = head_map(&a.pass[0].x, c.q, c.T, c.BH, c.D)) return rc;
+    if (int rc = head_map(&a.pass[0].y, c.k, c.T, c.BH, c.D)) return rc;
+    if (int rc = head_map(&a.pass[0].z, c.v, c.T, c.BH, c.D)) return rc;
+    if (int rc = head_map(&a.pass[0].out, c.o, c.T, c.BH, c.D)) return rc;
     LinPass &p = a.pass[0].p;
     p.beta = c.beta; p.gate = c.gate;
     p.scale = c.scale;
     p.log2_min = kLinLog2Min;
-    p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S;
+    p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S; p.D = c.D;
     p.zy = 1;
     if (int rc = lin_tc_tables<false>(a, 1, L, c.ws, GKA_KERNEL_LINEAR, c.s)) return rc;
     if (int rc = lin_tc_starts<false>(a, L, c.ws, c.init, GKA_KERNEL_LINEAR, c.s)) return rc;
     p.last = c.last;
-    return lin_tc_launch<false>(a, 1, L.S == 1, GKA_KERNEL_LINEAR, c.s);
+    return lin_tc_launch<false, false>(a, 1, L.S == 1, GKA_KERNEL_LINEAR, c.s);
 }
 
 static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
     constexpr int kProf = GKA_KERNEL_LINEAR_GRAD;
     CUtensorMap q, k, v, d_o;
-    if (int rc = head_map(&q, c.q, c.T, c.BH)) return rc;
-    if (int rc = head_map(&k, c.k, c.T, c.BH)) return rc;
-    if (int rc = head_map(&v, c.v, c.T, c.BH)) return rc;
-    if (int rc = head_map(&d_o, c.d_o, c.T, c.BH)) return rc;
+    if (int rc = head_map(&q, c.q, c.T, c.BH, c.D)) return rc;
+    if (int rc = head_map(&k, c.k, c.T, c.BH, c.D)) return rc;
+    if (int rc = head_map(&v, c.v, c.T, c.BH, c.D)) return rc;
+    if (int rc = head_map(&d_o, c.d_o, c.T, c.BH, c.D)) return rc;
     LinPass p = {};
     p.beta = c.beta; p.gate = c.gate;
     p.scale = c.scale;
     p.log2_min = kLinLog2MinBwd;
-    p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S;
+    p.BH = c.BH; p.T = c.T; p.N = L.N; p.S = L.S; p.D = c.D;
     LinPairsTc w = {};
     w.p.zeta = reinterpret_cast<float *>(c.ws + L.zeta);
     w.p.eta = reinterpret_cast<float *>(c.ws + L.eta);
@@ -296,11 +301,11 @@ static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
     if (int rc = lin_tc_tables<false>(f, 1, L, c.ws, kProf, c.s)) return rc;
     if (int rc = lin_tc_starts<false>(f, L, c.ws, c.init, kProf, c.s)) return rc;
     LinPass &pf = f.pass[0].p;
-    if (int rc = head_map(&f.pass[0].out, c.dq, c.T, c.BH)) return rc;
+    if (int rc = head_map(&f.pass[0].out, c.dq, c.T, c.BH, c.D)) return rc;
     pf.xd = c.q;
     pf.dot = const_cast<float *>(w.p.zeta);
     pf.states = reinterpret_cast<float *>(c.ws + L.states);
-    if (int rc = lin_tc_launch<false>(f, 1, L.S == 1, kProf, c.s)) return rc;
+    if (int rc = lin_tc_launch<false, true>(f, 1, L.S == 1, kProf, c.s)) return rc;
     // dv and dk, backwards in time, in one launch
     LinTcArgs r = {};
     r.pass[0].x = k; r.pass[0].y = q; r.pass[0].z = d_o;
@@ -310,8 +315,8 @@ static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
     if (int rc = lin_tc_starts<true>(r, L, c.ws, c.dlast, kProf, c.s)) return rc;
     LinPass &pv = r.pass[0].p, &pk = r.pass[1].p;
     r.pass[1].x = v; r.pass[1].y = d_o; r.pass[1].z = q;
-    if (int rc = head_map(&r.pass[0].out, c.dv, c.T, c.BH)) return rc;
-    if (int rc = head_map(&r.pass[1].out, c.dk, c.T, c.BH)) return rc;
+    if (int rc = head_map(&r.pass[0].out, c.dv, c.T, c.BH, c.D)) return rc;
+    if (int rc = head_map(&r.pass[1].out, c.dk, c.T, c.BH, c.D)) return rc;
     pk = p;
     pk.start = pv.start;
     // dk's state has dq's orientation: F there reads what dq's pass wrote, as it wrote it
@@ -320,30 +325,31 @@ static int lin_tc_backward(const LinCall &c, const LinLayout &L) {
     pv.xd = c.v;
     pv.dot = const_cast<float *>(w.p.eta);
     pv.last = c.dinit;
-    if (int rc = lin_tc_launch<true>(r, 2, L.S == 1, kProf, c.s)) return rc;
+    if (int rc = lin_tc_launch<true, true>(r, 2, L.S == 1, kProf, c.s)) return rc;
     w.q = q; w.k = k; w.v = v; w.d_o = d_o;
     w.p.beta = c.beta; w.p.gate = c.gate;
     w.p.dbeta = c.dbeta; w.p.dgate = c.dgate;
     w.p.scale = c.scale;
-    w.p.BH = c.BH; w.p.T = c.T; w.p.N = L.N; w.p.ZS = L.dots;
-    w.FS = L.fdots;
+    w.p.BH = c.BH; w.p.T = c.T; w.p.N = L.N; w.p.ZS = L.dots; w.p.FS = L.fdots;
+    w.D = c.D;
     int *flag = nullptr;
     if (int rc = timeout_flag_ptr(&flag)) return rc;
     ProfScope ps(kProf, c.s);
     return launch_after(k_linear_pairs_tc, dim3(L.N, c.BH), kLpThreads, LpSmem::bytes, true, c.s, w, flag);
 }
 
-// f(type tag, size tag) for the call's type and head size.
+// f(size tag) for the call's head size, f(type tag, size tag) for its type too.
+template <typename F>
+static int by_size(int D, F f) {
+    switch (D) {
+        case 32: return f(std::integral_constant<int, 32>());
+        case 64: return f(std::integral_constant<int, 64>());
+        default: return f(std::integral_constant<int, 128>());
+    }
+}
 template <typename F>
 static int by_type(gka_dtype dt, int D, F f) {
-    auto by_size = [&](auto tag) {
-        switch (D) {
-            case 32: return f(tag, std::integral_constant<int, 32>());
-            case 64: return f(tag, std::integral_constant<int, 64>());
-            default: return f(tag, std::integral_constant<int, 128>());
-        }
-    };
-    return dt == GKA_BF16 ? by_size(__nv_bfloat16()) : by_size(float());
+    return by_size(D, [&](auto d) { return dt == GKA_BF16 ? f(__nv_bfloat16(), d) : f(float(), d); });
 }
 
 // ---------------------------------------------------------------------------
@@ -449,13 +455,11 @@ int gka_linear_forward(const void *q, const void *k, const void *v, const float 
     LinCall c = {};
     c.q = q; c.k = k; c.v = v; c.beta = beta; c.gate = gate; c.o = o;
     c.init = initial_state; c.last = final_state;
-    c.BH = (int)BH; c.T = T; c.scale = scale;
+    c.BH = (int)BH; c.T = T; c.D = D; c.scale = scale;
     c.ws = static_cast<char *>(workspace);
     c.s = s;
     if (L.tc) return lin_tc_forward(c, L);
-    return by_type(dt, D, [&](auto tag, auto d) {
-        return lin_forward<decltype(tag), decltype(d)::value>(c, L);
-    });
+    return by_size(D, [&](auto d) { return lin_forward<decltype(d)::value>(c, L); });
 }
 
 int gka_linear_backward(const void *q, const void *k, const void *v, const float *beta,
@@ -486,13 +490,11 @@ int gka_linear_backward(const void *q, const void *k, const void *v, const float
     c.q = q; c.k = k; c.v = v; c.beta = beta; c.gate = gate; c.d_o = dout;
     c.init = initial_state; c.dlast = dfinal_state;
     c.dq = dq; c.dk = dk; c.dv = dv; c.dbeta = dbeta; c.dgate = dgate; c.dinit = dinitial_state;
-    c.BH = (int)BH; c.T = T; c.scale = scale;
+    c.BH = (int)BH; c.T = T; c.D = D; c.scale = scale;
     c.ws = static_cast<char *>(workspace);
     c.s = s;
     if (L.tc) return lin_tc_backward(c, L);
-    return by_type(dt, D, [&](auto tag, auto d) {
-        return lin_backward<decltype(tag), decltype(d)::value>(c, L);
-    });
+    return by_size(D, [&](auto d) { return lin_backward<decltype(d)::value>(c, L); });
 }
 
 int gka_linear_decode_step(float *state, const void *q, const void *k, const void *v,

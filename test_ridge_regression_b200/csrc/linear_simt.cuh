@@ -46,7 +46,6 @@
 namespace gka {
 
 constexpr int kLinC = 32;         // tokens per chunk of the CUDA-core pass
-constexpr int kLinZN = 32;        // columns of z a CTA owns
 constexpr int kLinThreads = 256;
 // Clamps of log2 beta: in the forward, below every fp32 product (a reset passes exactly
 // nothing); 2^-60 is the smallest decay the backward tells from zero.
@@ -96,7 +95,7 @@ struct LinPass {
     float *fdot;                  // [ZS][B*H*N]
     float scale;
     float log2_min;               // clamp of log2 beta
-    int BH, T, N, S;
+    int BH, T, N, S, D;
     int zy;                       // a state's memory is [z][y] (else [y][z])
 };
 
@@ -106,52 +105,56 @@ __host__ __device__ __forceinline__ int lin_seg(int s, int S, int N) {
     return (int)(((long long)s * N) / S);
 }
 
+// Columns of z a CTA owns, and the floats that lie before the tiles (two tables of 4 x kLinC,
+// cumulative logs among them as pairs, and a warp's worth of sums).
 template <int D>
 struct LinSmem {
+    static constexpr int ZN = D < 64 ? D : 64;
     static constexpr int LD = D + 4;
-    static constexpr int floats = 2 * kLinC * LD + 2 * kLinC * kLinZN + D * kLinZN +
-                                  kLinC * (kLinC + 1) + 3 * kLinC + 8;
-    static constexpr size_t bytes = sizeof(Log2Sum) * kLinC + sizeof(float) * floats;
+    static constexpr int TAB = 5 * kLinC, HEAD = 2 * TAB + 8;
+    static constexpr int floats = HEAD + 2 * kLinC * LD + 2 * kLinC * ZN + D * ZN + kLinC * (kLinC + 1);
+    static constexpr size_t bytes = sizeof(float) * floats;
 };
 
 // A chunk's tile of rows [kLinC][COLS] (from [T][D] at column c0; rows past T: zeros) into
-// registers, and from there as floats into shared memory: every load of a chunk goes out
-// before the first store.
-template <typename T, int COLS>
+// registers, and from there into shared memory: every load of a chunk goes out before the
+// first store.
+template <int COLS>
 struct LinTile {
-    using V = Vec16<T>;
-    static constexpr int PER = COLS / V::N, ITEMS = kLinC * PER, N = (ITEMS + kLinThreads - 1) / kLinThreads;
-    uint4 v[N];
-    __device__ __forceinline__ void load(const T *src, int t0, int Ttot, int D, int c0) {
+    static constexpr int PER = COLS / 4, N = kLinC * PER / kLinThreads;
+    float4 v[N];
+    __device__ __forceinline__ void load(const float *src, int t0, int Ttot, int D, int c0) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const int i = threadIdx.x + k * kLinThreads, r = i / PER;
-            v[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (i < ITEMS && t0 + r < Ttot)
-                v[k] = V::raw(src + (size_t)(t0 + r) * D + c0 + (i - r * PER) * V::N);
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t0 + r < Ttot)
+                v[k] = __ldg(reinterpret_cast<const float4 *>(src + (size_t)(t0 + r) * D + c0 + (i - r * PER) * 4));
         }
     }
     __device__ __forceinline__ void store(float *dst, int ld) const {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const int i = threadIdx.x + k * kLinThreads, r = i / PER;
-            if (i >= ITEMS) continue;
-            float f[V::N];
-            V::unpack(v[k], f);
+            *reinterpret_cast<float4 *>(dst + r * ld + (i - r * PER) * 4) = v[k];
+        }
+    }
+    // row r times u[r]
+    __device__ __forceinline__ void store(float *dst, int ld, const float *u) const {
 #pragma unroll
-            for (int e = 0; e < V::N; e += 4)
-                *reinterpret_cast<float4 *>(dst + r * ld + (i - r * PER) * V::N + e) =
-                    make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        for (int k = 0; k < N; ++k) {
+            const int i = threadIdx.x + k * kLinThreads, r = i / PER;
+            const float w = u[r];
+            *reinterpret_cast<float4 *>(dst + r * ld + (i - r * PER) * 4) =
+                make_float4(w * v[k].x, w * v[k].y, w * v[k].z, w * v[k].w);
         }
     }
 };
 
-// Inclusive prefix of the clamped log2 decays of one chunk by one warp (lane =
-// token; past T: no decay).
-__device__ __forceinline__ Log2Sum lin_log_prefix(const float *beta, int t0, int T, float log2_min) {
+// Inclusive prefix of a chunk's clamped log2 decays by one warp (lane = token).
+__device__ __forceinline__ Log2Sum lin_log_prefix(float log2_beta) {
     const int lane = threadIdx.x & 31;
-    Log2Sum x = {0.f, 0.f};
-    if (t0 + lane < T) x.hi = log2_decay(beta[t0 + lane], log2_min);
+    Log2Sum x = {log2_beta, 0.f};
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const Log2Sum y = {__shfl_up_sync(0xffffffffu, x.hi, o), __shfl_up_sync(0xffffffffu, x.lo, o)};
@@ -159,116 +162,146 @@ __device__ __forceinline__ Log2Sum lin_log_prefix(const float *beta, int t0, int
     }
     return x;
 }
+// the same from memory; past T: no decay
+__device__ __forceinline__ Log2Sum lin_log_prefix(const float *beta, int t0, int T, float log2_min) {
+    const int t = t0 + (threadIdx.x & 31);
+    return lin_log_prefix(t < T ? log2_decay(beta[t], log2_min) : 0.f);
+}
 
-// grid (D / kLinZN, B*H, S), block kLinThreads.  OUT = false: the segments'
-// aggregates (states from zero) and decays only.
-template <typename T, int D, bool REV, bool OUT>
-__global__ void __launch_bounds__(kLinThreads) k_linear_pass(const LinPass p) {
+struct LinPasses {
+    LinPass pass[2];
+};
+
+// CTAs of k_linear_pass an SM holds.
+__host__ __device__ constexpr int lin_per_sm(int D) { return D > 64 ? 2 : D > 32 ? 3 : 4; }
+
+// grid (passes * D / ZN, B*H, S), block kLinThreads.  OUT = false: the segments' aggregates
+// (states from zero) and decays only.
+//
+// Warp (token group, column half) and lane (four tokens or state rows) x (eight groups of four
+// columns): a thread has R tokens x 4 columns of the outputs and SR x 4 of the state, so that
+// a row of S or z is one pass of shared memory for the warp and serves R (SR) x 4 products of
+// each thread.  Chunk n + 1's tiles and decays come from memory, and its decay table is formed,
+// while chunk n is worked on.
+template <int D, bool REV, bool OUT>
+__global__ void __launch_bounds__(kLinThreads, lin_per_sm(D))
+k_linear_pass(const __grid_constant__ LinPasses args) {
     using L = LinSmem<D>;
-    constexpr int C = kLinC, ZN = kLinZN, LD = L::LD;
+    constexpr int C = kLinC, ZN = L::ZN, LD = L::LD;
+    constexpr int HC = ZN / 32, TG = 8 / HC, R = C / (4 * TG), SR = D * ZN / 1024;
     extern __shared__ float4 lin_smem[];
-    Log2Sum *s_l = reinterpret_cast<Log2Sum *>(lin_smem);     // [C]
-    float *xs = reinterpret_cast<float *>(s_l + C);           // [C][LD]
+    float *s_tab = reinterpret_cast<float *>(lin_smem);       // [2][TAB]: l (pairs), a, u, g
+    float *s_red = s_tab + 2 * L::TAB;                        // [8]
+    float *xs = s_tab + L::HEAD;                              // [C][LD]
     float *ys = xs + C * LD;                                  // [C][LD]
     float *zs = ys + C * LD;                                  // [C][ZN]
     float *wz = zs + C * ZN;                                  // [C][ZN] u_i z_i
     float *St = wz + C * ZN;                                  // [D][ZN]
     float *Ps = St + D * ZN;                                  // [C][C + 1]
-    float *s_a = Ps + C * (C + 1), *s_u = s_a + C, *s_g = s_u + C, *s_red = s_g + C;   // s_red [8]
     griddep_launch_dependents();
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int zsp = blockIdx.x, z0 = zsp * ZN, bh = blockIdx.y, seg = blockIdx.z;
+    const LinPass &p = args.pass[blockIdx.x / (D / ZN)];
+    const int zsp = blockIdx.x % (D / ZN), z0 = zsp * ZN, bh = blockIdx.y, seg = blockIdx.z;
     const int n0 = lin_seg(seg, p.S, p.N), n1 = lin_seg(seg + 1, p.S, p.N);
     if (!OUT && seg == (REV ? 0 : p.S - 1)) return;   // never carried on
-    const T *X = static_cast<const T *>(p.x) + (size_t)bh * p.T * D;
-    const T *Y = static_cast<const T *>(p.y) + (size_t)bh * p.T * D;
-    const T *Z = static_cast<const T *>(p.z) + (size_t)bh * p.T * D;
+    const float *X = static_cast<const float *>(p.x) + (size_t)bh * p.T * D;
+    const float *Y = static_cast<const float *>(p.y) + (size_t)bh * p.T * D;
+    const float *Z = static_cast<const float *>(p.z) + (size_t)bh * p.T * D;
     const float *beta = p.beta + (size_t)bh * p.T;
     const float *gate = p.gate ? p.gate + (size_t)bh * p.T : nullptr;
 
-    // state: thread (yg, zg) owns rows 4 yg.. and columns 4 zg..
-    const int yg = tid / (ZN / 4), zg = tid % (ZN / 4);
-    const bool has_state = yg < D / 4;
-    float st[4][4];
+    const int ch = warp % HC, tg = warp / HC, zc = ch * 32 + (lane & 7) * 4;   // columns zc..zc + 3
+    const int tok = tg * 4 * R + (lane >> 3);                                  // tokens tok + 4 i
+    const int yr = (tg * 4 + (lane >> 3)) * SR;                                // state rows yr + i
+    float st[SR][4];
     auto state_at = [&](size_t base, int i, int j) {
-        const int y = 4 * yg + i, z = z0 + 4 * zg + j;
-        return base + (p.zy ? (size_t)z * D + y : (size_t)y * D + z);
+        return base + (p.zy ? (size_t)(z0 + zc + j) * D + yr + i : (size_t)(yr + i) * D + z0 + zc + j);
     };
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < SR; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) st[i][j] = 0.f;
-    if (OUT && p.start && has_state) {
+    if (OUT && p.start) {
         const size_t base = ((size_t)bh * p.S + seg) * D * D;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < SR; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) st[i][j] = p.start[state_at(base, i, j)];
     }
     const Log2Sum zero = {0.f, 0.f};
     Log2Sum seglog = zero;
 
-    // a chunk's tiles are on their way while the one before is worked on
-    LinTile<T, D> tx, ty;
-    LinTile<T, ZN> tz;
+    auto first = [&](int it) { return (REV ? n1 - 1 - it : n0 + it) * C; };
+    LinTile<D> tx, ty;
+    LinTile<ZN> tz;
+    float nl = 0.f, ng = 0.f;   // warp 0: the token's log decay and gate
     auto fetch = [&](int it) {
-        const int t0 = (REV ? n1 - 1 - it : n0 + it) * C;
+        const int t0 = first(it);
+        if (warp == 0) {
+            const bool in = t0 + lane < p.T;
+            nl = in ? log2_decay(beta[t0 + lane], p.log2_min) : 0.f;
+            ng = in ? (gate ? gate[t0 + lane] : 1.f) : 0.f;
+        }
         if (OUT) tx.load(X, t0, p.T, D, 0);
         ty.load(Y, t0, p.T, D, 0);
         tz.load(Z, t0, p.T, D, z0);
     };
+    auto table = [&](int it) {
+        if (warp) return;
+        float *t = s_tab + (it & 1) * L::TAB;
+        const Log2Sum l = lin_log_prefix(nl), lC = shfl(l, 31);
+        const float to = exp2_diff(l, zero), from = exp2_diff(lC, l);
+        reinterpret_cast<Log2Sum *>(t)[lane] = l;
+        t[2 * C + lane] = REV ? from : to;
+        t[3 * C + lane] = REV ? p.scale * to : ng * from;
+        t[4 * C + lane] = ng;
+    };
     fetch(0);
+    table(0);
     for (int it = 0; it < n1 - n0; ++it) {
-        const int n = REV ? n1 - 1 - it : n0 + it, t0 = n * C;
+        const int t0 = first(it), n = t0 / C;
+        const float *tab = s_tab + (it & 1) * L::TAB;
+        const Log2Sum *s_l = reinterpret_cast<const Log2Sum *>(tab);
+        const float *s_a = tab + 2 * C, *s_u = tab + 3 * C, *s_g = tab + 4 * C;
         __syncthreads();
-        if (has_state) {
+        if (OUT) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4 *>(St + (4 * yg + i) * ZN + 4 * zg) =
+            for (int i = 0; i < SR; ++i)
+                *reinterpret_cast<float4 *>(St + (yr + i) * ZN + zc) =
                     make_float4(st[i][0], st[i][1], st[i][2], st[i][3]);
-            if (OUT && p.states) {
-                const size_t base = ((size_t)bh * p.N + n) * D * D;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) p.states[state_at(base, i, j)] = st[i][j];
-            }
+            tx.store(xs, LD);
+            tz.store(zs, ZN);
         }
-        if (OUT) tx.store(xs, LD);
         ty.store(ys, LD);
-        tz.store(zs, ZN);
-        if (warp == 0) {
-            const Log2Sum l = lin_log_prefix(beta, t0, p.T, p.log2_min), lC = shfl(l, 31);
-            const float g = t0 + lane < p.T ? (gate ? gate[t0 + lane] : 1.f) : 0.f;
-            s_l[lane] = l;
-            s_g[lane] = g;
-            const float to = exp2_diff(l, zero), from = exp2_diff(lC, l);
-            s_a[lane] = REV ? from : to;
-            s_u[lane] = REV ? p.scale * to : g * from;
-        }
+        tz.store(wz, ZN, s_u);
         __syncthreads();
         if (it + 1 < n1 - n0) fetch(it + 1);
         const Log2Sum lC = s_l[C - 1];
         const float b = exp2_diff(lC, zero);
         seglog = seglog + lC;
-        // F: the state of the other direction against this one's, before the chunk
-        if (OUT && p.states_in) {
-            float f = 0.f;
-            if (has_state) {
+        float4 si[R];
+        if (OUT) {
+            if (p.states) {
                 const size_t base = ((size_t)bh * p.N + n) * D * D;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < SR; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        f = fmaf(st[i][j], p.states_in[state_at(base, i, j)], f);
+                    for (int j = 0; j < 4; ++j) p.states[state_at(base, i, j)] = st[i][j];
             }
-            f = warp_sum(f);
-            if (lane == 0) s_red[warp] = f;
-        }
-        for (int i = tid; i < C * ZN; i += kLinThreads) wz[i] = s_u[i / ZN] * zs[i];
-        if (OUT) {
-            // P: thread (tr, tc) holds rows tr, tr + 16 and columns tc, tc + 16
+            // F: the state of the other direction against this one's, before the chunk
+            if (p.states_in) {
+                float f = 0.f;
+                const size_t base = ((size_t)bh * p.N + n) * D * D;
+#pragma unroll
+                for (int i = 0; i < SR; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) f = fmaf(st[i][j], p.states_in[state_at(base, i, j)], f);
+                f = warp_sum(f);
+                if (lane == 0) s_red[warp] = f;
+            }
+            // P: thread (tr, tc) holds rows tr, tr + 16 and columns tc, tc + 16, but for the
+            // pair beyond the diagonal
             const int tr = tid >> 4, tc = tid & 15;
             float acc[2][2] = {};
 #pragma unroll 4
@@ -283,6 +316,7 @@ __global__ void __launch_bounds__(kLinThreads) k_linear_pass(const LinPass p) {
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
+                        if (REV ? i > j : i < j) continue;
                         acc[i][j] = fmaf(xv[i].x, yv[j].x, acc[i][j]);
                         acc[i][j] = fmaf(xv[i].y, yv[j].y, acc[i][j]);
                         acc[i][j] = fmaf(xv[i].z, yv[j].z, acc[i][j]);
@@ -299,84 +333,113 @@ __global__ void __launch_bounds__(kLinThreads) k_linear_pass(const LinPass p) {
                     Ps[t * (C + 1) + c] =
                         in ? acc[i][j] * w * (REV ? exp2_diff(s_l[c], s_l[t]) : exp2_diff(s_l[t], s_l[c])) : 0.f;
                 }
+            // the state's part of the outputs
+#pragma unroll
+            for (int i = 0; i < R; ++i) si[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int d = 0; d < D; d += 4) {
+                float xa[R][4];
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float4 xv = *reinterpret_cast<const float4 *>(xs + (tok + 4 * i) * LD + d);
+                    xa[i][0] = xv.x; xa[i][1] = xv.y; xa[i][2] = xv.z; xa[i][3] = xv.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float4 s = *reinterpret_cast<const float4 *>(St + (d + e) * ZN + zc);
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        si[i].x = fmaf(xa[i][e], s.x, si[i].x);
+                        si[i].y = fmaf(xa[i][e], s.y, si[i].y);
+                        si[i].z = fmaf(xa[i][e], s.z, si[i].z);
+                        si[i].w = fmaf(xa[i][e], s.w, si[i].w);
+                    }
+                }
+            }
         }
-        __syncthreads();
+        if (it + 1 < n1 - n0) table(it + 1);
         if (OUT) {
+            __syncthreads();
             if (p.states_in && tid == 0) {
                 float f = 0.f;
                 for (int w = 0; w < kLinThreads / 32; ++w) f += s_red[w];
                 p.fdot[((size_t)zsp * p.BH + bh) * p.N + n] = b * f;
             }
-            // out: thread (t, zc) holds 4 columns of one token
-            const int t = tid >> 3, zc = (tid & 7) * 4;
-            float4 si = make_float4(0.f, 0.f, 0.f, 0.f), in = si;
+            // the chunk's own part, over the tokens of the thread's warp or before (after) them
+            float4 in[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) in[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int i0 = REV ? tg * 4 * R : 0, i1 = REV ? C : (tg + 1) * 4 * R;
 #pragma unroll 4
-            for (int d = 0; d < D; d += 4) {
-                const float4 xv = *reinterpret_cast<const float4 *>(xs + t * LD + d);
-                const float xa[4] = {xv.x, xv.y, xv.z, xv.w};
+            for (int c = i0; c < i1; ++c) {
+                const float4 z = *reinterpret_cast<const float4 *>(zs + c * ZN + zc);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 s = *reinterpret_cast<const float4 *>(St + (d + e) * ZN + zc);
-                    si.x = fmaf(xa[e], s.x, si.x);
-                    si.y = fmaf(xa[e], s.y, si.y);
-                    si.z = fmaf(xa[e], s.z, si.z);
-                    si.w = fmaf(xa[e], s.w, si.w);
+                for (int i = 0; i < R; ++i) {
+                    const float pv = Ps[(tok + 4 * i) * (C + 1) + c];
+                    in[i].x = fmaf(pv, z.x, in[i].x);
+                    in[i].y = fmaf(pv, z.y, in[i].y);
+                    in[i].z = fmaf(pv, z.z, in[i].z);
+                    in[i].w = fmaf(pv, z.w, in[i].w);
                 }
             }
-            const int i0 = REV ? t : 0, i1 = REV ? C : t + 1;
-            for (int i = i0; i < i1; ++i) {
-                const float pv = Ps[t * (C + 1) + i];
-                const float4 z = *reinterpret_cast<const float4 *>(zs + i * ZN + zc);
-                in.x = fmaf(pv, z.x, in.x);
-                in.y = fmaf(pv, z.y, in.y);
-                in.z = fmaf(pv, z.z, in.z);
-                in.w = fmaf(pv, z.w, in.w);
-            }
-            const float a = s_a[t] * (REV ? 1.f : p.scale), c = REV ? s_g[t] : p.scale;
-            float r[4] = {a * si.x, a * si.y, a * si.z, a * si.w};   // state part (without g)
-            const size_t row = (size_t)bh * p.T + t0 + t;
-            if (p.dot) {
-                float d = 0.f;
-                if (t0 + t < p.T) {
-                    const T *xd = static_cast<const T *>(p.xd) + row * D + z0 + zc;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) d = fmaf(r[e], load_f(xd + e), d);
+            for (int i = 0; i < R; ++i) {
+                const int t = tok + 4 * i;
+                const bool inside = t0 + t < p.T;
+                const float a = s_a[t] * (REV ? 1.f : p.scale), c = REV ? s_g[t] : p.scale;
+                const float4 r = make_float4(a * si[i].x, a * si[i].y, a * si[i].z, a * si[i].w);   // (without g)
+                const size_t row = (size_t)bh * p.T + t0 + t;
+                if (p.dot) {
+                    float d = 0.f;
+                    if (inside) {
+                        const float4 xd = __ldg(reinterpret_cast<const float4 *>(
+                            static_cast<const float *>(p.xd) + row * D + z0 + zc));
+                        d = fmaf(r.x, xd.x, fmaf(r.y, xd.y, fmaf(r.z, xd.z, r.w * xd.w)));
+                    }
+#pragma unroll
+                    for (int o = 4; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+                    if ((lane & 7) == 0 && inside) p.dot[(size_t)(zsp * HC + ch) * p.BH * p.T + row] = d;
                 }
-#pragma unroll
-                for (int o = 4; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                if ((tid & 7) == 0 && t0 + t < p.T) p.dot[(size_t)zsp * p.BH * p.T + row] = d;
-            }
-            if (t0 + t < p.T) {
-                const float pin[4] = {in.x, in.y, in.z, in.w};
-                T *o = static_cast<T *>(p.out) + row * D + z0 + zc;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    store_f(o + e, REV ? c * (r[e] + pin[e]) : fmaf(c, pin[e], r[e]));
+                if (inside)
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * D + z0 + zc) =
+                        REV ? make_float4(c * (r.x + in[i].x), c * (r.y + in[i].y), c * (r.z + in[i].z),
+                                          c * (r.w + in[i].w))
+                            : make_float4(fmaf(c, in[i].x, r.x), fmaf(c, in[i].y, r.y), fmaf(c, in[i].z, r.z),
+                                          fmaf(c, in[i].w, r.w));
             }
         }
         // S' = b S + sum_i y_i (u_i z_i)^T
-        if (has_state) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < SR; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) st[i][j] *= b;
+            for (int j = 0; j < 4; ++j) st[i][j] *= b;
 #pragma unroll 4
-            for (int i = 0; i < C; ++i) {
-                const float4 yv = *reinterpret_cast<const float4 *>(ys + i * LD + 4 * yg);
-                const float4 zv = *reinterpret_cast<const float4 *>(wz + i * ZN + 4 * zg);
-                const float ya[4] = {yv.x, yv.y, yv.z, yv.w}, za[4] = {zv.x, zv.y, zv.z, zv.w};
+        for (int c = 0; c < C; ++c) {
+            const float4 zv = *reinterpret_cast<const float4 *>(wz + c * ZN + zc);
+            float ya[SR];
+            if constexpr (SR >= 4) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int i = 0; i < SR; i += 4) {
+                    const float4 yv = *reinterpret_cast<const float4 *>(ys + c * LD + yr + i);
+                    ya[i] = yv.x; ya[i + 1] = yv.y; ya[i + 2] = yv.z; ya[i + 3] = yv.w;
+                }
+            } else {
+                ya[0] = ys[c * LD + yr];
+            }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) st[e][j] = fmaf(ya[e], za[j], st[e][j]);
+            for (int i = 0; i < SR; ++i) {
+                st[i][0] = fmaf(ya[i], zv.x, st[i][0]);
+                st[i][1] = fmaf(ya[i], zv.y, st[i][1]);
+                st[i][2] = fmaf(ya[i], zv.z, st[i][2]);
+                st[i][3] = fmaf(ya[i], zv.w, st[i][3]);
             }
         }
     }
     float *dst = OUT ? (seg == (REV ? 0 : p.S - 1) ? p.last : nullptr) : p.agg;
-    if (dst && has_state) {
+    if (dst) {
         const size_t base = OUT ? (size_t)bh * D * D : ((size_t)bh * p.S + seg) * D * D;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < SR; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) dst[state_at(base, i, j)] = st[i][j];
     }
@@ -429,12 +492,12 @@ struct LinPairs {
     const float *fdot;             // [ZS][B*H*N]
     float *dbeta, *dgate;          // [B*H, T]; dgate nullable
     float scale;
-    int BH, T, N, ZS;
+    int BH, T, N, ZS, FS;          // ZS planes of zeta and eta, FS of fdot
 };
 
 // dbeta and dgate of one chunk from its pair terms (top of this file).
 // grid (N, B*H), block kLinThreads.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kLinThreads) k_linear_pairs(const LinPairs p) {
     constexpr int C = kLinC, LD = D + 4;
     extern __shared__ float4 lin_smem[];
@@ -443,16 +506,15 @@ __global__ void __launch_bounds__(kLinThreads) k_linear_pairs(const LinPairs p) 
           *os = vs + C * LD;
     float *As = os + C * LD;                       // [C][C + 1]
     float *s_g = As + C * (C + 1), *s_ze = s_g + C, *s_ge = s_ze + C;
-    griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = blockIdx.x, bh = blockIdx.y, t0 = n * C;
     const size_t head = (size_t)bh * p.T, rowsall = (size_t)p.BH * p.T;
     {
-        LinTile<T, D> tq, tk, tv, to;
-        tq.load(static_cast<const T *>(p.q) + head * D, t0, p.T, D, 0);
-        tk.load(static_cast<const T *>(p.k) + head * D, t0, p.T, D, 0);
-        tv.load(static_cast<const T *>(p.v) + head * D, t0, p.T, D, 0);
-        to.load(static_cast<const T *>(p.d_o) + head * D, t0, p.T, D, 0);
+        LinTile<D> tq, tk, tv, to;
+        tq.load(static_cast<const float *>(p.q) + head * D, t0, p.T, D, 0);
+        tk.load(static_cast<const float *>(p.k) + head * D, t0, p.T, D, 0);
+        tv.load(static_cast<const float *>(p.v) + head * D, t0, p.T, D, 0);
+        to.load(static_cast<const float *>(p.d_o) + head * D, t0, p.T, D, 0);
         tq.store(qs, LD);
         tk.store(ks, LD);
         tv.store(vs, LD);
@@ -462,6 +524,7 @@ __global__ void __launch_bounds__(kLinThreads) k_linear_pairs(const LinPairs p) 
     if (warp == 0) {
         s_l[lane] = lin_log_prefix(p.beta + head, t0, p.T, kLinLog2MinBwd);
         float zeta = 0.f, g = 0.f;
+        griddep_wait();   // the passes are done (what came before them was, before the first began)
         if (t0 + lane < p.T) {
             g = p.gate ? p.gate[head + t0 + lane] : 1.f;
             for (int z = 0; z < p.ZS; ++z) {
@@ -538,7 +601,7 @@ __global__ void __launch_bounds__(kLinThreads) k_linear_pairs(const LinPairs p) 
     __syncthreads();
     if (warp == 0 && t0 + lane < p.T) {
         float d = s_ze[lane] + s_ge[lane];
-        for (int z = 0; z < p.ZS; ++z) d += p.fdot[((size_t)z * p.BH + bh) * p.N + n];
+        for (int z = 0; z < p.FS; ++z) d += p.fdot[((size_t)z * p.BH + bh) * p.N + n];
         float pairs = 0.f;
         for (int s = lane; s < C; ++s) pairs += As[s * (C + 1) + lane];
         const float bt = fmaxf(p.beta[head + t0 + lane], 8.6736174e-19f);   // 2^-60

@@ -57,7 +57,7 @@ constexpr int kLtGroup = 256;                   // threads of an arithmetic grou
 constexpr int kLtThreads = 2 * kLtGroup + 128;  // + two issuers, the decay warp, the loader
 constexpr int kLtTabs = 4;                      // stages of decay tables
 constexpr int kLtTabF = 8 * kLtC + 4;           // floats of a table
-constexpr int kLtDots = 4, kLtFdots = 16;       // planes of dot and fdot partials per pass
+constexpr int kLtDots = 2, kLtFdots = 8;        // planes of dot and fdot partials per column split
 constexpr uint32_t kLtProbes = 1u << 20;
 constexpr uint32_t kLtHintNs = 2000;            // a probe suspends its warp for up to this long
 
@@ -85,6 +85,10 @@ struct LinTcPass {
     LinPass p;
     const float *tab;             // decay tables of the pass's direction
 };
+// Column splits of z, and the bytes of a tile of x or y: a head of 32 or 64 columns has one
+// column half (32: the rest of its box reads as zeros).
+__host__ __device__ __forceinline__ int lt_splits(int D) { return D > kLtZN ? D / kLtZN : 1; }
+__device__ __forceinline__ uint32_t lt_tile_bytes(int D) { return D > 64 ? LtSmem::TILE : LtSmem::HALF; }
 struct LinTcArgs {
     LinTcPass pass[2];
 };
@@ -280,11 +284,11 @@ __device__ __forceinline__ void lt_parts(const uint8_t *z, uint8_t *dst, float u
 }
 
 // grid (2 * passes, B*H, S), block kLtThreads.
-template <bool REV>
+template <bool REV, bool GRAD>
 __global__ void __launch_bounds__(kLtThreads, 1)
 k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_flag) {
     using L = LtSmem;
-    constexpr int C = kLtC, D = 128;
+    constexpr int C = kLtC;
     // the swizzled tiles start at the array's own 1024-byte boundary: operand addresses are
     // constants, which an MMA takes without a register (checked below)
     extern __shared__ __align__(1024) uint8_t lt_smem[];
@@ -300,10 +304,13 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     uint32_t *tbase = reinterpret_cast<uint32_t *>(sm + L::TBASE);
     const uint32_t abort = sb + L::TBASE + 4;
     float *s_tab = reinterpret_cast<float *>(sm + L::TAB);
-    const LinTcPass &A = args.pass[blockIdx.x >> 1];
+    const int ZS = lt_splits(args.pass[0].p.D);
+    const LinTcPass &A = args.pass[blockIdx.x / ZS];
     const LinPass &p = A.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int zh = blockIdx.x & 1, bh = blockIdx.y, seg = blockIdx.z;
+    const int zh = blockIdx.x % ZS, bh = blockIdx.y, seg = blockIdx.z, D = p.D;
+    const uint32_t tile = lt_tile_bytes(D);   // of a tile of x or y in memory
+    const bool three = GRAD && p.dot;         // OS takes the state in three parts, not two
     const int n0 = lin_seg(seg, p.S, p.N), n1 = lin_seg(seg + 1, p.S, p.N), NL = n1 - n0;
     auto chunk = [&](int it) { return REV ? n1 - 1 - it : n0 + it; };
 
@@ -383,7 +390,15 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < 16; ++kk)   // K steps against S_hi, then S_lo, 16 KB on
-                    mma_bf16_ta(tmem + kOS, tmem + kX + (kk & 7) * 8, d_s + mnmaj(kk), ID_O, kk > 0);
+                    if ((kk & 7) * 16 < D)
+                        mma_bf16_ta(tmem + kOS, tmem + kX + (kk & 7) * 8, d_s + mnmaj(kk), ID_O, kk > 0);
+                if (three) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)   // and the third part
+                        if (kk * 16 < D)
+                            mma_bf16_ta(tmem + kOS, tmem + kX + kk * 8, d_u + 2 * (L::HALF / 16) + mnmaj(kk), ID_O,
+                                        true);
+                }
                 lt_commit(b_os);
             }
             ok = wait(b_parts, ph);
@@ -414,7 +429,8 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             tc::fence_after_sync();
             if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) cp_128x256b(tmem + kX + kk * 8, d_x + kmaj(kk));
+                for (int kk = 0; kk < 8; ++kk)
+                    if (kk * 16 < D) cp_128x256b(tmem + kX + kk * 8, d_x + kmaj(kk));
                 lt_commit(b_xfree);
             }
             return true;
@@ -424,7 +440,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 const uint64_t y = d_y + (it & 1) * (L::TILE / 16);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16_ta(tmem + kP, tmem + kX + kk * 8, y + kmaj(kk), ID_P, kk > 0);
+                    if (kk * 16 < D) mma_bf16_ta(tmem + kP, tmem + kX + kk * 8, y + kmaj(kk), ID_P, kk > 0);
                 lt_commit(b_p);
             }
         };
@@ -468,16 +484,16 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             int loads_x = 0, loads_y = 0, loads_z = 0, loads_t = 0;   // begun
             auto load_x = [&](int it) {
                 const int t0 = chunk(it) * C;
-                lt_expect(b_xy + 8 * (it & 1), L::TILE);
+                lt_expect(b_xy + 8 * (it & 1), tile);
                 tma_load_3d(sm + L::X, &A.x, 0, t0, bh, b_xy + 8 * (it & 1));
-                tma_load_3d(sm + L::X + L::HALF, &A.x, 64, t0, bh, b_xy + 8 * (it & 1));
+                if (D > 64) tma_load_3d(sm + L::X + L::HALF, &A.x, 64, t0, bh, b_xy + 8 * (it & 1));
                 ++loads_x;
             };
             auto load_y = [&](int it) {
                 const int st = it & 1, t0 = chunk(it) * C;
-                lt_expect(b_xy + 8 * st, L::TILE);
+                lt_expect(b_xy + 8 * st, tile);
                 tma_load_3d(sm + L::Y + st * L::TILE, &A.y, 0, t0, bh, b_xy + 8 * st);
-                tma_load_3d(sm + L::Y + st * L::TILE + L::HALF, &A.y, 64, t0, bh, b_xy + 8 * st);
+                if (D > 64) tma_load_3d(sm + L::Y + st * L::TILE + L::HALF, &A.y, 64, t0, bh, b_xy + 8 * st);
                 ++loads_y;
             };
             auto load_z = [&](int it) {
@@ -624,9 +640,9 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 const int t = chunk(it) * C + row;
                 const size_t grow = (size_t)bh * p.T + t;
                 const bool in = t < p.T;
-                const bool dots = p.dot && in;
+                const bool dots = GRAD && p.dot && in;
                 uint4 xd[4] = {};   // (in flight while the products run)
-                if (dots) {
+                if (dots && z0 < D) {
                     const uint4 *src = reinterpret_cast<const uint4 *>(
                         static_cast<const __nv_bfloat16 *>(p.xd) + grow * D + z0);
 #pragma unroll
@@ -676,6 +692,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     } else {
         // ---- state: thread has y row `row`, 32 columns of z ----
         const int half = (warp >> 2) & 1, z0 = zh * kLtZN + half * 32, gt = tid - kLtGroup;
+        const bool owns = row < D && z0 < D;   // else: nothing of the state in memory
         float st[32];
         // a state in memory: [y][z], or [z][y] (then lanes are neighbours)
         auto at = [&](size_t base, int j) {
@@ -684,7 +701,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
 #pragma unroll
         for (int j = 0; j < 32; ++j) st[j] = 0.f;
         griddep_wait();
-        if (p.start) {
+        if (p.start && owns) {
             const size_t base = ((size_t)bh * p.S + seg) * D * D;
 #pragma unroll
             for (int j = 0; j < 32; ++j) st[j] = p.start[at(base, j)];
@@ -694,24 +711,29 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             const int sg = it & 1, ph = it & 1, ts = it % kLtTabs, n = chunk(it);
             const float *tab = s_tab + ts * kLtTabF;
             {
-                // the state before the chunk as the B operand, rows of y, two bf16 parts
+                // the state before the chunk as the B operand, rows of y, two or three bf16 parts
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    uint32_t a[4], b[4];
+                    uint32_t a[4], b[4], c[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 y = make_float2(st[h * 8 + 2 * e], st[h * 8 + 2 * e + 1]);
+                        float2 y = make_float2(st[h * 8 + 2 * e], st[h * 8 + 2 * e + 1]);
                         a[e] = f2_bf16x2(y);
-                        b[e] = f2_bf16x2(f2_rest(y, a[e]));
+                        y = f2_rest(y, a[e]);
+                        b[e] = f2_bf16x2(y);
+                        c[e] = GRAD ? f2_bf16x2(f2_rest(y, b[e])) : 0u;
                     }
-                    uint8_t *dst = sm + L::SOP + row * 128 + (((half * 4 + h) ^ (row & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
-                    *reinterpret_cast<uint4 *>(dst + L::HALF) = make_uint4(b[0], b[1], b[2], b[3]);
+                    const uint32_t at = row * 128 + (((half * 4 + h) ^ (row & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(sm + L::SOP + at) = make_uint4(a[0], a[1], a[2], a[3]);
+                    *reinterpret_cast<uint4 *>(sm + L::SOP + L::HALF + at) = make_uint4(b[0], b[1], b[2], b[3]);
+                    if (three)   // in the place of the third part of u z, which waits for OS
+                        *reinterpret_cast<uint4 *>(sm + L::PARTS + 2 * L::HALF + at) = make_uint4(c[0], c[1], c[2], c[3]);
                 }
                 fence_proxy_async_smem();
                 arrive(b_s);
             }
-            ok = wait(b_w + 8 * ts, (it / kLtTabs) & 1) && wait(b_z + 8 * sg, (it >> 1) & 1);
+            ok = wait(b_w + 8 * ts, (it / kLtTabs) & 1) && wait(b_z + 8 * sg, (it >> 1) & 1) &&
+                 (!three || wait(b_os, ph));
             if (!ok) break;
 #pragma unroll 1
             for (int item = gt; item < 1024; item += kLtGroup)   // row item / 8
@@ -719,16 +741,18 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             fence_proxy_async_smem();
             arrive(b_parts);
             const float b = tab[8 * C];
-            if (p.states) {
+            if (GRAD && p.states && owns) {
                 float *dst = p.states + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) dst[j * D] = st[j];
             }
-            if (p.states_in) {
-                const float *src = p.states_in + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
+            if (GRAD && p.states_in) {
                 float f = 0.f;
+                if (owns) {
+                    const float *src = p.states_in + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) f = fmaf(st[j], __ldcs(src + j * D), f);
+                    for (int j = 0; j < 32; ++j) f = fmaf(st[j], __ldcs(src + j * D), f);
+                }
                 f = warp_sum(f);
                 if (lane == 0) p.fdot[((size_t)(zh * 8 + warp - 8) * p.BH + bh) * p.N + n] = b * f;
             }
@@ -752,7 +776,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             tc::fence_before_sync();
             arrive(b_tfree + 8 * ts);
         }
-        if (ok && p.last && seg == (REV ? 0 : p.S - 1)) {
+        if (ok && p.last && owns && seg == (REV ? 0 : p.S - 1)) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) p.last[at((size_t)bh * D * D, j)] = st[j];
         }
@@ -790,7 +814,7 @@ template <bool REV>
 __global__ void __launch_bounds__(kLtThreads, 1)
 k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_flag) {
     using L = LaSmem;
-    constexpr int C = kLtC, D = 128, PARTB = 3 * LtSmem::HALF;
+    constexpr int C = kLtC, PARTB = 3 * LtSmem::HALF;
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smem_align1024(smraw);
     const uint32_t sb = smem_u32(sm), bars = sb + L::BARS;
@@ -800,7 +824,7 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
     float *s_u = reinterpret_cast<float *>(sm + L::U);
     const LinPass &p = A.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int zh = blockIdx.x, bh = blockIdx.y, seg = blockIdx.z;
+    const int zh = blockIdx.x, bh = blockIdx.y, seg = blockIdx.z, D = p.D;
     if (seg == (REV ? 0 : p.S - 1)) return;   // never carried on
     const int n0 = lin_seg(seg, p.S, p.N), n1 = lin_seg(seg + 1, p.S, p.N), NL = n1 - n0;
     auto chunk = [&](int it) { return REV ? n0 + it : n1 - 1 - it; };
@@ -859,10 +883,11 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
                 const int st = it & 1, t0 = chunk(it) * C;
                 if (it >= 2) ok = lt_wait(b_ds + 8 * st, ((it >> 1) - 1) & 1, abort);
                 if (!ok) break;
-                lt_expect(b_yz + 8 * st, LtSmem::TILE + LtSmem::HALF + 4 * kLtC + 16);
+                lt_expect(b_yz + 8 * st, lt_tile_bytes(D) + LtSmem::HALF + 4 * kLtC + 16);
                 tma_load_3d(sm + L::Z + st * LtSmem::HALF, &A.z, zh * kLtZN, t0, bh, b_yz + 8 * st);
                 tma_load_3d(sm + L::Y + st * LtSmem::TILE, &A.y, 0, t0, bh, b_yz + 8 * st);
-                tma_load_3d(sm + L::Y + st * LtSmem::TILE + LtSmem::HALF, &A.y, 64, t0, bh, b_yz + 8 * st);
+                if (D > 64)
+                    tma_load_3d(sm + L::Y + st * LtSmem::TILE + LtSmem::HALF, &A.y, 64, t0, bh, b_yz + 8 * st);
                 if (it == 0) griddep_wait();   // the tables' kernel is done
                 const float *tab = A.tab + ((size_t)bh * p.N + chunk(it)) * kLtTabF;
                 lt_bulk_load(sb + L::U + st * (4 * kLtC + 16), tab + kLtC, 4 * kLtC, b_yz + 8 * st);
@@ -908,9 +933,10 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
             tc::tmem_ld16(tl, w);
             tc::tmem_wait_ld();
             const size_t base = ((size_t)bh * p.S + seg) * D * D;
+            if (row < D && z0 < D)
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                p.agg[base + (p.zy ? (size_t)(z0 + j) * D + row : (size_t)row * D + z0 + j)] = w[j] + v[j];
+                for (int j = 0; j < 16; ++j)
+                    p.agg[base + (p.zy ? (size_t)(z0 + j) * D + row : (size_t)row * D + z0 + j)] = w[j] + v[j];
         }
     }
     tc::fence_before_sync();
@@ -951,7 +977,7 @@ struct LpSmem {
 struct LinPairsTc {
     CUtensorMap q, k, v, d_o;
     LinPairs p;
-    int FS;          // planes of fdot (at most 32)
+    int D;
 };
 
 // x[j] over the 32 lanes of a warp: lane j returns the sum of every lane's x[j].
@@ -1002,12 +1028,11 @@ k_linear_pairs_tc(const __grid_constant__ LinPairsTc args, int *__restrict__ tim
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tbase;
-    griddep_wait();
     bool ok = true;
     if (tid == kLpThreads - 32) {   // warps 0-3 prepare the tokens meanwhile
         auto load = [&](const CUtensorMap *a, const CUtensorMap *b, uint32_t bar) {
-            lt_expect(bar, 2 * LtSmem::TILE);
-            for (int h = 0; h < 2; ++h) {
+            lt_expect(bar, 2 * lt_tile_bytes(args.D));
+            for (int h = 0; h * 64 < args.D; ++h) {
                 tma_load_3d(sm + L::A + h * LtSmem::HALF, a, h * 64, t0, bh, bar);
                 tma_load_3d(sm + L::B + h * LtSmem::HALF, b, h * 64, t0, bh, bar);
             }
@@ -1019,7 +1044,7 @@ k_linear_pairs_tc(const __grid_constant__ LinPairsTc args, int *__restrict__ tim
             constexpr uint32_t ID = tc::idesc_bf16(128, 128, false, false);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-                tc::mma_f16(tmem + col, kmaj(L::A, kk), kmaj(L::B, kk), ID, kk > 0);
+                if (kk * 16 < args.D) tc::mma_f16(tmem + col, kmaj(L::A, kk), kmaj(L::B, kk), ID, kk > 0);
             lt_commit(bar);
         };
         load(&args.q, &args.k, bars + 8 * 0);
@@ -1045,7 +1070,8 @@ k_linear_pairs_tc(const __grid_constant__ LinPairsTc args, int *__restrict__ tim
     // tokens by threads 0..127: logs, gates, and the sums of zeta from and g eta before a token
     float eta = 0.f, zeta = 0.f, ge = 0.f, through = 0.f;
     if (tid < C) {
-        if (lane < args.FS) through = p.fdot[((size_t)lane * p.BH + bh) * p.N + n];   // FS <= 32
+        griddep_wait();   // the passes are done (what came before them was, before the first began)
+        if (lane < p.FS) through = p.fdot[((size_t)lane * p.BH + bh) * p.N + n];   // FS <= 32
         through = warp_sum(through);
         const int t = t0 + tid;
         float g = 0.f;
