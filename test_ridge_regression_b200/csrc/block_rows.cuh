@@ -312,23 +312,35 @@ k_block_in_grad(const BlockInArgs a, const BlockInGrad g) {
     T *out = static_cast<T *>(k.kind == 0 ? g.xq : k.kind == 1 ? g.xk : g.xv) + lane * V::N;
     const int rep = k.kind ? a.H / a.Hk : 1;
     const int len = a.lengths ? min(a.lengths[k.at.b], a.T) : a.T;
-    uint4 x[RPT];
+    uint4 x[RPT], d[RPT];
     float dy[RPT][V::N];
+    // the loads of all the group's rows go out together
+    auto grads = [&](int h) {
+#pragma unroll
+        for (int j = 0; j < RPT; ++j) {
+            const SlotRow s = tile_row(tile, k.at, grp + j * GROUPS, len, k.heads);
+            d[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (s.in) d[j] = V::raw(up + (((size_t)k.at.b * a.H + s.slot * rep + h) * a.T + s.t) * D);
+        }
+    };
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
         const SlotRow s = tile_row(tile, k.at, grp + j * GROUPS, len, k.heads);
         x[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (s.in && k.kind < 2) x[j] = V::raw(src + s.t * in.st + s.slot * in.sh);
+    }
+    grads(0);
 #pragma unroll
-        for (int i = 0; i < V::N; ++i) dy[j][i] = 0.f;
-        if (!s.in) continue;
-        if (k.kind < 2) x[j] = V::raw(src + s.t * in.st + s.slot * in.sh);
-        // a shared key or value head collects the gradients of its group
-        const T *u = up + (((size_t)k.at.b * a.H + s.slot * rep) * a.T + s.t) * D;
-        for (int h = 0; h < rep; ++h, u += (size_t)a.T * D) {
-            float d[V::N];
-            V::load(u, d);
+    for (int j = 0; j < RPT; ++j) V::unpack(d[j], dy[j]);
+    // a shared key or value head collects the gradients of its group
+    for (int h = 1; h < rep; ++h) {
+        grads(h);
 #pragma unroll
-            for (int i = 0; i < V::N; ++i) dy[j][i] += d[i];
+        for (int j = 0; j < RPT; ++j) {
+            float y[V::N];
+            V::unpack(d[j], y);
+#pragma unroll
+            for (int i = 0; i < V::N; ++i) dy[j][i] += y[i];
         }
     }
 #pragma unroll
@@ -396,42 +408,47 @@ k_block_out(const BlockOutArgs a, T *__restrict__ y) {
     const TileAt at = tile_at<GROUPS * RPT>(a.tile, blockIdx.x);
     float w[V::N];
 #pragma unroll
-    for (int i = 0; i < V::N; ++i) w[i] = a.w[lane * V::N + i];
-    float u[RPT][V::N], z[RPT][V::N];
+    for (int i = 0; i < V::N; i += 4) Vec16<float>::load(a.w + lane * V::N + i, w + i);
+    uint4 o[RPT], v[RPT], z[RPT];   // the loads of all the group's rows go out together
+    float sk[RPT];
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
         const SlotRow s = tile_row(a.tile, at, grp + j * GROUPS, a.T, a.H);
-#pragma unroll
-        for (int i = 0; i < V::N; ++i) u[j][i] = z[j][i] = 0.f;
+        o[j] = v[j] = z[j] = make_uint4(0u, 0u, 0u, 0u);
+        sk[j] = 0.f;
         if (!s.in) continue;
-        const size_t r = ((size_t)s.b * a.H + s.slot) * a.T + s.t;
-        V::load(static_cast<const T *>(a.o) + r * D + lane * V::N, u[j]);
+        const size_t r = (((size_t)s.b * a.H + s.slot) * a.T + s.t) * D + lane * V::N;
+        o[j] = V::raw(static_cast<const T *>(a.o) + r);
         if (a.z.ptr)
-            V::load(static_cast<const T *>(a.z.ptr) + s.b * a.z.sb + s.t * a.z.st + s.slot * a.z.sh +
-                        lane * V::N, z[j]);
+            z[j] = V::raw(static_cast<const T *>(a.z.ptr) + s.b * a.z.sb + s.t * a.z.st + s.slot * a.z.sh +
+                          lane * V::N);
         if (a.v) {
-            float v[V::N];
-            V::load(static_cast<const T *>(a.v) + r * D + lane * V::N, v);
-            const float sk = a.skip[s.slot];
-#pragma unroll
-            for (int i = 0; i < V::N; ++i) u[j][i] = fmaf(sk, v[i], u[j][i]);
+            v[j] = V::raw(static_cast<const T *>(a.v) + r);
+            sk[j] = a.skip[s.slot];
         }
     }
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
         const SlotRow s = tile_row(a.tile, at, grp + j * GROUPS, a.T, a.H);
-        float ss = 0.f;
+        float u[V::N], g[V::N], ss = 0.f;
+        V::unpack(o[j], u);
+        if (a.v) {
+            V::unpack(v[j], g);
 #pragma unroll
-        for (int i = 0; i < V::N; ++i) ss = fmaf(u[j][i], u[j][i], ss);
+            for (int i = 0; i < V::N; ++i) u[i] = fmaf(sk[j], g[i], u[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) ss = fmaf(u[i], u[i], ss);
         ss = row_sum<LPR>(ss);
         if (!s.in) continue;
         const float rn = rsqrtf(ss * (1.f / D) + a.eps);
+        V::unpack(z[j], g);
 #pragma unroll
         for (int i = 0; i < V::N; ++i) {
-            u[j][i] *= rn * w[i];
-            if (a.z.ptr) u[j][i] *= z[j][i] * sigmoid_row<T>(z[j][i]);
+            u[i] *= rn * w[i];
+            if (a.z.ptr) u[i] *= g[i] * sigmoid_row<T>(g[i]);
         }
-        V::store(y + (((size_t)s.b * a.T + s.t) * a.H + s.slot) * D + lane * V::N, u[j]);
+        V::store(y + (((size_t)s.b * a.T + s.t) * a.H + s.slot) * D + lane * V::N, u);
     }
 }
 

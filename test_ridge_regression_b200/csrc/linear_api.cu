@@ -390,11 +390,11 @@ static int out_blocks(int B, int T, int H, int D, gka_dtype dt) {
     return (int)std::max<size_t>(1, std::min(rounds, most));
 }
 
-// Tiles of R rows over B x slots x T: 8 slots by R / 8 tokens, or fewer tokens and more
-// slots where the sequences are short.  Returns their number.
+// Tiles of R rows over B x slots x T: 8 slots by R / 8 tokens, with fewer slots where there
+// are not as many, and fewer tokens where the sequences are short.  Returns their number.
 static size_t row_tiles(int R, int B, int T, int slots, RowTile *g) {
     int tb = 0;
-    while ((1 << tb) < T && (1 << tb) < R / 8) ++tb;
+    while ((1 << tb) < T && (1 << tb) < R && ((1 << tb) < R / 8 || (R >> tb) >= 2 * slots)) ++tb;
     g->tb = tb;
     g->tcount = (unsigned)(((size_t)T + (1u << tb) - 1) >> tb);
     g->scount = (unsigned)((slots + (R >> tb) - 1) / (R >> tb));
