@@ -307,10 +307,10 @@ int gka_solver_study(const void *q, const void *k, const float *beta, const floa
  *               and may be initial_state itself; T = 0 copies the one to the other
  *   workspace   at least gka_linear_forward_workspace_bytes(), 256-byte aligned
  *               (0 bytes for some sizes: then NULL will do)
- * B*H is at most 65535.  The state is carried in fp32.  With bf16 inputs and D = 128
- * the products run on the tensor cores (fp32 accumulation): inputs enter exactly, the
- * state and its increments in two and three bf16 parts (16 and 24 bits), the decayed
- * scores rounded once to bf16.  Every other case runs on CUDA cores in fp32.
+ * B*H is at most 65535.  The state is carried in fp32.  With bf16 inputs the products
+ * run on the tensor cores (fp32 accumulation): inputs enter exactly, the state and its
+ * increments in two (the gradients' three) and three bf16 parts (16 and 24 bits), the
+ * decayed scores rounded once to bf16.  fp32 inputs run on CUDA cores in fp32.
  */
 size_t gka_linear_forward_workspace_bytes(int B, int H, int T, int D, gka_dtype dt);
 int gka_linear_forward(const void *q, const void *k, const void *v, const float *beta,

@@ -1,44 +1,54 @@
-// Gated linear recurrence on the tensor cores: bf16 inputs, D = 128.
+// Gated linear recurrence on the tensor cores: bf16 inputs, D = 32, 64 or 128.
 //
 // The same passes, with the same operands x, y, z, weights and dbeta terms, as on
 // CUDA cores (linear_simt.cuh, which has the formulas); here a chunk is 128
 // tokens and every product is tcgen05 with fp32 accumulators in TMEM:
 //   P  [128 t][128 i] = X Y^T                      scores (both operands as loaded)
 //   OI [128 t][64 z]  = (w . P) Z                  inside the chunk; w . P bf16 in TMEM
-//   OS [128 t][64 z]  = X (S_hi + S_lo)            against the state before the chunk
+//   OS [128 t][64 z]  = X (S_hi + S_lo (+ S_3))    against the state before the chunk
 //   DS [128 y][64 z]  = Y^T (u Z)_hi,mid,lo        the chunk's increment
 //   S' = b S + DS                                  fp32, in registers for the whole sequence
-// A CTA owns 64 of z's 128 columns for one head and one segment (a whole sequence
-// where the heads alone fill the SMs), so that 64 heads make 128 CTAs for 148 SMs
-// and the state takes 16 registers a thread; the two CTAs of a head read the same
-// x and y, the second time from L2.
+// A CTA owns 64 of z's columns for one head and one segment (a whole sequence where
+// the heads alone fill the SMs); with D = 128 the two CTAs of a head read the same x
+// and y, the second time from L2.  Heads of 32 and 64 columns take the same tiles:
+// their boxes' missing columns read as zeros, the K steps and column halves beyond D
+// are not issued.  (On CUDA cores B8 H8 T2048 D64 took 345 us, here 46.)
 //
 // Roundings.  bf16 inputs enter the products exactly.  The increments' weighted
 // rows u z are split into three bf16 parts (24 bits: the state is an fp32 one, and
-// final_state is an output), the state read by OS into two (16 bits, relative
-// 2^-17), the weighted scores are rounded once to bf16 (as
-// large as the output's own rounding and independent of it).
+// final_state is an output).  The state read by OS is split into two (16 bits,
+// relative 2^-17: the output is rounded to 8 bits), or three where its product also
+// forms a term of dbeta, an fp32 output (dbeta and dgate were 1e-6 to 3e-6 off with
+// two parts, 2e-7 to 8e-7 with three).  The weighted scores are rounded once to bf16
+// (as large as the output's own rounding and independent of it).
 //
-// Warps 0-15 (arithmetic): thread (quarter q, lane, group cg) owns TMEM lane
-// 32 q + lane and a 16- or 32-column group cg.  Warp 16 issues TMA loads and MMAs;
-// warp 17 forms each chunk's decay tables one chunk ahead.
+// Roles (640 threads, one CTA an SM).  What follows at -> is a barrier and who waits:
+//   warp 18      loads x (one stage), y, z (two), decay tables (four) -> 17, 8-15, 0-7
+//   warp 17      x from shared memory to TMEM, P -> 0-7;  OI -> 0-7
+//   warp 16      OS -> 0-7, 17;  DS -> 8-15
+//   warps 0-7    P -> weighted scores in TMEM (thread: a token, 64 columns) -> 17;
+//                a OS + OI -> rows staged where z was -> 19
+//   warps 8-15   S as OS's operand -> 16;  parts of u z -> 16;  S' = b S + DS
+//   warp 19      rows out by TMA, z's stage free again -> 18
+// A barrier that some waiter could be two phases behind on has two copies.  Every wait
+// is bounded and gives up once another role has; the issuers and the loader then drain
+// what they have in flight, TMEM is freed and the device flag set.
 //
-// Decay weights.  exp(l_t - l_i) of a 32 x 32 block below the diagonal is the
-// product of two factors at most 1, ta_t (from the block row's edge to t) and
-// c_b,i (from i to that edge), both from differences in double: two vectors
-// instead of 1024 exponentials, no overflow however strong the decay.  Only
-// diagonal blocks evaluate exponentials, blocks beyond the diagonal are zero.
-//
-// Chunk n's steps, by role (-> barrier -> waiting role):
-//   math: S operand(n) -> MMA OS(n);  parts(n) -> MMA DS(n);  P(n) -> weights ->
-//         MMA OI(n);  S += DS(n);  OS, OI -> rows staged in shared memory -> TMA store
-//   issuer: between them loads x(n + 1) once P(n) and OS(n) are done, y and z of
-//         n + 2 once chunk n is, and issues P(n + 1) while OI(n) runs
-// Shared memory's bandwidth is what the products compete for with the warps, so the
-// parts of one operand are columns of one product (N = 192 for DS, 128 for OS: the
-// other operand is read once) and their sums are taken in registers; rows leave
-// through shared memory and TMA, since a thread's 32 bytes of a row, stored from
-// registers, cost a pass of the memory pipe per row.
+// What decided the layout (cycles a chunk, B8 H8 T2048 D128, 1.9 GHz).
+// - An MMA with both operands in shared memory and N = 128 leaves the warps no bandwidth
+//   there: P took 1222.  X as a TMEM operand (copied once, used by P and OS) frees it.
+// - Parts of one operand are columns of one product (N = 192 for DS: y is read once)
+//   and their sums are taken in registers.
+// - Issuing an MMA costs 33 from a converged warp under elect_one, 70 to 200 otherwise,
+//   hence a warp per queue and operand addresses that are constants.
+// - Rows leave through shared memory and TMA: a thread's 32 bytes of a row, stored from
+//   registers, are a pass of the memory pipe per row.
+// - Loops stay rolled: unrolled, the roles' code no longer fits the instruction caches
+//   together (no variant of it was faster).
+// What bounds it: the outputs' warps, in sequence the scores (1400), OI (700), the rows
+// (1000) and the hand-offs between (a satisfied wait is 130), 4100 a chunk against 2600
+// of tensor work; loads, stores and hand-offs alone are 29 us of the kernel's 47, the
+// bytes 21.5 at the copy rate.  (Tensor pipe 46 % active, issue slots 49 %.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -54,7 +64,7 @@ namespace gka {
 constexpr int kLtC = 128;                       // tokens per chunk
 constexpr int kLtZN = 64;                       // columns of z a CTA owns
 constexpr int kLtGroup = 256;                   // threads of an arithmetic group (two)
-constexpr int kLtThreads = 2 * kLtGroup + 128;  // + two issuers, the decay warp, the loader
+constexpr int kLtThreads = 2 * kLtGroup + 128;  // + two issuers, the loader, the rows' store
 constexpr int kLtTabs = 4;                      // stages of decay tables
 constexpr int kLtTabF = 8 * kLtC + 4;           // floats of a table
 constexpr int kLtDots = 2, kLtFdots = 8;        // planes of dot and fdot partials per column split
@@ -79,8 +89,8 @@ struct LtSmem {
 };
 
 struct LinTcPass {
-    // [B*H][T][128] bf16, boxes of 64 columns x 128 tokens of a head, 128B swizzle; tokens
-    // past T read as zeros and are not written
+    // [B*H][T][D] bf16, boxes of 64 columns x 128 tokens of a head, 128B swizzle; tokens
+    // past T and columns past D read as zeros and are not written
     CUtensorMap x, y, z, out;
     LinPass p;
     const float *tab;             // decay tables of the pass's direction
@@ -203,7 +213,8 @@ __device__ __forceinline__ float2 f2_rest(float2 y, uint32_t w) {
 }
 // Decay tables of every chunk, a warp each, into tab [B*H][N][kLtTabF] (LtSmem lists a table's
 // parts).  A kernel of its own: formed by a warp of the passes, chunk by chunk, they took 4500
-// to 6300 cycles a chunk (600 instructions that no cache held) and bounded those.
+// to 6300 cycles a chunk (600 instructions that no cache held) and bounded those; this one is
+// 4.5 us (B8 H8 T2048; 4 KB a chunk, latency), most of it under the set-up of the pass.
 // grid ceil(B*H*N / 8), block 256.  Lane l holds tokens 32 j + l.
 template <bool REV>
 __global__ void __launch_bounds__(256)
@@ -283,7 +294,11 @@ __device__ __forceinline__ void lt_parts(const uint8_t *z, uint8_t *dst, float u
     *reinterpret_cast<uint4 *>(dst + 2 * LtSmem::HALF) = make_uint4(c[0], c[1], c[2], c[3]);
 }
 
-// grid (2 * passes, B*H, S), block kLtThreads.
+// GRAD: the passes of the backward, which also keep the states, form dbeta's dots and, for
+// those, take the state in three parts.  The third lies where the third part of u z goes next,
+// which therefore waits for OS: dq's pass 60 -> 64 us, and dv's with dk's 105 -> 130 (their 256
+// CTAs are two waves on 148 SMs).  Over x's stage instead it held back the next x: 73 and 136.
+// grid (lt_splits(D) * passes, B*H, S), block kLtThreads.
 template <bool REV, bool GRAD>
 __global__ void __launch_bounds__(kLtThreads, 1)
 k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_flag) {
@@ -797,7 +812,9 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
 //   u_i = g_i prod_{m > i} beta_m   (backward: c prod_{m <= i} beta_m)
 // over the segment (a chunk's u times the decay of the chunks between it and that end): one
 // product per chunk into the same accumulators, with nothing of the state in between.  Warps
-// 0-15 form the weighted rows (as in k_linear_tc), warp 16 issues, warp 18 loads.
+// 0-15 form the weighted rows (as in k_linear_tc), warp 16 issues, warp 18 loads.  B1 H8
+// T131072 D128: 145 us for 538 MB (58 % of the copy rate); the weighted rows' three parts, 48 KB
+// of shared memory written a chunk, set the pace.
 struct LaSmem {
     static constexpr uint32_t Y = 0;                             // 2 stages
     static constexpr uint32_t Z = Y + 2 * LtSmem::TILE;          // 2 stages
@@ -809,7 +826,7 @@ struct LaSmem {
     static constexpr size_t bytes = END + 1024;
 };
 
-// grid (2, B*H, S), block kLtThreads.
+// grid (lt_splits(D), B*H, S), block kLtThreads.
 template <bool REV>
 __global__ void __launch_bounds__(kLtThreads, 1)
 k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_flag) {
@@ -953,8 +970,9 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
 // The two score matrices are tcgen05 products of bf16 inputs (exact operands);
 // weights, pairs and sums are fp32, with the cumulative logs as a sum of two
 // floats so that differences after a reset keep fp32 precision.  q and k, then
-// dout and v, go through the same 64 KB, which leaves room for two CTAs an SM:
-// one loads while the other computes.
+// dout and v, go through the same 64 KB, which leaves room for two CTAs an SM (TMEM's
+// limit too): one loads while the other computes.  B8 H8 T2048 D128: 38 us for 140 MB,
+// bounded by a CTA's sequence of load, product and column sums (issue slots 33 %).
 // grid (N, B*H), block 256: thread (quarter, lane, half) has row s = 32 quarter +
 // lane and the 32-column blocks 2 half, 2 half + 1.
 // ---------------------------------------------------------------------------

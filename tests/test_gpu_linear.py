@@ -83,6 +83,29 @@ def test_few_and_many_heads(B, H, T, dtype):
         check_backward(a, kw, gen, True)
 
 
+@pytest.mark.parametrize("D,B,H,T", [(64, 1, 1, 5000), (32, 1, 2, 1500), (32, 3, 50, 700), (64, 2, 200, 260)])
+def test_narrow_heads_in_segments_and_waves(D, B, H, T):
+    """bf16 heads of fewer columns than a tensor-core tile has."""
+    a, kw, gen = linear_inputs(B, H, T, D, torch.bfloat16, 8, gate=True, state=True, resets=(T // 3, T - 1))
+    check_forward(a, kw)
+    if T < 2000:
+        check_backward(a, kw, gen, True)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_fp32_gradients_of_bf16_inputs_read_all_of_the_state(D):
+    """dgate of one token is v^T R k with R = dfinal_state: a state whose third bf16 part is as large
+    as it can be (1 + 2^-9 + 2^-16 1.49, where two parts are 2^-17 off) and rows of one sign.
+    24 accumulations of the tensor cores, each off by at most 2^-23 of the sum."""
+    gen = torch.Generator().manual_seed(21)
+    q, k, v, do = ((torch.rand(2, 3, 1, D, generator=gen) + 0.5).bfloat16().cuda() for _ in range(4))
+    beta, gate = torch.ones(2, 3, 1, device="cuda"), torch.full((2, 3, 1), 0.5, device="cuda")
+    R = torch.full((2, 3, D, D), 1 + 2.0 ** -9 + 1.49 * 2.0 ** -16, device="cuda")
+    got = gka.gka_linear_backward(q, k, v, beta, do, gate=gate, scale=0.0, dfinal_state=R)
+    want = torch.einsum("bhti,bhij,bhtj->bht", v.double(), R.double(), k.double())
+    assert rel(got["dgate"], want) <= 24 * 2.0 ** -23
+
+
 @pytest.mark.parametrize("T", [200, 3000])
 def test_backward_long_one_head(T):
     a, kw, gen = linear_inputs(1, 2, T, 128, torch.bfloat16, 11, gate=True, state=True,
