@@ -183,8 +183,8 @@ __host__ __device__ constexpr int lin_per_sm(int D) { return D > 64 ? 2 : D > 32
 // a row of S or z is one pass of shared memory for the warp and serves R (SR) x 4 products of
 // each thread.  Chunk n + 1's tiles and decays come from memory, and its decay table is formed,
 // while chunk n is worked on.  What bounds it: the fp32 pipe and shared memory, 5000 cycles each
-// of some 8000 a chunk (D = 128); B2 H1 T88769 D128 590 us with the aggregates (32 columns a
-// CTA, 2 x 2 and 1 x 4 tiles, tables between the chunks: 1276), against 194 of FMAs at 60 TFLOP/s.
+// of some 8000 a chunk (D = 128); B2 H1 T88769 D128 730 us with the aggregates (32 columns a
+// CTA, 1 x 4 and 4 x 4 tiles, tables between the chunks: 1276), against 194 of FMAs at 60 TFLOP/s.
 // Where few chunks are left a launch (T of some hundreds), the launches' latency.
 template <int D, bool REV, bool OUT>
 __global__ void __launch_bounds__(kLinThreads, lin_per_sm(D))
@@ -453,7 +453,9 @@ k_linear_pass(const __grid_constant__ LinPasses args) {
 // linear, S(end) = dec S(start) + A, so with few heads the sequences are cut into S
 // segments whose aggregates A (states from zero) are formed in parallel, and this
 // kernel, element-wise and in order, leaves in each entry the state in force where
-// the segment begins (rev: behind its end).  init nullable [B*H][D2].
+// the segment begins (rev: behind its end).  init nullable [B*H][D2].  Latency bounds it (a
+// chain over S): 32 segments' loads at a time, not 8, took the fp32 gradient of B1 H1 T16000
+// D128 from 381 to 313 us.
 // grid (D2 / 1024, B*H), block 256.
 __global__ void __launch_bounds__(256)
 k_linear_scan(float *__restrict__ agg, const float *__restrict__ segdec,
@@ -465,7 +467,7 @@ k_linear_scan(float *__restrict__ agg, const float *__restrict__ segdec,
     float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
     if (init) run = *reinterpret_cast<const float4 *>(init + (size_t)bh * D2 + e);
     float *base = agg + (size_t)bh * S * D2 + e;
-    constexpr int kB = 8;   // loads of eight segments go out before the first store
+    constexpr int kB = 32;   // loads of so many segments go out before the first store
     for (int s0 = 0; s0 < S; s0 += kB) {
         float4 av[kB];
         float bv[kB];
