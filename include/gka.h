@@ -304,7 +304,7 @@ int gka_solver_study(const void *q, const void *k, const float *beta, const floa
  *   o           [B, H, T, D] in `dt` (written; no input's memory)
  *   initial_state, final_state   nullable fp32 [B, H, D, D] (M maps keys to
  *               values); final_state (written) is the state after the last token
- *               and may be initial_state itself; T = 0 copies the one to the other
+ *               and may be initial_state itself, else no input's memory; T = 0 copies the one to the other
  *   workspace   at least gka_linear_forward_workspace_bytes(), 256-byte aligned
  *               (0 bytes for some sizes: then NULL will do)
  * B*H is at most 65535.  The state is carried in fp32.  With bf16 inputs the products
@@ -320,7 +320,8 @@ int gka_linear_forward(const void *q, const void *k, const void *v, const float 
 
 /*
  * One token of the recurrence, in place on the fp32 state [B, H, D, D]:
- *   M <- beta M + g v k^T,  o = c M q.   q, k, v, o [B, H, D]; beta, gate [B, H].
+ *   M <- beta M + g v k^T,  o = c M q.   q, k, v, o [B, H, D]; beta, gate [B, H];
+ *   state and o share no memory with each other or an input.
  */
 int gka_linear_decode_step(float *state, const void *q, const void *k, const void *v,
                            const float *beta, const float *gate, void *o, int B, int H, int D,

@@ -201,8 +201,10 @@ k_linear_pass(const __grid_constant__ LinPasses args) {
     float *wz = zs + C * ZN;                                  // [C][ZN] u_i z_i
     float *St = wz + C * ZN;                                  // [D][ZN]
     float *Ps = St + D * ZN;                                  // [C][C + 1]
-    griddep_launch_dependents();
+    // in this order: the pair terms' kernel, further on in the call, reads the call's inputs
+    // before its own wait, and may only exist once what wrote them is done
     griddep_wait();
+    griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const LinPass &p = args.pass[blockIdx.x / (D / ZN)];
     const int zsp = blockIdx.x % (D / ZN), z0 = zsp * ZN, bh = blockIdx.y, seg = blockIdx.z;

@@ -367,9 +367,8 @@ def gka_backward(q, k, v, beta, dout, a: float, r: int, chunk: int = 32, *, gate
 # ---------------------------------------------------------------------------
 # The gated linear recurrence and the block's row operations.  These calls run on
 # the device that holds their tensors, whichever is current, on `stream` or that
-# device's current stream.  Outputs and workspaces that a call allocates belong to
-# the stream that is current at the call, as torch's allocator has it: with a
-# `stream` of one's own, pass them, or call under `torch.cuda.stream(stream)`.
+# device's current stream, to which outputs and workspaces that a call allocates
+# belong too, as torch's allocator has it.
 # ---------------------------------------------------------------------------
 def _device_of(first, *rest):
     """The one CUDA device of the tensors given (None: not given)."""
@@ -402,14 +401,17 @@ def _apart(*outs):
             raise ValueError("outputs must not share memory with each other or with inputs")
 
 
-def _invoke(fn, dev, stream, *args):
-    """Calls a C entry point whose last argument is the stream, on device ``dev``."""
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    elif stream.device != dev:
+def _under(stream, fn, *args, **kw):
+    """The call with ``stream`` current: what it allocates is that stream's too."""
+    if stream.device != args[0].device:
         raise ValueError("stream must belong to the tensors' device")
-    else:
-        raw = stream.cuda_stream
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
+
+
+def _invoke(fn, dev, *args):
+    """Calls a C entry point whose last argument is the stream, on device ``dev``."""
+    raw = torch._C._cuda_getCurrentRawStream(dev.index)
     call = getattr(_lib(), fn)
     if torch._C._cuda_getDevice() == dev.index:
         rc = call(*args, raw)
@@ -464,6 +466,10 @@ def gka_linear_forward(q, k, v, beta, *, gate=None, scale=1.0, initial_state=Non
     (see include/gka.h).  q, k, v: [B, H, T, D] fp32 or bf16 CUDA tensors, any T; beta
     (and the optional gate): [B, H, T] fp32; initial_state, final_state (written; may be
     initial_state): fp32 [B, H, D, D].  Returns o (shape and dtype of v)."""
+    if stream is not None:
+        return _under(stream, gka_linear_forward, q, k, v, beta, gate=gate, scale=scale,
+                      initial_state=initial_state, final_state=final_state, o=o,
+                      workspace=workspace)
     dev = _device_of(q, k, v, beta, gate, initial_state, final_state, o, workspace)
     _dense(q, k, v, beta, gate, initial_state, final_state, o)
     B, H, T, D = q.shape
@@ -474,12 +480,14 @@ def gka_linear_forward(q, k, v, beta, *, gate=None, scale=1.0, initial_state=Non
         o = torch.empty_like(v)
     else:
         _need("o", o, q.shape, q.dtype)
-        _apart(o, final_state)
-        for t in (q, k, v, beta, gate, initial_state, workspace):
+        for t in (q, k, v, beta, gate, initial_state, final_state, workspace):
             _apart(o, t)
+    if final_state is not None and initial_state is not None and \
+            0 < abs(final_state.data_ptr() - initial_state.data_ptr()) < _nbytes(final_state):
+        raise ValueError("final_state must be initial_state itself or share none of its memory")
     n = _query("gka_linear_forward_workspace_bytes", B, H, T, D, dt)
     workspace = _scratch(n, workspace, dev)
-    _invoke("gka_linear_forward", dev, stream, _p(q), _p(k), _p(v), _p(beta), _p(gate), _p(o), B, H,
+    _invoke("gka_linear_forward", dev, _p(q), _p(k), _p(v), _p(beta), _p(gate), _p(o), B, H,
             T, D, dt, scale, _p(initial_state), _p(final_state), _p(workspace), _nbytes(workspace))
     return o
 
@@ -487,6 +495,9 @@ def gka_linear_forward(q, k, v, beta, *, gate=None, scale=1.0, initial_state=Non
 def gka_linear_decode_step(state, q, k, v, beta, *, gate=None, scale=1.0, o=None, stream=None):
     """One token of the gated linear recurrence, in place on state [B, H, D, D] fp32;
     q, k, v: [B, H, D]; beta (and the optional gate): [B, H] fp32.  Returns o [B, H, D]."""
+    if stream is not None:
+        return _under(stream, gka_linear_decode_step, state, q, k, v, beta, gate=gate,
+                      scale=scale, o=o)
     dev = _device_of(state, q, k, v, beta, gate, o)
     _dense(state, q, k, v, beta, gate, o)
     B, H, D = q.shape
@@ -499,7 +510,7 @@ def gka_linear_decode_step(state, q, k, v, beta, *, gate=None, scale=1.0, o=None
         _need("o", o, q.shape, q.dtype)
         for t in (state, q, k, v, beta, gate):
             _apart(o, t)
-    _invoke("gka_linear_decode_step", dev, stream, _p(state), _p(q), _p(k), _p(v), _p(beta),
+    _invoke("gka_linear_decode_step", dev, _p(state), _p(q), _p(k), _p(v), _p(beta),
             _p(gate), _p(o), B, H, D, dt, scale)
     return o
 
@@ -510,6 +521,10 @@ def gka_linear_backward(q, k, v, beta, dout, *, gate=None, scale=1.0, initial_st
     inputs' dtype; dfinal_state: optional gradient of the final state, fp32 [B, H, D, D].
     Returns a dict with dq, dk, dv (dtype of q), dbeta, with a gate dgate (fp32), and with
     an initial_state dstate (its gradient, fp32)."""
+    if stream is not None:
+        return _under(stream, gka_linear_backward, q, k, v, beta, dout, gate=gate,
+                      scale=scale, initial_state=initial_state, dfinal_state=dfinal_state,
+                      workspace=workspace)
     dev = _device_of(q, k, v, beta, gate, dout, initial_state, dfinal_state, workspace)
     _dense(q, k, v, beta, gate, dout, initial_state, dfinal_state)
     B, H, T, D = q.shape
@@ -525,7 +540,7 @@ def gka_linear_backward(q, k, v, beta, dout, *, gate=None, scale=1.0, initial_st
         out["dstate"] = torch.empty_like(initial_state)
     n = _query("gka_linear_backward_workspace_bytes", B, H, T, D, dt)
     workspace = _scratch(n, workspace, dev)
-    _invoke("gka_linear_backward", dev, stream, _p(q), _p(k), _p(v), _p(beta), _p(gate), _p(dout),
+    _invoke("gka_linear_backward", dev, _p(q), _p(k), _p(v), _p(beta), _p(gate), _p(dout),
             _p(initial_state), _p(dfinal_state), _p(out["dq"]), _p(out["dk"]), _p(out["dv"]),
             _p(out["dbeta"]), _p(out.get("dgate")), _p(out.get("dstate")), B, H, T, D, dt, scale,
             _p(workspace), _nbytes(workspace))
@@ -573,6 +588,9 @@ def gka_block_in(q, k, v, beta_logit, *, gate_logit=None, beta_bias=None, gate_b
     dtype; beta_bias, gate_bias: [H] fp32; lengths: [B] int32, tokens past it are padding.
     Returns (q, k, v [B, H, T, D], beta [B, H, T] fp32, gate or None): the inputs of
     gka_forward_gated and gka_linear_forward."""
+    if stream is not None:
+        return _under(stream, gka_block_in, q, k, v, beta_logit, gate_logit=gate_logit,
+                      beta_bias=beta_bias, gate_bias=gate_bias, lengths=lengths, eps=eps)
     dev = _device_of(q, k, v, beta_logit, gate_logit, beta_bias, gate_bias, lengths)
     B, T, H, Hk, D, dt, (sq, sk, sb, sg) = _block_in_args(q, k, beta_logit, gate_logit, beta_bias,
                                                           gate_bias, lengths)
@@ -581,7 +599,7 @@ def gka_block_in(q, k, v, beta_logit, *, gate_logit=None, beta_bias=None, gate_b
     ko, vo = torch.empty_like(qo), torch.empty_like(qo)
     beta = torch.empty((B, H, T), device=dev, dtype=torch.float32)
     gate = torch.empty_like(beta) if gate_logit is not None or lengths is not None else None
-    _invoke("gka_block_in_forward", dev, stream, sq, sk, sv, sb, sg, _p(beta_bias), _p(gate_bias),
+    _invoke("gka_block_in_forward", dev, sq, sk, sv, sb, sg, _p(beta_bias), _p(gate_bias),
             _p(lengths), _p(qo), _p(ko), _p(vo), _p(beta), _p(gate), B, T, H, Hk, D, dt, eps)
     return qo, ko, vo, beta, gate
 
@@ -593,6 +611,10 @@ def gka_block_in_backward(q, k, beta_logit, dq, dk, dv, dbeta, *, gate_logit=Non
     inputs' dtype, dbeta (and dgate exactly with gate_logit) [B, H, T] fp32.  Returns a dict
     with dq [B, T, H, D], dk, dv [B, T, Hk, D], dbeta_logit (dgate_logit) [B, T, H], and for
     each bias given dbeta_bias (dgate_bias) [H] fp32."""
+    if stream is not None:
+        return _under(stream, gka_block_in_backward, q, k, beta_logit, dq, dk, dv, dbeta,
+                      gate_logit=gate_logit, dgate=dgate, beta_bias=beta_bias,
+                      gate_bias=gate_bias, lengths=lengths, eps=eps, workspace=workspace)
     dev = _device_of(q, k, beta_logit, gate_logit, dq, dk, dv, dbeta, dgate, beta_bias, gate_bias,
                        lengths, workspace)
     B, T, H, Hk, D, dt, (sq, sk, sb, sg) = _block_in_args(q, k, beta_logit, gate_logit, beta_bias,
@@ -615,7 +637,7 @@ def gka_block_in_backward(q, k, beta_logit, dq, dk, dv, dbeta, *, gate_logit=Non
             out[n] = torch.empty_like(t)
     n = _query("gka_block_in_backward_workspace_bytes", B, T, H, Hk, D, dt)
     workspace = _scratch(n, workspace, dev)
-    _invoke("gka_block_in_backward", dev, stream, sq, sk, sb, sg, _p(beta_bias), _p(gate_bias),
+    _invoke("gka_block_in_backward", dev, sq, sk, sb, sg, _p(beta_bias), _p(gate_bias),
             _p(lengths), _p(dq), _p(dk), _p(dv), _p(dbeta), _p(dgate), _p(out["dq"]), _p(out["dk"]),
             _p(out["dv"]), _p(out["dbeta_logit"]), _p(out.get("dgate_logit")),
             _p(out.get("dbeta_bias")), _p(out.get("dgate_bias")), B, T, H, Hk, D, dt, eps,
@@ -639,6 +661,8 @@ def gka_block_out(o, w, *, z=None, v=None, skip=None, eps=1e-6, y=None, stream=N
     """After the layer (see include/gka.h): y = rmsnorm(o + skip_h v) w silu(z), token-major.
     o (and the layer's v): [B, H, T, D] fp32 or bf16; w: [D] fp32; skip: [H] fp32, with v;
     z: [B, T, H, D] at any strides with contiguous rows.  Returns y [B, T, H, D]."""
+    if stream is not None:
+        return _under(stream, gka_block_out, o, w, z=z, v=v, skip=skip, eps=eps, y=y)
     dev = _device_of(o, w, z, v, skip, y)
     B, H, T, D, dt, sz = _block_out_args(o, w, z, v, skip)
     if y is None:
@@ -648,7 +672,7 @@ def gka_block_out(o, w, *, z=None, v=None, skip=None, eps=1e-6, y=None, stream=N
         _need("y", y, (B, T, H, D), o.dtype)
         for t in (o, w, v, skip):
             _apart(y, t)
-    _invoke("gka_block_out_forward", dev, stream, _p(o), _p(v), sz, _p(w), _p(skip), _p(y), B, T, H,
+    _invoke("gka_block_out_forward", dev, _p(o), _p(v), sz, _p(w), _p(skip), _p(y), B, T, H,
             D, dt, eps)
     return y
 
@@ -657,6 +681,9 @@ def gka_block_out_backward(o, w, dy, *, z=None, v=None, skip=None, eps=1e-6, wor
                            stream=None):
     """Gradients of gka_block_out from dy [B, T, H, D].  Returns a dict with do [B, H, T, D],
     dw [D] fp32; with z: dz [B, T, H, D]; with v and skip: dv [B, H, T, D], dskip [H] fp32."""
+    if stream is not None:
+        return _under(stream, gka_block_out_backward, o, w, dy, z=z, v=v, skip=skip,
+                      eps=eps, workspace=workspace)
     dev = _device_of(o, w, dy, z, v, skip, workspace)
     B, H, T, D, dt, sz = _block_out_args(o, w, z, v, skip)
     _dense(dy)
@@ -668,7 +695,7 @@ def gka_block_out_backward(o, w, dy, *, z=None, v=None, skip=None, eps=1e-6, wor
         out["dv"], out["dskip"] = torch.empty_like(v), torch.empty_like(skip)
     n = _query("gka_block_out_backward_workspace_bytes", B, T, H, D, dt)
     workspace = _scratch(n, workspace, dev)
-    _invoke("gka_block_out_backward", dev, stream, _p(o), _p(v), sz, _p(w), _p(skip), _p(dy),
+    _invoke("gka_block_out_backward", dev, _p(o), _p(v), sz, _p(w), _p(skip), _p(dy),
             _p(out["do"]), _p(out.get("dv")), _p(out.get("dz")), _p(out["dw"]), _p(out.get("dskip")),
             B, T, H, D, dt, eps, _p(workspace), _nbytes(workspace))
     return out

@@ -315,6 +315,22 @@ def test_offsets_past_two_to_the_31():
         assert rel(last[:, h], l1[:, 0]) <= TOL32
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [40, 900])
+def test_gradients_of_a_result_that_is_still_being_written(dtype, T):
+    """dout is the output of the call just before: no kernel of the gradients may read it early."""
+    a, kw, _ = linear_inputs(1, 2, T, 64, dtype, 31)
+    a = list(a.values())
+    for _ in range(20):
+        o = torch.empty_like(a[0]).fill_(float("nan"))
+        torch.cuda.synchronize()
+        gka.gka_linear_forward(*a, scale=kw["scale"], o=o)
+        got = gka.gka_linear_backward(*a, o, scale=kw["scale"])
+        torch.cuda.synchronize()
+        want = gka.gka_linear_backward(*a, o, scale=kw["scale"])
+        assert all(torch.equal(got[n], want[n]) for n in want)
+
+
 def test_two_streams_at_once():
     """Independent calls in flight together, each with its own workspace."""
     sets = [linear_inputs(1, 3 + 40 * (i % 2), 600 + i, 128, torch.bfloat16, 20 + i, gate=True, state=True)
@@ -331,6 +347,23 @@ def test_two_streams_at_once():
     for ((o, l), g), ((ro, rl), rg) in zip(got, want):
         assert torch.equal(o, ro) and torch.equal(l, rl)
         assert all(torch.equal(g[n], rg[n]) for n in rg)
+
+
+def test_stream_argument():
+    """With `stream` given, what the call allocates is that stream's: a workspace that is freed while
+    the call runs goes to no other stream's work."""
+    a, kw, _ = linear_inputs(2, 4, 700, 128, torch.bfloat16, 41)
+    a = list(a.values())
+    want = gka.gka_linear_backward(*a, a[2], scale=kw["scale"])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = [gka.gka_linear_backward(*a, a[2], scale=kw["scale"], stream=s) for _ in range(2)]
+    n = gka.linear_workspace_bytes(2, 4, 700, 128, backward=True)
+    for _ in range(4):   # the freed workspace's size, written on the current stream meanwhile
+        torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(g[m], want[m]) for m in want)
 
 
 def test_nan_decay_shows():
@@ -371,3 +404,10 @@ def test_refusals():
     x = {n: y[:, :, 0].contiguous() for n, y in a.items()}
     with pytest.raises(ValueError):
         gka.gka_linear_decode_step(kw["state"], **x, o=x["v"])
+
+
+def test_states_that_overlap_are_refused():
+    a, kw, _ = linear_inputs(2, 2, 9, 32, torch.float32, 42)
+    both = torch.zeros(3, 2, 32, 32, device="cuda")
+    with pytest.raises(ValueError):
+        gka.gka_linear_forward(*a.values(), initial_state=both[:2], final_state=both[1:])
