@@ -710,16 +710,14 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         const bool owns = row < D && z0 < D;   // else: nothing of the state in memory
         float st[32];
         // a state in memory: [y][z], or [z][y] (then lanes are neighbours)
-        auto at = [&](size_t base, int j) {
-            return base + (p.zy ? (size_t)(z0 + j) * D + row : (size_t)row * D + z0 + j);
-        };
+        const int first = p.zy ? z0 * D + row : row * D + z0, step = p.zy ? D : 1;
 #pragma unroll
         for (int j = 0; j < 32; ++j) st[j] = 0.f;
         griddep_wait();
         if (p.start && owns) {
-            const size_t base = ((size_t)bh * p.S + seg) * D * D;
+            const float *src = p.start + ((size_t)bh * p.S + seg) * D * D + first;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) st[j] = p.start[at(base, j)];
+            for (int j = 0; j < 32; ++j, src += step) st[j] = *src;
         }
         bool ok = true;
         for (int it = 0; it < NL; ++it) {
@@ -759,14 +757,14 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             if (GRAD && p.states && owns) {
                 float *dst = p.states + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) dst[j * D] = st[j];
+                for (int j = 0; j < 32; ++j, dst += D) *dst = st[j];
             }
             if (GRAD && p.states_in) {
                 float f = 0.f;
                 if (owns) {
                     const float *src = p.states_in + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) f = fmaf(st[j], __ldcs(src + j * D), f);
+                    for (int j = 0; j < 32; ++j, src += D) f = fmaf(st[j], __ldcs(src), f);
                 }
                 f = warp_sum(f);
                 if (lane == 0) p.fdot[((size_t)(zh * 8 + warp - 8) * p.BH + bh) * p.N + n] = b * f;
@@ -792,8 +790,9 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             arrive(b_tfree + 8 * ts);
         }
         if (ok && p.last && owns && seg == (REV ? 0 : p.S - 1)) {
+            float *dst = p.last + (size_t)bh * D * D + first;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) p.last[at((size_t)bh * D * D, j)] = st[j];
+            for (int j = 0; j < 32; ++j, dst += step) *dst = st[j];
         }
     }
     // every product and copy has completed (the arithmetic warps waited for the last
