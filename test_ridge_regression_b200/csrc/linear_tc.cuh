@@ -815,12 +815,13 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
 // T131072 D128: 145 us for 538 MB (58 % of the copy rate); the weighted rows' three parts, 48 KB
 // of shared memory written a chunk, set the pace.
 struct LaSmem {
-    static constexpr uint32_t Y = 0;                             // 2 stages
-    static constexpr uint32_t Z = Y + 2 * LtSmem::TILE;          // 2 stages
-    static constexpr uint32_t PARTS = Z + 2 * LtSmem::HALF;      // 2 x hi, mid, lo
-    static constexpr uint32_t U = PARTS + 6 * LtSmem::HALF;      // 2 x (u, b)
-    static constexpr uint32_t BARS = U + 2 * (4 * kLtC + 16);
-    static constexpr uint32_t TBASE = BARS + 8 * (8 + 2);
+    static constexpr int ST = 3;                                 // stages of loads
+    static constexpr uint32_t Y = 0;
+    static constexpr uint32_t Z = Y + ST * LtSmem::TILE;
+    static constexpr uint32_t PARTS = Z + ST * LtSmem::HALF;     // hi, mid, lo
+    static constexpr uint32_t U = PARTS + 3 * LtSmem::HALF;      // u, b
+    static constexpr uint32_t BARS = U + ST * (4 * kLtC + 16);
+    static constexpr uint32_t TBASE = BARS + 8 * (2 * ST + 2);
     static constexpr uint32_t END = TBASE + 16;
     static constexpr size_t bytes = END + 1024;
 };
@@ -830,11 +831,11 @@ template <bool REV>
 __global__ void __launch_bounds__(kLtThreads, 1)
 k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_flag) {
     using L = LaSmem;
-    constexpr int C = kLtC, PARTB = 3 * LtSmem::HALF;
+    constexpr int C = kLtC, ST = L::ST;
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smem_align1024(smraw);
     const uint32_t sb = smem_u32(sm), bars = sb + L::BARS;
-    const uint32_t b_yz = bars, b_parts = bars + 16, b_ds = bars + 32, b_fin = bars + 48;
+    const uint32_t b_yz = bars, b_ds = bars + 8 * ST, b_parts = b_ds + 8 * ST, b_fin = b_parts + 8;   // [ST], [ST]
     uint32_t *tbase = reinterpret_cast<uint32_t *>(sm + L::TBASE);
     const uint32_t abort = sb + L::TBASE + 4;
     float *s_u = reinterpret_cast<float *>(sm + L::U);
@@ -845,11 +846,11 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
     const int n0 = lin_seg(seg, p.S, p.N), n1 = lin_seg(seg + 1, p.S, p.N), NL = n1 - n0;
     auto chunk = [&](int it) { return REV ? n0 + it : n1 - 1 - it; };
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < ST; ++i) {
             lt_init(b_yz + 8 * i, 1);
-            lt_init(b_parts + 8 * i, 16);
             lt_init(b_ds + 8 * i, 1);
         }
+        lt_init(b_parts, 16);
         lt_init(b_fin, 1);
         asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(0u) : "memory");
         fence_mbar_init();
@@ -863,8 +864,8 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
     tc::fence_after_sync();
     const uint32_t tmem = *tbase;
     auto wait = [&](uint32_t bar, uint32_t parity) { return lt_wait_warp(bar, parity, abort); };
-    // phase of chunk it on a barrier of two: (it / 2) & 1; done(it): its product has completed
-    auto done = [&](int it) { return wait(b_ds + 8 * (it & 1), (it >> 1) & 1); };
+    // phase of chunk it on a barrier of ST: (it / ST) & 1; done(it): its product has completed
+    auto done = [&](int it) { return wait(b_ds + 8 * (it % ST), (it / ST) & 1); };
     bool ok = true;
 
     if (warp == 16) {
@@ -873,15 +874,15 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
                        d_u = tc::sdesc(sb + L::PARTS, LtSmem::HALF, 1024);
 #pragma unroll 1
         for (int it = 0; it < NL; ++it) {
-            const int st = it & 1;
-            ok = wait(b_parts + 8 * st, (it >> 1) & 1);
+            const int st = it % ST;
+            ok = wait(b_parts, it & 1);
             if (!ok) break;
             tc::fence_after_sync();
             if (elect_one()) {
-                const uint64_t y = d_y + st * (LtSmem::TILE / 16), u = d_u + st * (PARTB / 16);
+                const uint64_t y = d_y + st * (LtSmem::TILE / 16);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    tc::mma_f16(tmem, y + kk * 128, u + kk * 128, ID_D, (it | kk) != 0);
+                    tc::mma_f16(tmem, y + kk * 128, d_u + kk * 128, ID_D, (it | kk) != 0);
                 lt_commit(b_ds + 8 * st);
             }
         }
@@ -896,8 +897,8 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
             int loads = 0;
 #pragma unroll 1
             for (int it = 0; it < NL; ++it) {
-                const int st = it & 1, t0 = chunk(it) * C;
-                if (it >= 2) ok = lt_wait(b_ds + 8 * st, ((it >> 1) - 1) & 1, abort);
+                const int st = it % ST, t0 = chunk(it) * C;
+                if (it >= ST) ok = lt_wait(b_ds + 8 * st, (it / ST - 1) & 1, abort);
                 if (!ok) break;
                 lt_expect(b_yz + 8 * st, lt_tile_bytes(D) + LtSmem::HALF + 4 * kLtC + 16);
                 tma_load_3d(sm + L::Z + st * LtSmem::HALF, &A.z, zh * kLtZN, t0, bh, b_yz + 8 * st);
@@ -911,28 +912,28 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
                 ++loads;
             }
             if (!ok)
-                for (int i = 0; i < 2; ++i)
-                    if ((loads + 1 - i) / 2) lt_drain(b_yz + 8 * i, ((loads + 1 - i) / 2 - 1) & 1);
+                for (int i = 0; i < ST; ++i)
+                    if (loads > i) lt_drain(b_yz + 8 * i, ((loads - 1 - i) / ST) & 1);
         }
         __syncwarp();
     } else if (warp < 16) {
         float far = 1.f;   // decay of the chunks between this one and the segment's end
 #pragma unroll 1
         for (int it = 0; it < NL; ++it) {
-            const int st = it & 1;
+            const int st = it % ST;
             const float *u = s_u + st * (kLtC + 4);
-            ok = wait(b_yz + 8 * st, (it >> 1) & 1) && (it < 2 || done(it - 2));
+            ok = wait(b_yz + 8 * st, (it / ST) & 1) && (it < 1 || done(it - 1));
             if (!ok) break;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int item = tid + i * 512;   // row item / 8
-                lt_parts(sm + L::Z + st * LtSmem::HALF + item * 16, sm + L::PARTS + st * PARTB + item * 16,
+                lt_parts(sm + L::Z + st * LtSmem::HALF + item * 16, sm + L::PARTS + item * 16,
                          u[item >> 3] * far);
             }
             far *= u[kLtC];
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) lt_arrive(b_parts + 8 * st);
+            if (lane == 0) lt_arrive(b_parts);
         }
         if (ok) ok = done(NL - 1);
         if (ok && tid == 0 && zh == 0) p.segdec[(size_t)bh * p.S + seg] = far;
