@@ -45,10 +45,13 @@
 //   registers, are a pass of the memory pipe per row.
 // - Loops stay rolled: unrolled, the roles' code no longer fits the instruction caches
 //   together (no variant of it was faster).
-// What bounds it: the outputs' warps, in sequence the scores (1400), OI (700), the rows
-// (1000) and the hand-offs between (a satisfied wait is 130), 4100 a chunk against 2600
-// of tensor work; loads, stores and hand-offs alone are 29 us of the kernel's 47, the
-// bytes 21.5 at the copy rate.  (Tensor pipe 46 % active, issue slots 49 %.)
+// - Sixteen warps for the outputs (registers split by role) were 7 % slower.
+// What bounds it: the chain from chunk to chunk through the outputs' warps: the scores
+// (1400), OI (700), the rows (1000) and the hand-offs between (a satisfied wait is 130),
+// 4100 a chunk against 2600 of tensor work; loads, stores and hand-offs alone are 29 us of
+// the kernel's 46, the bytes 21.5 at the copy rate.  No unit is full: tensor pipe 47 %
+// active, issue slots 50 %, the warps' shared memory accesses 26 %, its banks 16 % reading
+// and 13 % writing.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -296,8 +299,8 @@ __device__ __forceinline__ void lt_parts(const uint8_t *z, uint8_t *dst, float u
 
 // GRAD: the passes of the backward, which also keep the states, form dbeta's dots and, for
 // those, take the state in three parts.  The third lies where the third part of u z goes next,
-// which therefore waits for OS: dq's pass 60 -> 64 us, and dv's with dk's 105 -> 130 (their 256
-// CTAs are two waves on 148 SMs).  Over x's stage instead it held back the next x: 73 and 136.
+// which therefore waits for OS.  B8 H8 T2048 D128: dq's pass 59 us, dv's and dk's 120 (256 CTAs,
+// two waves on 148 SMs).  Over x's stage instead it held back the next x: 14 and 6 % more.
 // grid (lt_splits(D) * passes, B*H, S), block kLtThreads.
 template <bool REV, bool GRAD>
 __global__ void __launch_bounds__(kLtThreads, 1)
@@ -812,8 +815,8 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
 // over the segment (a chunk's u times the decay of the chunks between it and that end): one
 // product per chunk into the same accumulators, with nothing of the state in between.  Warps
 // 0-15 form the weighted rows (as in k_linear_tc), warp 16 issues, warp 18 loads.  B1 H8
-// T131072 D128: 145 us for 538 MB (58 % of the copy rate); the weighted rows' three parts, 48 KB
-// of shared memory written a chunk, set the pace.
+// T131072 D128: 145 us for 538 MB (58 % of the copy rate); the parts (48 KB of shared
+// memory written a chunk) and the product follow one another, 2400 cycles a chunk.
 struct LaSmem {
     static constexpr int ST = 3;                                 // stages of loads
     static constexpr uint32_t Y = 0;
