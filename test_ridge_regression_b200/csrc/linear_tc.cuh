@@ -46,12 +46,14 @@
 // - Loops stay rolled: unrolled, the roles' code no longer fits the instruction caches
 //   together (no variant of it was faster).
 // - Sixteen warps for the outputs (registers split by role) were 7 % slower.
-// What bounds it: the chain from chunk to chunk through the outputs' warps: the scores
-// (1400), OI (700), the rows (1000) and the hand-offs between (a satisfied wait is 130),
-// 4100 a chunk against 2600 of tensor work; loads, stores and hand-offs alone are 29 us of
-// the kernel's 46, the bytes 21.5 at the copy rate.  No unit is full: tensor pipe 47 %
-// active, issue slots 50 %, the warps' shared memory accesses 26 %, its banks 16 % reading
-// and 13 % writing.
+// - Rows formed one chunk late, under the next chunk's OI and P: 6 % slower (two accumulators
+//   of OI and OS leave DS 64 columns, its parts one product each).
+// What bounds it: several chains from chunk to chunk of nearly one length, 4100 to 4500 against
+// 2600 of tensor work.  The outputs' warps: scores (1400), OI (700), rows (1000), hand-offs
+// (130 a satisfied wait); the state's: its operand, parts, DS, sum; loads, stores and hand-offs
+// alone: 29 us of the kernel's 46 (the bytes 21.5 at the copy rate).  No unit is full: tensor
+// pipe 47 % active, issue slots 50 %, the warps' shared memory accesses 26 %, its banks 16 %
+// reading and 13 % writing.
 #pragma once
 
 #include <cuda_bf16.h>
