@@ -372,13 +372,13 @@ def gka_backward(q, k, v, beta, dout, a: float, r: int, chunk: int = 32, *, gate
 # ---------------------------------------------------------------------------
 def _device_of(first, *rest):
     """The one CUDA device of the tensors given (None: not given)."""
-    dev = first.device
-    if dev.type != "cuda":
+    index = first.get_device()
+    if index < 0:
         raise ValueError("tensors must be CUDA tensors")
     for t in rest:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != index:
             raise ValueError("tensors must be on one CUDA device")
-    return dev
+    return first.device
 
 
 def _dense(*ts):
@@ -411,15 +411,21 @@ def _under(stream, fn, *args, **kw):
 
 def _invoke(fn, dev, *args):
     """Calls a C entry point whose last argument is the stream, on device ``dev``."""
-    raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    call = getattr(_lib(), fn)
-    if torch._C._cuda_getDevice() == dev.index:
+    index = dev.index
+    raw = torch._C._cuda_getCurrentRawStream(index)
+    call = _entry(fn)
+    if torch._C._cuda_getDevice() == index:
         rc = call(*args, raw)
     else:
         with torch.cuda.device(dev):
             rc = call(*args, raw)
     if rc != 0:
         raise GkaError(fn, rc)
+
+
+@functools.lru_cache(maxsize=None)
+def _entry(fn):
+    return getattr(_lib(), fn)
 
 
 @functools.lru_cache(maxsize=1024)
