@@ -4,7 +4,7 @@
 // CUDA cores (linear_simt.cuh, which has the formulas); here a chunk is 128
 // tokens and every product is tcgen05 with fp32 accumulators in TMEM:
 //   P  [128 t][128 i] = X Y^T                      scores (both operands as loaded)
-//   OI [128 t][64 z]  = (w . P) Z                  inside the chunk; w . P bf16 in TMEM
+//   OI [128 t][64 z]  = (w . P)_hi,lo Z            inside the chunk; w . P in TMEM
 //   OS [128 t][64 z]  = X (S_hi + S_lo (+ S_3))    against the state before the chunk
 //   DS [128 y][64 z]  = Y^T (u Z)_hi,mid,lo        the chunk's increment
 //   S' = b S + DS                                  fp32, in registers for the whole sequence
@@ -19,8 +19,10 @@
 // final_state is an output).  The state read by OS is split into two (16 bits,
 // relative 2^-17: the output is rounded to 8 bits), or three where its product also
 // forms a term of dbeta, an fp32 output (dbeta and dgate were 1e-6 to 3e-6 off with
-// two parts, 2e-7 to 8e-7 with three).  The weighted scores are rounded once to bf16
-// (as large as the output's own rounding and independent of it).
+// two parts, 2e-7 to 8e-7 with three).  The weighted scores enter in two parts: one
+// alone is a rounding as large as the output's own (2.3e-3 off against 1.7e-3, and up to
+// twice that in sequences of a few tokens, whose rows are few products), and two cost
+// 4 % (B8 H8 T2048 D128 kernel 49 -> 51 us, B1 H8 T131072 269 -> 281).
 //
 // Roles (640 threads, one CTA an SM).  What follows at -> is a barrier and who waits:
 //   warp 18      loads x (one stage), y, z (two), decay tables (four) -> 17, 8-15, 0-7
@@ -48,10 +50,10 @@
 // - Sixteen warps for the outputs (registers split by role) were 7 % slower.
 // - Rows formed one chunk late, under the next chunk's OI and P: 6 % slower (two accumulators
 //   of OI and OS leave DS 64 columns, its parts one product each).
-// What bounds it: several chains from chunk to chunk of nearly one length, 4100 to 4500 against
-// 2600 of tensor work.  The outputs' warps: scores (1400), OI (700), rows (1000), hand-offs
+// What bounds it: several chains from chunk to chunk of nearly one length, 4500 against 2900
+// of tensor work.  The outputs' warps: scores (1400), OI (700), rows (1000), hand-offs
 // (130 a satisfied wait); the state's: its operand, parts, DS, sum; loads, stores and hand-offs
-// alone: 29 us of the kernel's 46 (the bytes 21.5 at the copy rate).  No unit is full: tensor
+// alone: 29 us of the kernel's 49 (the bytes 21.5 at the copy rate).  No unit is full: tensor
 // pipe 47 % active, issue slots 50 %, the warps' shared memory accesses 26 %, its banks 16 %
 // reading and 13 % writing.
 #pragma once
@@ -301,7 +303,7 @@ __device__ __forceinline__ void lt_parts(const uint8_t *z, uint8_t *dst, float u
 
 // GRAD: the passes of the backward, which also keep the states, form dbeta's dots and, for
 // those, take the state in three parts.  The third lies where the third part of u z goes next,
-// which therefore waits for OS.  B8 H8 T2048 D128: dq's pass 59 us, dv's and dk's 120 (256 CTAs,
+// which therefore waits for OS.  B8 H8 T2048 D128: dq's pass 62 us, dv's and dk's 124 (256 CTAs,
 // two waves on 148 SMs).  Over x's stage instead it held back the next x: 14 and 6 % more.
 // grid (lt_splits(D) * passes, B*H, S), block kLtThreads.
 template <bool REV, bool GRAD>
@@ -377,7 +379,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     // those (x, y, z, beta) at once; the tables, the start states and the other direction's states
     // only after the wait (loader, state warps).
     griddep_launch_dependents();
-    // TMEM columns; the bf16 weighted scores of each half of the columns lie over its scores
+    // TMEM columns; the two bf16 parts of 16 weighted scores lie over those scores
     constexpr uint32_t kP = 0, kOI = 128, kOS = 192, kDS = 256, kX = 448;
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;              // TMEM lane: token of P, OI, OS; y row of S
@@ -478,9 +480,8 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             if (elect_one()) {
                 const uint64_t z = d_z + st * (L::HALF / 16);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16_ta(tmem + kOI, tmem + kP + (kk >> 2) * 64 + (kk & 3) * 8, z + mnmaj(kk), ID_O,
-                                kk > 0);
+                for (int kk = 0; kk < 16; ++kk)   // both parts of every 16 scores
+                    mma_bf16_ta(tmem + kOI, tmem + kP + kk * 8, z + mnmaj(kk >> 1), ID_O, kk > 0);
                 lt_commit(b_oi);
                 lt_commit(b_o + 8 * st);
             }
@@ -603,15 +604,19 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 if (!wait(b_w + 8 * ts, (it / kLtTabs) & 1) || !wait(b_p, ph)) break;
                 tc::fence_after_sync();
                 // 16 columns at a time, in a loop: straight-line code for all of them would not
-                // stay in the instruction caches.  A warp's bf16 columns lie over scores that
-                // it has read itself.
+                // stay in the instruction caches.  Their two parts take the columns that they were in.
 #pragma unroll 1
                 for (int h = 0; h < 4; ++h) {
                     const int c0 = half * 64 + h * 16, cb = c0 >> 5;
-                    float pk[8];   // pairs of bf16 as 32-bit columns
+                    float pk[16];   // pairs of bf16 as 32-bit columns, then what their rounding left
+                    auto put = [&](int j, float2 x) {
+                        const uint32_t w = f2_bf16x2(x);
+                        pk[j] = __uint_as_float(w);
+                        pk[8 + j] = __uint_as_float(f2_bf16x2(f2_rest(x, w)));
+                    };
                     if (REV ? cb < quarter : cb > quarter) {   // beyond the diagonal
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) pk[j] = 0.f;
+                        for (int j = 0; j < 16; ++j) pk[j] = 0.f;
                     } else {
                         float v[16];
                         tc::tmem_ld16(tl + kP + c0, v);
@@ -630,8 +635,8 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                                     w[e] = ex2(REV ? -w[e] : w[e]) * v[j + e];
                                     w[e] = (REV ? j + e >= first : j + e <= first) ? w[e] : 0.f;
                                 }
-                                pk[j / 2] = __uint_as_float(bf16x2_bits(w[0], w[1]));
-                                pk[j / 2 + 1] = __uint_as_float(bf16x2_bits(w[2], w[3]));
+                                put(j / 2, make_float2(w[0], w[1]));
+                                put(j / 2 + 1, make_float2(w[2], w[3]));
                             }
                         } else {
                             const float4 *w4 = reinterpret_cast<const float4 *>(
@@ -646,12 +651,12 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                                                             make_float2(v[j], v[j + 1]));
                                 const float2 y = __fmul2_rn(__fmul2_rn(make_float2(c4.z, c4.w), rf),
                                                             make_float2(v[j + 2], v[j + 3]));
-                                pk[j / 2] = __uint_as_float(f2_bf16x2(x));
-                                pk[j / 2 + 1] = __uint_as_float(f2_bf16x2(y));
+                                put(j / 2, x);
+                                put(j / 2 + 1, y);
                             }
                         }
                     }
-                    tc::tmem_st8(tl + kP + half * 64 + h * 8, pk);
+                    tc::tmem_st16(tl + kP + c0, pk);
                 }
                 tc::tmem_wait_st();
                 tc::fence_before_sync();

@@ -93,6 +93,18 @@ def test_narrow_heads_in_segments_and_waves(D, B, H, T):
 
 
 @pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("T", [1, 200])
+def test_scores_are_not_rounded_to_the_inputs_type(D, T):
+    """A score of 1 + 2^-8, halfway between two bf16 values, on v = 1 - 2^-8: the product 1 - 2^-16
+    rounds to 1, a rounded score's would be v or v (1 + 2^-7).  Every token is its own document."""
+    q, k = (torch.zeros(1, 2, T, D, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    q[..., 0], q[..., 1], k[..., :2] = 1.0, 2.0 ** -8, 1.0
+    v = torch.full_like(q, 1 - 2.0 ** -8)
+    o = gka.gka_linear_forward(q, k, v, torch.zeros(1, 2, T, device="cuda"))
+    assert torch.equal(o, torch.ones_like(o))
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
 def test_fp32_gradients_of_bf16_inputs_read_all_of_the_state(D):
     """dgate of one token is v^T R k with R = dfinal_state: a state whose third bf16 part is as large
     as it can be (1 + 2^-9 + 2^-16 1.49, where two parts are 2^-17 off) and rows of one sign.
