@@ -52,10 +52,13 @@ struct LinLayout {
     size_t total;
 };
 
-// Segments per sequence: enough CTAs for `per_sm` on every SM, whole chunks each.
-static int lin_segments(int ctas, int N, int per_sm) {
-    const int S = ctas > 0 ? kSms * per_sm / ctas : 1;
-    return std::max(1, std::min(S, N));
+// Segments per sequence: enough CTAs for every SM, whole chunks each.  A few chunks in a row are
+// faster than the two launches more: 4 heads of D = 128, device time without and with segments, on
+// the tensor cores 4 chunks 13.9 and 16.4 us (gradients 42 and 53), 6 chunks 18.4 and 16.7 (57
+// and 54); on CUDA cores 2 chunks 18.0 and 20.7, 4 chunks 35 and 21.
+static int lin_segments(int ctas, int N, int D, bool tc) {
+    const int S = ctas > 0 ? kSms * (tc ? 1 : lin_per_sm(D)) / ctas : 1;
+    return N <= (tc ? 5 : 2) ? 1 : std::max(1, std::min(S, N));
 }
 
 static int lin_layout(int B, int H, int T, int D, gka_dtype dt, bool bwd, LinLayout *L) {
@@ -67,7 +70,7 @@ static int lin_layout(int B, int H, int T, int D, gka_dtype dt, bool bwd, LinLay
     const int C = L->tc ? kLtC : kLinC;
     L->ZS = lt_splits(D);   // of 64 columns, in both forms
     L->N = (int)(((long long)T + C - 1) / C);
-    L->S = lin_segments((int)BH * L->ZS, L->N, L->tc ? 1 : lin_per_sm(D));
+    L->S = lin_segments((int)BH * L->ZS, L->N, D, L->tc);
     L->dots = L->tc ? kLtDots * L->ZS : D / 32;
     L->fdots = L->tc ? kLtFdots * L->ZS : L->ZS;
     size_t off = 0;

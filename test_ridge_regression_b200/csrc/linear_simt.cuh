@@ -182,9 +182,10 @@ __host__ __device__ constexpr int lin_per_sm(int D) { return D > 64 ? 2 : D > 32
 // columns): a thread has R tokens x 4 columns of the outputs and SR x 4 of the state, so that
 // a row of S or z is one pass of shared memory for the warp and serves R (SR) x 4 products of
 // each thread.  Chunk n + 1's tiles and decays come from memory, and its decay table is formed,
-// while chunk n is worked on.  What bounds it: the fp32 pipe and shared memory, 5000 cycles each
-// of some 8000 a chunk (D = 128); B2 H1 T88769 D128 730 us with the aggregates (32 columns a
-// CTA, 1 x 4 and 4 x 4 tiles, tables between the chunks: 1276), against 194 of FMAs at 60 TFLOP/s.
+// while chunk n is worked on.  What bounds it: shared memory, whose passes take 70 % of the
+// cycles (a 16-byte load is four, whatever its lanes share; larger tiles a thread are the next
+// step), issue slots 50 %.  B2 H1 T88769 D128: 730 us with the aggregates (32 columns a CTA, 1 x 4
+// and 4 x 4 tiles, tables between the chunks: 1276), against 194 of FMAs at 60 TFLOP/s.
 // Where few chunks are left a launch (T of some hundreds), the launches' latency.
 template <int D, bool REV, bool OUT>
 __global__ void __launch_bounds__(kLinThreads, lin_per_sm(D))
