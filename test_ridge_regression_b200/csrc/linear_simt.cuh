@@ -168,6 +168,26 @@ __device__ __forceinline__ Log2Sum lin_log_prefix(const float *beta, int t0, int
     return lin_log_prefix(t < T ? log2_decay(beta[t], log2_min) : 0.f);
 }
 
+// A 4 x 4 tile's sums over lanes 8 (STEPS = 1) or 8 and 16 (2) apart, the rows shared out among
+// those lanes: lane group k = (lane >> 3) % (2 STEPS) is left with rows 2 k, 2 k + 1 (1) or k (2)
+// as its first.
+template <int STEPS>
+__device__ __forceinline__ void quarter_sums(float (&a)[4][4]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int s = STEPS; s > 0; --s) {
+        const int rows = STEPS == 2 && s == 1 ? 1 : 2;   // left after this exchange
+        const bool up = lane & (8 * s);
+#pragma unroll
+        for (int i = 0; i < rows; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float send = up ? a[i][j] : a[i + rows][j], keep = up ? a[i + rows][j] : a[i][j];
+                a[i][j] = keep + __shfl_xor_sync(0xffffffffu, send, 8 * s);
+            }
+    }
+}
+
 struct LinPasses {
     LinPass pass[2];
 };
@@ -179,13 +199,13 @@ __host__ __device__ constexpr int lin_per_sm(int D) { return D > 64 ? 2 : D > 32
 // (states from zero) and decays only.
 //
 // Warp (token group, column half) and lane (four tokens or state rows) x (eight groups of four
-// columns): a thread has R tokens x 4 columns of the outputs and SR x 4 of the state, so that
-// a row of S or z is one pass of shared memory for the warp and serves R (SR) x 4 products of
-// each thread.  Chunk n + 1's tiles and decays come from memory, and its decay table is formed,
-// while chunk n is worked on.  What bounds it: shared memory, whose passes take 70 % of the
-// cycles (a 16-byte load is four, whatever its lanes share; larger tiles a thread are the next
-// step), issue slots 50 %.  B2 H1 T88769 D128: 730 us with the aggregates (32 columns a CTA, 1 x 4
-// and 4 x 4 tiles, tables between the chunks: 1276), against 194 of FMAs at 60 TFLOP/s.
+// columns): a thread has SR x 4 of the state and, for the scores and the state's part of the
+// outputs, a 4 x 4 tile over a part of the sum, which shuffles join, since a 16-byte load is four
+// passes of shared memory whatever its lanes share.  Chunk n + 1's tiles and decays come from
+// memory, and its decay table is formed, while chunk n is worked on.  What bounds it: shared
+// memory (70 % of the cycles before those tiles, issue slots 50 %).  B2 H1 T88769 D128: 638 us with
+// the aggregates (whole sums a thread, 2 x 2 and 2 x 4: 730; 32 columns a CTA and tables between
+// the chunks: 1276), against 194 of FMAs at 60 TFLOP/s.
 // Where few chunks are left a launch (T of some hundreds), the launches' latency.
 template <int D, bool REV, bool OUT>
 __global__ void __launch_bounds__(kLinThreads, lin_per_sm(D))
@@ -218,7 +238,9 @@ k_linear_pass(const __grid_constant__ LinPasses args) {
     const float *gate = p.gate ? p.gate + (size_t)bh * p.T : nullptr;
 
     const int ch = warp % HC, tg = warp / HC, zc = ch * 32 + (lane & 7) * 4;   // columns zc..zc + 3
-    const int tok = tg * 4 * R + (lane >> 3);                                  // tokens tok + 4 i
+    constexpr int KG = 4 / R;                                                  // parts of a sum over d
+    const int kg = (lane >> 3) % KG, tile = tg * 4 * R + (lane >> 3) / KG * 4;  // its tile's first token
+    const int tok = tile + kg * R;                                             // tokens tok + i
     const int yr = (tg * 4 + (lane >> 3)) * SR;                                // state rows yr + i
     float st[SR][4];
     auto state_at = [&](size_t base, int i, int j) {
@@ -306,62 +328,65 @@ k_linear_pass(const __grid_constant__ LinPasses args) {
                 f = warp_sum(f);
                 if (lane == 0) s_red[warp] = f;
             }
-            // P: thread (tr, tc) holds rows tr, tr + 16 and columns tc, tc + 16, but for the
-            // pair beyond the diagonal
-            const int tr = tid >> 4, tc = tid & 15;
-            float acc[2][2] = {};
-#pragma unroll 4
-            for (int d = 0; d < D; d += 4) {
-                float4 xv[2], yv[2];
+            // P: a lane's 4 x 4 tile, rows 4 warp + i and columns (lane & 7) + 8 j, over a quarter
+            // of d (16 bytes of every 64); columns beyond the warp's diagonal are left out
+            {
+                const int p4 = lane & 7, k4 = lane >> 3;
+                float acc[4][4] = {};
+#pragma unroll 2
+                for (int d = 4 * k4; d < D; d += 16) {
+                    float4 xv[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    xv[i] = *reinterpret_cast<const float4 *>(xs + (tr + 16 * i) * LD + d);
-                    yv[i] = *reinterpret_cast<const float4 *>(ys + (tc + 16 * i) * LD + d);
-                }
+                    for (int i = 0; i < 4; ++i) xv[i] = *reinterpret_cast<const float4 *>(xs + (4 * warp + i) * LD + d);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                    for (int j = 0; j < 4; ++j) {
+                        if (REV ? j < (warp >> 1) : j > (warp >> 1)) continue;
+                        const float4 yv = *reinterpret_cast<const float4 *>(ys + (p4 + 8 * j) * LD + d);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (REV ? i > j : i < j) continue;
-                        acc[i][j] = fmaf(xv[i].x, yv[j].x, acc[i][j]);
-                        acc[i][j] = fmaf(xv[i].y, yv[j].y, acc[i][j]);
-                        acc[i][j] = fmaf(xv[i].z, yv[j].z, acc[i][j]);
-                        acc[i][j] = fmaf(xv[i].w, yv[j].w, acc[i][j]);
+                        for (int i = 0; i < 4; ++i) {
+                            acc[i][j] = fmaf(xv[i].x, yv.x, acc[i][j]);
+                            acc[i][j] = fmaf(xv[i].y, yv.y, acc[i][j]);
+                            acc[i][j] = fmaf(xv[i].z, yv.z, acc[i][j]);
+                            acc[i][j] = fmaf(xv[i].w, yv.w, acc[i][j]);
+                        }
                     }
-            }
+                }
+                quarter_sums<2>(acc);   // row k4 of the tile is left
+                const int t = 4 * warp + k4;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int t = tr + 16 * i, c = tc + 16 * j;
+                for (int j = 0; j < 4; ++j) {
+                    const int c = p4 + 8 * j;
                     const bool in = REV ? c >= t : c <= t;
                     const float w = REV ? p.scale : s_g[c];
                     Ps[t * (C + 1) + c] =
-                        in ? acc[i][j] * w * (REV ? exp2_diff(s_l[c], s_l[t]) : exp2_diff(s_l[t], s_l[c])) : 0.f;
+                        in ? acc[0][j] * w * (REV ? exp2_diff(s_l[c], s_l[t]) : exp2_diff(s_l[t], s_l[c])) : 0.f;
                 }
-            // the state's part of the outputs
+            }
+            // the state's part of the outputs: 4 tokens x 4 columns, over a part of d
+            float acc[4][4] = {};
+#pragma unroll 2
+            for (int d = 4 * kg; d < D; d += 4 * KG) {
+                float xa[4][4];
 #pragma unroll
-            for (int i = 0; i < R; ++i) si[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int d = 0; d < D; d += 4) {
-                float xa[R][4];
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const float4 xv = *reinterpret_cast<const float4 *>(xs + (tok + 4 * i) * LD + d);
+                for (int i = 0; i < 4; ++i) {
+                    const float4 xv = *reinterpret_cast<const float4 *>(xs + (tile + i) * LD + d);
                     xa[i][0] = xv.x; xa[i][1] = xv.y; xa[i][2] = xv.z; xa[i][3] = xv.w;
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float4 s = *reinterpret_cast<const float4 *>(St + (d + e) * ZN + zc);
 #pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        si[i].x = fmaf(xa[i][e], s.x, si[i].x);
-                        si[i].y = fmaf(xa[i][e], s.y, si[i].y);
-                        si[i].z = fmaf(xa[i][e], s.z, si[i].z);
-                        si[i].w = fmaf(xa[i][e], s.w, si[i].w);
+                    for (int i = 0; i < 4; ++i) {
+                        acc[i][0] = fmaf(xa[i][e], s.x, acc[i][0]);
+                        acc[i][1] = fmaf(xa[i][e], s.y, acc[i][1]);
+                        acc[i][2] = fmaf(xa[i][e], s.z, acc[i][2]);
+                        acc[i][3] = fmaf(xa[i][e], s.w, acc[i][3]);
                     }
                 }
             }
+            quarter_sums<KG / 2>(acc);
+#pragma unroll
+            for (int i = 0; i < R; ++i) si[i] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
         }
         if (it + 1 < n1 - n0) table(it + 1);
         if (OUT) {
@@ -381,7 +406,7 @@ k_linear_pass(const __grid_constant__ LinPasses args) {
                 const float4 z = *reinterpret_cast<const float4 *>(zs + c * ZN + zc);
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    const float pv = Ps[(tok + 4 * i) * (C + 1) + c];
+                    const float pv = Ps[(tok + i) * (C + 1) + c];
                     in[i].x = fmaf(pv, z.x, in[i].x);
                     in[i].y = fmaf(pv, z.y, in[i].y);
                     in[i].z = fmaf(pv, z.z, in[i].z);
@@ -390,7 +415,7 @@ k_linear_pass(const __grid_constant__ LinPasses args) {
             }
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int t = tok + 4 * i;
+                const int t = tok + i;
                 const bool inside = t0 + t < p.T;
                 const float a = s_a[t] * (REV ? 1.f : p.scale), c = REV ? s_g[t] : p.scale;
                 const float4 r = make_float4(a * si[i].x, a * si[i].y, a * si[i].z, a * si[i].w);   // (without g)
