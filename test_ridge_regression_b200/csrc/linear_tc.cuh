@@ -25,13 +25,17 @@
 // 4 % (B8 H8 T2048 D128 kernel 49 -> 51 us, B1 H8 T131072 269 -> 281).
 //
 // Roles (640 threads, one CTA an SM).  What follows at -> is a barrier and who waits:
-//   warp 18      loads x (one stage), y, z (two), decay tables (four) -> 17, 8-15, 0-7
+//   warp 18      loads x (one stage), y (two) -> 17;  z (two) -> 17, 8-15;  decay tables (four)
+//                -> 0-15
 //   warp 17      x from shared memory to TMEM, P -> 0-7;  OI -> 0-7
 //   warp 16      OS -> 0-7, 17;  DS -> 8-15
 //   warps 0-7    P -> weighted scores in TMEM (thread: a token, 64 columns) -> 17;
 //                a OS + OI -> rows staged where z was -> 19
 //   warps 8-15   S as OS's operand -> 16;  parts of u z -> 16;  S' = b S + DS
 //   warp 19      rows out by TMA, z's stage free again -> 18
+// An operand's load is waited for by the issuer that reads it, or by a role whose arrival that
+// issuer waits for: y by 17, whose copies of x 16 waits for; z by 17 itself, since the state's
+// warps hand S over (and so let OS run) before they look at z.
 // A barrier that some waiter could be two phases behind on has two copies.  Every wait
 // is bounded and gives up once another role has; the issuers and the loader then drain
 // what they have in flight, TMEM is freed and the device flag set.
@@ -474,7 +478,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             // x of the next chunk once this one's OS and P have read it in TMEM, while the
             // weighted scores are formed
             if (it + 1 < NL) ok = wait(b_p, ph) && wait(b_os, ph) && copy_x(it + 1);
-            ok = ok && wait(b_pb, ph);
+            ok = ok && wait(b_z + 8 * st, (it >> 1) & 1) && wait(b_pb, ph);
             if (!ok) break;
             tc::fence_after_sync();
             if (elect_one()) {
