@@ -372,6 +372,8 @@ typedef struct {
  *   q_out, k_out, v_out   [B, H, T, D] in `dt` (written);  beta [B, H, T] fp32 (written)
  *   gate          [B, H, T] fp32 (written); non-NULL exactly when gate_logit or
  *                 lengths is (1 where only lengths is)
+ *   eps           finite, >= 0.  With 0 a zero row has no direction and becomes NaN
+ *                 (not padding, which is zero whatever eps is)
  */
 int gka_block_in_forward(const gka_strided *q, const gka_strided *k, const gka_strided *v,
                          const gka_strided *beta_logit, const gka_strided *gate_logit,

@@ -225,7 +225,8 @@ k_block_in(const BlockInArgs a, T *__restrict__ qo, T *__restrict__ ko, T *__res
             V::unpack(y, f);
 #pragma unroll
             for (int i = 0; i < V::N; ++i) ss = fmaf(f[i], f[i], ss);
-            const float rn = rsqrtf(row_sum<LPR>(ss) + a.eps);
+            ss = row_sum<LPR>(ss);
+            const float rn = s.t < len ? rsqrtf(ss + a.eps) : 0.f;   // padding stays zero, with eps = 0 too
 #pragma unroll
             for (int i = 0; i < V::N; ++i) f[i] *= rn;
             y = V::pack(f);
@@ -361,7 +362,8 @@ k_block_in_grad(const BlockInArgs a, const BlockInGrad g) {
             }
             ss = row_sum<LPR>(ss);
             xd = row_sum<LPR>(xd);
-            const float rn = rsqrtf(ss + a.eps), c = rn * rn * xd;   // r (dy - r x (r x . dy))
+            const float rn = s.t < len ? rsqrtf(ss + a.eps) : 0.f;   // (as in k_block_in)
+            const float c = rn * rn * xd;                            // r (dy - r x (r x . dy))
 #pragma unroll
             for (int i = 0; i < V::N; ++i) dy[j][i] = rn * (dy[j][i] - c * f[i]);
         }
@@ -532,7 +534,8 @@ k_block_out_grad(const BlockOutArgs a, const BlockOutGrad g) {
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < V::N; ++i) ss = fmaf(u[i], u[i], ss);
-        const float rn = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
+        ss = row_sum<LPR>(ss);
+        const float rn = in0 ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;   // past the end zeros, with eps = 0 too
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < V::N; ++i) {
@@ -545,7 +548,7 @@ k_block_out_grad(const BlockOutArgs a, const BlockOutGrad g) {
                 dy[i] = dyi * (z[i] * sg);
                 z[i] = dyi * u[i] * w[i] * dsil;
             }
-            dw[i] = fmaf(dy[i], u[i], dw[i]);   // (rows past the end are zeros)
+            dw[i] = fmaf(dy[i], u[i], dw[i]);   // (zeros past the end)
             dy[i] *= w[i];   // dn
             dot = fmaf(dy[i], u[i], dot);
         }

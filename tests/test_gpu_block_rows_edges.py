@@ -1,0 +1,54 @@
+"""Edges of the block's row operations: no eps under the root."""
+import pytest
+import torch
+
+import linear_ref as ref
+from linear_ref import TOL32, rel
+from test_gpu_block_rows import make_in, make_out
+from test_ridge_regression_b200 import build, gka
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_block_in_without_eps(dtype, D):
+    """eps = 0: padding is zero rows and zero gradients, as with any eps."""
+    args, kw, g = make_in(3, 37, 4, 2, D, dtype, 31, lengths=[37, 0, 13])
+    got = gka.gka_block_in(*args, **kw, eps=0.0)
+    want = ref.block_in(*args, kw["gate_logit"], kw["beta_bias"], kw["gate_bias"], kw["lengths"], 0.0)
+    for x, y in zip(got, want):
+        tol = 2.0 ** -8 + 1e-6 if x.dtype == torch.bfloat16 else 1e-6   # half a step of the type
+        assert rel(x, y) <= tol
+    for x in got[:3]:
+        assert not x[1].any() and not x[2, :, 13:].any()
+    ups = [torch.randn(3, 4, 37, D, generator=g).to(dtype).cuda() for _ in range(3)]
+    ups += [torch.randn(3, 4, 37, generator=g).cuda() for _ in range(2)]
+    back = gka.gka_block_in_backward(args[0], args[1], args[3], *ups[:4], dgate=ups[4], **kw, eps=0.0)
+    leaves = [x.double().requires_grad_() for x in args[:3]]
+    out = ref.block_in(*leaves, args[3], kw["gate_logit"], kw["beta_bias"], kw["gate_bias"], None, 0.0)
+    real = torch.arange(37, device="cuda")[None, :] < kw["lengths"][:, None]
+    loss = sum((torch.where(real[:, None, :, None], x, 0.0) * u.double()).sum() for x, u in zip(out, ups[:3]))
+    for n, y in zip(("dq", "dk", "dv"), torch.autograd.grad(loss, leaves)):
+        assert rel(back[n], y) <= (2.0 ** -8 if dtype == torch.bfloat16 else TOL32), n
+        assert not back[n][1].any() and not back[n][2, 13:].any(), n
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("T", [1, 7, 250])
+def test_block_out_gradient_without_eps(dtype, D, T):
+    """eps = 0 and real rows that are not zero: lanes past a block's run add nothing to dw and dskip."""
+    o, w, kw, g = make_out(1, T, 3, D, dtype, 32, True, True)
+    dy = torch.randn(1, T, 3, D, generator=g).to(dtype).cuda()
+    got = gka.gka_block_out_backward(o, w, dy, **kw, eps=0.0)
+    leaves = {n: x.double().requires_grad_() for n, x in {"o": o, "w": w, **kw}.items()}
+    loss = (ref.block_out(**leaves, eps=0.0) * dy.double()).sum()
+    for n, y in zip(leaves, torch.autograd.grad(loss, list(leaves.values()))):
+        x = got["d" + n]
+        assert rel(x, y) <= (TOL32 if x.dtype == torch.float32 else 2.0 ** -8), n
