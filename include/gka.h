@@ -403,7 +403,8 @@ int gka_block_in_backward(const gka_strided *q, const gka_strided *k,
  *   u = o + skip_h v,   y = u (|u|^2 / D + eps)^-1/2 * w * silu(z)
  *   o, v   [B, H, T, D] in `dt`; v nullable, and skip (fp32 [H]) non-NULL exactly when v is
  *   z      [B, T, H, D] at strides; nullable (no gate)
- *   w      fp32 [D];   y [B, T, H, D] dense in `dt` (written)
+ *   w      fp32 [D];   y [B, T, H, D] dense in `dt` (written; no input's memory, nor any
+ *          between z's first element and its last)
  */
 int gka_block_out_forward(const void *o, const void *v, const gka_strided *z, const float *w,
                           const float *skip, void *y, int B, int T, int H, int D, gka_dtype dt,

@@ -393,12 +393,19 @@ def _need(name, t, shape, dtype):
 
 
 def _apart(*outs):
-    """No two of a call's outputs (and the inputs given with them) share memory."""
-    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
-                   for t in outs if t is not None and t.numel())
+    """No two of a call's outputs (and the inputs given with them) share memory; of a strided
+    tensor, from its first element to its last."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + _extent(t)) for t in outs if t is not None and t.numel())
     for (_, e), (b, _) in zip(spans, spans[1:]):
         if b < e:
             raise ValueError("outputs must not share memory with each other or with inputs")
+
+
+def _extent(t):
+    """Bytes from a tensor's first element to behind its last."""
+    if t.is_contiguous():
+        return t.numel() * t.element_size()
+    return (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))) * t.element_size()
 
 
 def _under(stream, fn, *args, **kw):
@@ -676,7 +683,7 @@ def gka_block_out(o, w, *, z=None, v=None, skip=None, eps=1e-6, y=None, stream=N
     else:
         _dense(y)
         _need("y", y, (B, T, H, D), o.dtype)
-        for t in (o, w, v, skip):
+        for t in (o, w, z, v, skip):
             _apart(y, t)
     _invoke("gka_block_out_forward", dev, _p(o), _p(v), sz, _p(w), _p(skip), _p(y), B, T, H,
             D, dt, eps)

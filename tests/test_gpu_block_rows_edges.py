@@ -1,4 +1,4 @@
-"""Edges of the block's row operations: no eps under the root."""
+"""Edges of the block's row operations: no eps under the root, an output over the gate's rows."""
 import pytest
 import torch
 
@@ -52,3 +52,18 @@ def test_block_out_gradient_without_eps(dtype, D, T):
     for n, y in zip(leaves, torch.autograd.grad(loss, list(leaves.values()))):
         x = got["d" + n]
         assert rel(x, y) <= (TOL32 if x.dtype == torch.float32 else 2.0 ** -8), n
+
+
+def test_an_output_over_the_gate_is_refused():
+    """y in z's memory, all of it, a part, or between z's strided rows: other blocks still read z."""
+    o, w, _, _ = make_out(2, 8, 4, 64, torch.bfloat16, 33, False, False)
+    rows = torch.zeros(3, 8, 4, 64, device="cuda", dtype=torch.bfloat16)
+    for z, y in ((rows[:2], rows[:2]), (rows[:2], rows[1:])):
+        with pytest.raises(ValueError):
+            gka.gka_block_out(o, w, z=z, y=y)
+    wide = torch.zeros(2, 8, 12, 64, device="cuda", dtype=torch.bfloat16)
+    inside = wide.view(-1)[4 * 64:4 * 64 + o.numel()].view(2, 8, 4, 64)
+    with pytest.raises(ValueError):
+        gka.gka_block_out(o, w, z=wide[:, :, :4], y=inside)
+    y = gka.gka_block_out(o, w, z=rows[:2], y=rows[2:].new_zeros(2, 8, 4, 64))   # apart: taken
+    assert not y.any()
