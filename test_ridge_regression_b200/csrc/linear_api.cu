@@ -583,7 +583,13 @@ int gka_block_in_backward(const gka_strided *q, const gka_strided *k,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const size_t n = (size_t)B * H * T;
     if (n == 0) {
-        // no token: the shared gradients are empty sums
+        // no token: the shared gradients are empty sums; no query heads: those of k and v too
+        const size_t kv = (size_t)B * T * Hk * D * (dt == GKA_BF16 ? 2 : 4) / sizeof(float);
+        if (kv > 0) {
+            if (!dk || !dv) return GKA_ERR_INVALID_ARG;
+            if (int rc = pass_state(static_cast<float *>(dk), nullptr, kv, s)) return rc;
+            if (int rc = pass_state(static_cast<float *>(dv), nullptr, kv, s)) return rc;
+        }
         if (int rc = pass_state(dbeta_bias, nullptr, H, s)) return rc;
         return pass_state(dgate_bias, nullptr, H, s);
     }

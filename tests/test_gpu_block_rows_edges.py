@@ -1,4 +1,5 @@
-"""Edges of the block's row operations: no eps under the root, an output over the gate's rows."""
+"""Edges of the block's row operations: no eps under the root, an output over the gate's rows,
+no query heads."""
 import pytest
 import torch
 
@@ -67,3 +68,18 @@ def test_an_output_over_the_gate_is_refused():
         gka.gka_block_out(o, w, z=wide[:, :, :4], y=inside)
     y = gka.gka_block_out(o, w, z=rows[:2], y=rows[2:].new_zeros(2, 8, 4, 64))   # apart: taken
     assert not y.any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_no_query_heads(dtype):
+    """H = 0: the gradients of the key and value heads are empty sums, written as such."""
+    q, bl = torch.zeros(2, 5, 0, 64, device="cuda", dtype=dtype), torch.zeros(2, 5, 0, device="cuda", dtype=dtype)
+    k = torch.ones(2, 5, 3, 64, device="cuda", dtype=dtype)
+    up, db = q.transpose(1, 2).contiguous(), torch.zeros(2, 0, 5, device="cuda")
+    assert gka.gka_block_in(q, k, k, bl)[1].shape == (2, 0, 5, 64)
+    for _ in range(3):   # the allocator hands out memory that held NaN
+        dirty = [torch.full_like(k, float("nan")) for _ in range(4)]
+        torch.cuda.synchronize()
+        del dirty
+        got = gka.gka_block_in_backward(q, k, bl, up, up, up, db)
+        assert not got["dk"].any() and not got["dv"].any() and got["dq"].shape == q.shape
