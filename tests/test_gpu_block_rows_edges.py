@@ -1,5 +1,5 @@
 """Edges of the block's row operations: no eps under the root, an output over the gate's rows,
-no query heads."""
+no query heads, far negative gates."""
 import pytest
 import torch
 
@@ -83,3 +83,25 @@ def test_no_query_heads(dtype):
         del dirty
         got = gka.gka_block_in_backward(q, k, bl, up, up, up, db)
         assert not got["dk"].any() and not got["dv"].any() and got["dq"].shape == q.shape
+
+
+def test_far_gates_element_by_element():
+    """z from -95 to 40 in bf16, each element for itself.  The result's rounding (2^-8), at most
+    2^-15 of arithmetic (the exponential's error grows with |z|, to 2^-16 at -90), and half of
+    bf16's smallest step, 2^-134, with the same again for an exponential below fp32's normals."""
+    D, T = 128, 64
+    g = torch.Generator().manual_seed(34)
+    o = torch.randn(1, 1, T, D, generator=g).bfloat16().cuda()
+    o = torch.where(o.abs() < 0.1, torch.ones_like(o), o)
+    z = torch.linspace(-95.0, 40.0, T * D).view(1, T, 1, D).bfloat16().cuda()
+    z = torch.where((z + 1.2785).abs() < 0.5, torch.full_like(z, 2.0), z)   # silu' has its zero there
+    w = torch.rand(D, generator=g).cuda() + 0.5
+    dy = (torch.rand(1, T, 1, D, generator=g) + 0.5).bfloat16().cuda()
+    want = ref.block_out(o, w, z=z)
+    y = gka.gka_block_out(o, w, z=z).double()
+    leaf = z.double().requires_grad_()
+    (dz,) = torch.autograd.grad((ref.block_out(o, w, z=leaf) * dy.double()).sum(), leaf)
+    got = gka.gka_block_out_backward(o, w, dy, z=z)["dz"].double()
+    for x, e in ((y, want), (got, dz)):
+        assert ((x - e).abs() <= (2.0 ** -8 + 2.0 ** -15) * e.abs() + 2.0 ** -133).all()
+    assert (y[z < -80].abs() > 0).any()
