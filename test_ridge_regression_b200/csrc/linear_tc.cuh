@@ -5,7 +5,7 @@
 // tokens and every product is tcgen05 with fp32 accumulators in TMEM:
 //   P  [128 t][128 i] = X Y^T                      scores (both operands as loaded)
 //   OI [128 t][64 z]  = (w . P)_hi,lo Z            inside the chunk; w . P in TMEM
-//   OS [128 t][64 z]  = X (S_hi + S_lo (+ S_3))    against the state before the chunk
+//   OS [128 t][64 z]  = X (S_hi + S_mid + S_lo)    against the state before the chunk
 //   DS [128 y][64 z]  = Y^T (u Z)_hi,mid,lo        the chunk's increment
 //   S' = b S + DS                                  fp32, in registers for the whole sequence
 // A CTA owns 64 of z's columns for one head and one segment (a whole sequence where
@@ -16,10 +16,10 @@
 //
 // Roundings.  bf16 inputs enter the products exactly.  The increments' weighted
 // rows u z are split into three bf16 parts (24 bits: the state is an fp32 one, and
-// final_state is an output).  The state read by OS is split into two (16 bits,
-// relative 2^-17: the output is rounded to 8 bits), or three where its product also
-// forms a term of dbeta, an fp32 output (dbeta and dgate were 1e-6 to 3e-6 off with
-// two parts, 2e-7 to 8e-7 with three).  The weighted scores enter in two parts: one
+// final_state is an output).  The state read by OS is split into three too: an error of two
+// parts, 2^-17 of the state, is more than the output's own rounding where a query reads
+// something 2^9 times smaller than the rest of the state, and shows in dbeta and dgate, fp32
+// outputs (1e-6 to 3e-6 off with two parts, 2e-7 to 8e-7 with three).  The weighted scores enter in two parts: one
 // alone is a rounding as large as the output's own (2.3e-3 off against 1.7e-3, and up to
 // twice that in sequences of a few tokens, whose rows are few products), and two cost
 // 4 % (B8 H8 T2048 D128 kernel 49 -> 51 us, B1 H8 T131072 269 -> 281).
@@ -31,7 +31,8 @@
 //   warp 16      OS -> 0-7, 17;  DS -> 8-15
 //   warps 0-7    P -> weighted scores in TMEM (thread: a token, 64 columns) -> 17;
 //                a OS + OI -> rows staged where z was -> 19
-//   warps 8-15   S as OS's operand -> 16;  parts of u z -> 16;  S' = b S + DS
+//   warps 8-15   S as OS's operand -> 16;  parts of u z (once OS is done: the third lies where
+//                the state's third was) -> 16;  S' = b S + DS
 //   warp 19      rows out by TMA, z's stage free again -> 18
 // An operand's load is waited for by the issuer that reads it, or by a role whose arrival that
 // issuer waits for: y by 17, whose copies of x 16 waits for; z by 17 itself, since the state's
@@ -89,7 +90,7 @@ struct LtSmem {
     static constexpr uint32_t Y = X + TILE;               // 2 stages
     static constexpr uint32_t Z = Y + 2 * TILE;           // 2 stages
     static constexpr uint32_t PARTS = Z + 2 * HALF;       // hi, mid, lo of u z
-    static constexpr uint32_t SOP = PARTS + 3 * HALF;     // hi, lo of the state
+    static constexpr uint32_t SOP = PARTS + 3 * HALF;     // hi, mid of the state
     static constexpr uint32_t TAB = SOP + 2 * HALF;       // decay tables of the chunks in flight
     // table floats, 128 tokens each: a, u, l (of the row), ta, c[3], and g (backward) or m (l
     // less log2 of the gate, of the column; forward); then b
@@ -305,10 +306,9 @@ __device__ __forceinline__ void lt_parts(const uint8_t *z, uint8_t *dst, float u
     *reinterpret_cast<uint4 *>(dst + 2 * LtSmem::HALF) = make_uint4(c[0], c[1], c[2], c[3]);
 }
 
-// GRAD: the passes of the backward, which also keep the states, form dbeta's dots and, for
-// those, take the state in three parts.  The third lies where the third part of u z goes next,
-// which therefore waits for OS.  B8 H8 T2048 D128: dq's pass 62 us, dv's and dk's 124 (256 CTAs,
-// two waves on 148 SMs).  Over x's stage instead it held back the next x: 14 and 6 % more.
+// GRAD: the passes of the backward, which also keep the states and form dbeta's dots.
+// B8 H8 T2048 D128: dq's pass 62 us, dv's and dk's 124 (256 CTAs, two waves on 148 SMs).
+// The state's third part over x's stage instead held back the next x: 14 and 6 % more.
 // grid (lt_splits(D) * passes, B*H, S), block kLtThreads.
 template <bool REV, bool GRAD>
 __global__ void __launch_bounds__(kLtThreads, 1)
@@ -336,7 +336,6 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int zh = blockIdx.x % ZS, bh = blockIdx.y, seg = blockIdx.z, D = p.D;
     const uint32_t tile = lt_tile_bytes(D);   // of a tile of x or y in memory
-    const bool three = GRAD && p.dot;         // OS takes the state in three parts, not two
     const int n0 = lin_seg(seg, p.S, p.N), n1 = lin_seg(seg + 1, p.S, p.N), NL = n1 - n0;
     auto chunk = [&](int it) { return REV ? n1 - 1 - it : n0 + it; };
 
@@ -415,16 +414,13 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             tc::fence_after_sync();
             if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 16; ++kk)   // K steps against S_hi, then S_lo, 16 KB on
+                for (int kk = 0; kk < 16; ++kk)   // K steps against S_hi, then S_mid, 16 KB on
                     if ((kk & 7) * 16 < D)
                         mma_bf16_ta(tmem + kOS, tmem + kX + (kk & 7) * 8, d_s + mnmaj(kk), ID_O, kk > 0);
-                if (three) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)   // and the third part
-                        if (kk * 16 < D)
-                            mma_bf16_ta(tmem + kOS, tmem + kX + kk * 8, d_u + 2 * (L::HALF / 16) + mnmaj(kk), ID_O,
-                                        true);
-                }
+                for (int kk = 0; kk < 8; ++kk)   // and S_lo
+                    if (kk * 16 < D)
+                        mma_bf16_ta(tmem + kOS, tmem + kX + kk * 8, d_u + 2 * (L::HALF / 16) + mnmaj(kk), ID_O, true);
                 lt_commit(b_os);
             }
             ok = wait(b_parts, ph);
@@ -738,7 +734,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             const int sg = it & 1, ph = it & 1, ts = it % kLtTabs, n = chunk(it);
             const float *tab = s_tab + ts * kLtTabF;
             {
-                // the state before the chunk as the B operand, rows of y, two or three bf16 parts
+                // the state before the chunk as the B operand, rows of y, three bf16 parts
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     uint32_t a[4], b[4], c[4];
@@ -748,19 +744,18 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                         a[e] = f2_bf16x2(y);
                         y = f2_rest(y, a[e]);
                         b[e] = f2_bf16x2(y);
-                        c[e] = GRAD ? f2_bf16x2(f2_rest(y, b[e])) : 0u;
+                        c[e] = f2_bf16x2(f2_rest(y, b[e]));
                     }
                     const uint32_t at = row * 128 + (((half * 4 + h) ^ (row & 7)) << 4);
                     *reinterpret_cast<uint4 *>(sm + L::SOP + at) = make_uint4(a[0], a[1], a[2], a[3]);
                     *reinterpret_cast<uint4 *>(sm + L::SOP + L::HALF + at) = make_uint4(b[0], b[1], b[2], b[3]);
-                    if (three)   // in the place of the third part of u z, which waits for OS
-                        *reinterpret_cast<uint4 *>(sm + L::PARTS + 2 * L::HALF + at) = make_uint4(c[0], c[1], c[2], c[3]);
+                    // in the place of the third part of u z, which waits for OS
+                    *reinterpret_cast<uint4 *>(sm + L::PARTS + 2 * L::HALF + at) = make_uint4(c[0], c[1], c[2], c[3]);
                 }
                 fence_proxy_async_smem();
                 arrive(b_s);
             }
-            ok = wait(b_w + 8 * ts, (it / kLtTabs) & 1) && wait(b_z + 8 * sg, (it >> 1) & 1) &&
-                 (!three || wait(b_os, ph));
+            ok = wait(b_w + 8 * ts, (it / kLtTabs) & 1) && wait(b_z + 8 * sg, (it >> 1) & 1) && wait(b_os, ph);
             if (!ok) break;
 #pragma unroll 1
             for (int item = gt; item < 1024; item += kLtGroup)   // row item / 8

@@ -1,0 +1,47 @@
+"""bf16 inputs, elements for themselves: outputs and gradients that are small beside the terms they
+are sums of are as near as their own rounding, like those of fp32 arithmetic on the same inputs."""
+import pytest
+import torch
+
+from linear_ref import linear, linear_grad
+from test_ridge_regression_b200 import build, gka
+
+pytestmark = pytest.mark.gpu
+HALF = 2.0 ** -8   # half a step of bf16, relative to the value
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+
+
+def near(got, want, terms, share):
+    """|got - want| within the rounding of the result and `share` of the terms' sizes."""
+    return ((got.double() - want).abs() <= HALF * want.abs() + share * terms).all()
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("T", [1, 130, 1500])
+def test_little_of_a_large_state(D, T):
+    """A state whose first two columns (rows) differ by 2^-10 of them, read by e0 - e1: what a query
+    reads that the rest of the memory is orthogonal to.  The first of T tokens has all of it (the
+    others write nothing; beta is 1).  The state's parts leave 2^-25 of it, and each of their three
+    products is off by at most 2^-23 of its largest term: 2^-21 of the terms in all."""
+    gen = torch.Generator().manual_seed(61)
+    B, H = 2, 9
+    S = torch.randn(B, H, D, D, generator=gen)
+    S[..., 1] = S[..., 0] * (1 + 2.0 ** -10 * torch.randn(B, H, D, generator=gen))
+    R = S.transpose(-1, -2).contiguous()   # dk reads rows of the state's gradient, and dq of the state
+    S, R = S.cuda(), R.cuda()
+    pair, zero = (torch.zeros(B, H, T, D, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    pair[..., 0], pair[..., 1] = 1.0, -1.0
+    one = torch.ones(B, H, T, device="cuda")
+    o = gka.gka_linear_forward(pair, zero, zero, one, initial_state=S)
+    want = (S[..., 0].double() - S[..., 1].double())[:, :, None].expand(B, H, T, D)
+    terms = (S[..., 0].abs() + S[..., 1].abs()).double()[:, :, None]
+    assert near(o, want, terms, 2.0 ** -21)
+    g = gka.gka_linear_backward(zero, zero, zero, one, pair, initial_state=R)
+    assert near(g["dq"], want, terms, 2.0 ** -21)
+    for n, a, X in (("dv", (zero, pair, zero), S), ("dk", (zero, zero, pair), R)):
+        g = gka.gka_linear_backward(*a, one, zero, dfinal_state=X)
+        assert near(g[n], want, terms, 2.0 ** -21), n
