@@ -4,7 +4,7 @@
 // CUDA cores (linear_simt.cuh, which has the formulas); here a chunk is 128
 // tokens and every product is tcgen05 with fp32 accumulators in TMEM:
 //   P  [128 t][128 i] = X Y^T                      scores (both operands as loaded)
-//   OI [128 t][64 z]  = (w . P)_hi,lo Z            inside the chunk; w . P in TMEM
+//   OI [128 t][64 z]  = (w . P)_hi,mid,lo Z        inside the chunk; w . P in TMEM
 //   OS [128 t][64 z]  = X (S_hi + S_mid + S_lo)    against the state before the chunk
 //   DS [128 y][64 z]  = Y^T (u Z)_hi,mid,lo        the chunk's increment
 //   S' = b S + DS                                  fp32, in registers for the whole sequence
@@ -19,10 +19,12 @@
 // final_state is an output).  The state read by OS is split into three too: an error of two
 // parts, 2^-17 of the state, is more than the output's own rounding where a query reads
 // something 2^9 times smaller than the rest of the state, and shows in dbeta and dgate, fp32
-// outputs (1e-6 to 3e-6 off with two parts, 2e-7 to 8e-7 with three).  The weighted scores enter in two parts: one
-// alone is a rounding as large as the output's own (2.3e-3 off against 1.7e-3, and up to
-// twice that in sequences of a few tokens, whose rows are few products), and two cost
-// 4 % (B8 H8 T2048 D128 kernel 49 -> 51 us, B1 H8 T131072 269 -> 281).
+// outputs (1e-6 to 3e-6 off with two parts, 2e-7 to 8e-7 with three).  The weighted scores
+// enter in three for the same reason: a write that the next token takes back leaves a
+// difference of weights, which two parts hold to 2^-17 of either (one part is a rounding as large
+// as the output's own).  What is left of the difference from fp32 arithmetic is the hardware's
+// exponential (2^-22).  B8 H8 T2048 D128, kernel: state and scores in two parts 50 us, the
+// state in three 54, both in three 57.
 //
 // Roles (640 threads, one CTA an SM).  What follows at -> is a barrier and who waits:
 //   warp 18      loads x (one stage), y (two) -> 17;  z (two) -> 17, 8-15;  decay tables (four)
@@ -31,8 +33,8 @@
 //   warp 16      OS -> 0-7, 17;  DS -> 8-15
 //   warps 0-7    P -> weighted scores in TMEM (thread: a token, 64 columns) -> 17;
 //                a OS + OI -> rows staged where z was -> 19
-//   warps 8-15   S as OS's operand -> 16;  parts of u z (once OS is done: the third lies where
-//                the state's third was) -> 16;  S' = b S + DS
+//   warps 8-15   S as OS's operand -> 16;  two parts of u z -> 16;  once OS is done, the third,
+//                which lies where the state's third was -> 16;  S' = b S + DS
 //   warp 19      rows out by TMA, z's stage free again -> 18
 // An operand's load is waited for by the issuer that reads it, or by a role whose arrival that
 // issuer waits for: y by 17, whose copies of x 16 waits for; z by 17 itself, since the state's
@@ -44,8 +46,9 @@
 // What decided the layout (cycles a chunk, B8 H8 T2048 D128, 1.9 GHz).
 // - An MMA with both operands in shared memory and N = 128 leaves the warps no bandwidth
 //   there: P took 1222.  X as a TMEM operand (copied once, used by P and OS) frees it.
-// - Parts of one operand are columns of one product (N = 192 for DS: y is read once)
-//   and their sums are taken in registers.
+// - Two parts of an operand are columns of one product (N = 128 for DS: y is read once); the
+//   third, which comes later, is added to the second's columns.  All three parts of u z held
+//   back until OS is done, in one product: 62 us, not 54.
 // - Issuing an MMA costs 33 from a converged warp under elect_one, 70 to 200 otherwise,
 //   hence a warp per queue and operand addresses that are constants.
 // - Rows leave through shared memory and TMA: a thread's 32 bytes of a row, stored from
@@ -95,7 +98,7 @@ struct LtSmem {
     // table floats, 128 tokens each: a, u, l (of the row), ta, c[3], and g (backward) or m (l
     // less log2 of the gate, of the column; forward); then b
     static constexpr uint32_t BARS = TAB + kLtTabs * 4 * kLtTabF;
-    static constexpr uint32_t TBASE = BARS + 8 * (20 + 2 * kLtTabs);      // TMEM base, abort flag
+    static constexpr uint32_t TBASE = BARS + 8 * (21 + 2 * kLtTabs);      // TMEM base, abort flag
     static constexpr uint32_t END = TBASE + 16;
     static constexpr size_t bytes = END + 1024;
 };
@@ -288,8 +291,9 @@ k_linear_tables(const float *__restrict__ beta, const float *__restrict__ gate, 
     if (lane < 4) ta[8 * kLtC] = lane ? 0.f : ex2(end.hi + end.lo);   // b
 }
 
-// (u z) of item i (16 bytes of a row) in three bf16 parts, 16 KB apart.
-__device__ __forceinline__ void lt_parts(const uint8_t *z, uint8_t *dst, float u) {
+// (u z) of item i (16 bytes of a row) in three bf16 parts: the first two stored 16 KB apart, the
+// third returned.
+__device__ __forceinline__ uint4 lt_parts(const uint8_t *z, uint8_t *dst, float u) {
     const uint4 w4 = *reinterpret_cast<const uint4 *>(z);
     const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
     uint32_t a[4], b[4], c[4];
@@ -303,7 +307,7 @@ __device__ __forceinline__ void lt_parts(const uint8_t *z, uint8_t *dst, float u
     }
     *reinterpret_cast<uint4 *>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
     *reinterpret_cast<uint4 *>(dst + LtSmem::HALF) = make_uint4(b[0], b[1], b[2], b[3]);
-    *reinterpret_cast<uint4 *>(dst + 2 * LtSmem::HALF) = make_uint4(c[0], c[1], c[2], c[3]);
+    return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
 // GRAD: the passes of the backward, which also keep the states and form dbeta's dots.
@@ -326,7 +330,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     const uint32_t b_xy = bars + 64, b_z = bars + 80, b_o = bars + 96, b_out = bars + 112,
                    b_fin = bars + 128;                                                        // [2]
     const uint32_t b_zfree = bars + 144;                                                      // [2]
-    const uint32_t b_w = bars + 160, b_tfree = b_w + 8 * kLtTabs;                             // [kLtTabs]
+    const uint32_t b_lo = bars + 160, b_w = bars + 168, b_tfree = b_w + 8 * kLtTabs;                             // [kLtTabs]
     uint32_t *tbase = reinterpret_cast<uint32_t *>(sm + L::TBASE);
     const uint32_t abort = sb + L::TBASE + 4;
     float *s_tab = reinterpret_cast<float *>(sm + L::TAB);
@@ -354,6 +358,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
         }
         lt_init(b_p, 1);
         lt_init(b_parts, 8);
+        lt_init(b_lo, 8);
         lt_init(b_s, 16);   // S staged, and the last chunk's OS read
         lt_init(b_pb, 8);
         lt_init(b_ds, 1);
@@ -382,8 +387,8 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     // those (x, y, z, beta) at once; the tables, the start states and the other direction's states
     // only after the wait (loader, state warps).
     griddep_launch_dependents();
-    // TMEM columns; the two bf16 parts of 16 weighted scores lie over those scores
-    constexpr uint32_t kP = 0, kOI = 128, kOS = 192, kDS = 256, kX = 448;
+    // TMEM columns; of the three bf16 parts of 16 weighted scores, two lie over those scores
+    constexpr uint32_t kP = 0, kOI = 128, kOS = 192, kDS = 256, kPL = 384, kX = 448;
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;              // TMEM lane: token of P, OI, OS; y row of S
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -394,7 +399,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     auto wait = [&](uint32_t bar, uint32_t parity) { return lt_wait_warp(bar, parity, abort); };
     constexpr uint32_t ID_P = tc::idesc_bf16(128, 128, false, false);
     constexpr uint32_t ID_O = tc::idesc_bf16(128, 64, false, true);
-    constexpr uint32_t ID_D = tc::idesc_bf16(128, 192, true, true);
+    constexpr uint32_t ID_D = tc::idesc_bf16(128, 128, true, true), ID_DL = tc::idesc_bf16(128, 64, true, true);
     // steps (in 16 bytes) from an operand's descriptor to its kk-th K step
     auto kmaj = [](int kk) { return (uint64_t)((kk >> 2) * (L::HALF / 16) + (kk & 3) * 2); };
     auto mnmaj = [](int kk) { return (uint64_t)(kk * 128); };
@@ -431,6 +436,15 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                     tc::mma_f16(tmem + kDS, y + mnmaj(kk), d_u + mnmaj(kk), ID_D, kk > 0);
+            }
+            ok = wait(b_lo, ph);
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (elect_one()) {   // the third part, onto the second's columns
+                const uint64_t y = d_y + st * (L::TILE / 16);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    tc::mma_f16(tmem + kDS + 64, y + mnmaj(kk), d_u + 2 * (L::HALF / 16) + mnmaj(kk), ID_DL, true);
                 lt_commit(b_ds);
                 lt_commit(b_o + 8 * st);
             }
@@ -480,8 +494,11 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             if (elect_one()) {
                 const uint64_t z = d_z + st * (L::HALF / 16);
 #pragma unroll
-                for (int kk = 0; kk < 16; ++kk)   // both parts of every 16 scores
+                for (int kk = 0; kk < 16; ++kk)   // the parts that lie over the scores, two for every 16
                     mma_bf16_ta(tmem + kOI, tmem + kP + kk * 8, z + mnmaj(kk >> 1), ID_O, kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)    // and the third
+                    mma_bf16_ta(tmem + kOI, tmem + kPL + kk * 8, z + mnmaj(kk), ID_O, true);
                 lt_commit(b_oi);
                 lt_commit(b_o + 8 * st);
             }
@@ -604,19 +621,22 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 if (!wait(b_w + 8 * ts, (it / kLtTabs) & 1) || !wait(b_p, ph)) break;
                 tc::fence_after_sync();
                 // 16 columns at a time, in a loop: straight-line code for all of them would not
-                // stay in the instruction caches.  Their two parts take the columns that they were in.
+                // stay in the instruction caches.  Two of their parts take the columns that they were in.
 #pragma unroll 1
                 for (int h = 0; h < 4; ++h) {
                     const int c0 = half * 64 + h * 16, cb = c0 >> 5;
-                    float pk[16];   // pairs of bf16 as 32-bit columns, then what their rounding left
+                    float pk[24];   // pairs of bf16 as 32-bit columns, then what their rounding left, twice
                     auto put = [&](int j, float2 x) {
-                        const uint32_t w = f2_bf16x2(x);
-                        pk[j] = __uint_as_float(w);
-                        pk[8 + j] = __uint_as_float(f2_bf16x2(f2_rest(x, w)));
+#pragma unroll
+                        for (int e = 0; e < 3; ++e) {
+                            const uint32_t w = f2_bf16x2(x);
+                            pk[8 * e + j] = __uint_as_float(w);
+                            x = f2_rest(x, w);
+                        }
                     };
                     if (REV ? cb < quarter : cb > quarter) {   // beyond the diagonal
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) pk[j] = 0.f;
+                        for (int j = 0; j < 24; ++j) pk[j] = 0.f;
                     } else {
                         float v[16];
                         tc::tmem_ld16(tl + kP + c0, v);
@@ -657,6 +677,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                         }
                     }
                     tc::tmem_st16(tl + kP + c0, pk);
+                    tc::tmem_st8(tl + kPL + c0 / 2, pk + 16);
                 }
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
@@ -755,13 +776,25 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 fence_proxy_async_smem();
                 arrive(b_s);
             }
-            ok = wait(b_w + 8 * ts, (it / kLtTabs) & 1) && wait(b_z + 8 * sg, (it >> 1) & 1) && wait(b_os, ph);
+            ok = wait(b_w + 8 * ts, (it / kLtTabs) & 1) && wait(b_z + 8 * sg, (it >> 1) & 1);
             if (!ok) break;
-#pragma unroll 1
-            for (int item = gt; item < 1024; item += kLtGroup)   // row item / 8
-                lt_parts(sm + L::Z + sg * L::HALF + item * 16, sm + L::PARTS + item * 16, tab[C + (item >> 3)]);
-            fence_proxy_async_smem();
-            arrive(b_parts);
+            {
+                uint4 lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int item = gt + i * kLtGroup;   // row item / 8
+                    lo[i] = lt_parts(sm + L::Z + sg * L::HALF + item * 16, sm + L::PARTS + item * 16, tab[C + (item >> 3)]);
+                }
+                fence_proxy_async_smem();
+                arrive(b_parts);
+                ok = wait(b_os, ph);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(sm + L::PARTS + 2 * L::HALF + (gt + i * kLtGroup) * 16) = lo[i];
+                fence_proxy_async_smem();
+                arrive(b_lo);
+            }
             const float b = tab[8 * C];
             if (GRAD && p.states && owns) {
                 float *dst = p.states + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
@@ -786,10 +819,6 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
             for (int h = 0; h < 32; h += 16) {
                 float v[16], w[16];
                 tc::tmem_ld16(tl + kDS + 64 + half * 32 + h, v);
-                tc::tmem_ld16(tl + kDS + 128 + half * 32 + h, w);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] += w[j];
                 tc::tmem_ld16(tl + kDS + half * 32 + h, w);
                 tc::tmem_wait_ld();
 #pragma unroll
@@ -936,8 +965,9 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int item = tid + i * 512;   // row item / 8
-                lt_parts(sm + L::Z + st * LtSmem::HALF + item * 16, sm + L::PARTS + item * 16,
-                         u[item >> 3] * far);
+                const uint4 lo = lt_parts(sm + L::Z + st * LtSmem::HALF + item * 16, sm + L::PARTS + item * 16,
+                                          u[item >> 3] * far);
+                *reinterpret_cast<uint4 *>(sm + L::PARTS + 2 * LtSmem::HALF + item * 16) = lo;
             }
             far *= u[kLtC];
             fence_proxy_async_smem();

@@ -45,3 +45,48 @@ def test_little_of_a_large_state(D, T):
     for n, a, X in (("dv", (zero, pair, zero), S), ("dk", (zero, zero, pair), R)):
         g = gka.gka_linear_backward(*a, one, zero, dfinal_state=X)
         assert near(g[n], want, terms, 2.0 ** -21), n
+
+
+def erasing(D, T, resets):
+    """Unit key e0, written with V and, one token on, with -V: what later tokens read of the pair is
+    2^-12 of either, by the decay between the two.  64 heads, the pair at another place in each.
+    Returns (rows e0 at the pair, rows +-V at the pair, rows e0 everywhere, the decays)."""
+    gen = torch.Generator().manual_seed(62 + T)
+    B, H = 2, 32
+    unit, value, read = (torch.zeros(B * H, T, D) for _ in range(3))
+    read[..., 0] = 1.0
+    for h in range(B * H):
+        i = 4 + (h * 29) % min(T - 6, 200)
+        unit[h, i:i + 2, 0] = 1.0
+        value[h, i] = torch.randn(D, generator=gen)
+        value[h, i + 1] = -value[h, i]
+    beta = 1 - 2.0 ** -12 * torch.rand(B * H, T, generator=gen)
+    beta[:, list(resets)] = 0.0
+    rows = [x.view(B, H, T, D).bfloat16().cuda() for x in (unit, value, read)]
+    return (*rows, beta.view(B, H, T).cuda())
+
+
+def check_erased(D, T, resets):
+    """Share: a weight's exponential is off by 2^-22, its parts by 2^-25, and the two terms' sum by
+    2^-23 of them, in the chunk and again in the state: below 2^-20 in all."""
+    unit, value, read, beta = erasing(D, T, resets)
+    share = 2.0 ** -20
+    o = gka.gka_linear_forward(read, unit, value, beta)
+    assert near(o, linear(read, unit, value, beta)[0], linear(read, unit, value.abs(), beta)[0], share)
+    # time reversed: two reads of opposite sign behind every write
+    back = [x.flip(2) for x in (unit, value, read)]
+    beta = beta.flip(2).contiguous()
+    cases = {"dq": (value * 0, value, unit, read), "dv": (back[0], back[2], value * 0, back[1]),
+             "dk": (back[1], value * 0, back[2], back[0])}   # q, k, v, dout
+    for n, (q, k, v, do) in cases.items():
+        b = beta if n != "dq" else beta.flip(2).contiguous()
+        got = gka.gka_linear_backward(q, k, v, b, do)[n]
+        want = linear_grad(q, k, v, b, do)[n]
+        terms = linear_grad(q.abs(), k.abs(), v.abs(), b, do.abs())[n]
+        assert near(got, want, terms, share), n
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("T", [40, 128, 300])
+def test_a_write_that_the_next_one_erases(D, T):
+    check_erased(D, T, ())
