@@ -223,10 +223,9 @@ static int lin_tc_tables(LinTcArgs &a, int passes, const LinLayout &L, char *ws,
     const LinPass &p = a.pass[0].p;
     float *tab = reinterpret_cast<float *>(ws + L.tab) + (REV ? (size_t)p.BH * L.N * kLtTabF : 0);
     for (int i = 0; i < passes; ++i) a.pass[i].tab = tab;
-    const long long chunks = (long long)p.BH * L.N;
     ProfScope ps(prof, s);
-    return launch_after(k_linear_tables<REV>, dim3((unsigned)((chunks + 7) / 8)), 256, 0, true, s, p.beta, p.gate,
-                        tab, p.BH, L.N, p.T, p.scale, p.log2_min);
+    return launch_after(k_linear_tables<REV>, dim3((unsigned)p.BH * (unsigned)L.N), 32, 0, true, s, p.beta, p.gate, tab,
+                        L.N, p.T, p.scale, p.log2_min);
 }
 
 // `pdl`: the kernel before is the tables'.

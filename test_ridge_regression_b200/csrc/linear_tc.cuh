@@ -27,7 +27,7 @@
 // state in three 54, both in three 57.
 //
 // Roles (640 threads, one CTA an SM).  What follows at -> is a barrier and who waits:
-//   warp 18      loads x (one stage), y (two) -> 17;  z (two) -> 17, 8-15;  decay tables (four)
+//   warp 18      loads x (one stage), y (two) -> 17;  z (two) -> 17, 8-15;  decay tables (three)
 //                -> 0-15
 //   warp 17      x from shared memory to TMEM, P -> 0-7;  OI -> 0-7
 //   warp 16      OS -> 0-7, 17;  DS -> 8-15
@@ -80,8 +80,9 @@ constexpr int kLtC = 128;                       // tokens per chunk
 constexpr int kLtZN = 64;                       // columns of z a CTA owns
 constexpr int kLtGroup = 256;                   // threads of an arithmetic group (two)
 constexpr int kLtThreads = 2 * kLtGroup + 128;  // + two issuers, the loader, the rows' store
-constexpr int kLtTabs = 4;                      // stages of decay tables
-constexpr int kLtTabF = 8 * kLtC + 4;           // floats of a table
+constexpr int kLtTabs = 3;                      // stages of decay tables
+constexpr int kLtTabB = 10 * kLtC;              // a table's b
+constexpr int kLtTabF = kLtTabB + 4;            // floats of a table
 constexpr int kLtDots = 2, kLtFdots = 8;        // planes of dot and fdot partials per column split
 constexpr uint32_t kLtProbes = 1u << 20;
 constexpr uint32_t kLtHintNs = 2000;            // a probe suspends its warp for up to this long
@@ -96,7 +97,8 @@ struct LtSmem {
     static constexpr uint32_t SOP = PARTS + 3 * HALF;     // hi, mid of the state
     static constexpr uint32_t TAB = SOP + 2 * HALF;       // decay tables of the chunks in flight
     // table floats, 128 tokens each: a, u, l (of the row), ta, c[3], and g (backward) or m (l
-    // less log2 of the gate, of the column; forward); then b
+    // less log2 of the gate, of the column; forward), what l and (forward) m are short of as
+    // one float; then b
     static constexpr uint32_t BARS = TAB + kLtTabs * 4 * kLtTabF;
     static constexpr uint32_t TBASE = BARS + 8 * (21 + 2 * kLtTabs);      // TMEM base, abort flag
     static constexpr uint32_t END = TBASE + 16;
@@ -229,19 +231,22 @@ __device__ __forceinline__ float2 f2_rest(float2 y, uint32_t w) {
 // Decay tables of every chunk, a warp each, into tab [B*H][N][kLtTabF] (LtSmem lists a table's
 // parts).  A kernel of its own: formed by a warp of the passes, chunk by chunk, they took 4500
 // to 6300 cycles a chunk (600 instructions that no cache held) and bounded those; this one is
-// 4.5 us (B8 H8 T2048; 4 KB a chunk, latency), most of it under the set-up of the pass.
-// grid ceil(B*H*N / 8), block 256.  Lane l holds tokens 32 j + l.
+// 3.5 us (B8 H8 T2048; 5 KB a chunk, latency), most of it under the set-up of the pass.
+// Differences of logs within a block of 32 tokens are of pairs: as single floats they were up to
+// 2^-17 off behind a reset in the block, 2^-12 behind thirty.
+// grid B*H*N, block 32 (a small block fits beside a pass that is still running: 8 chunks a block
+// were 1.3 to 2 us slower a call, all of them on the few SMs that the pass leaves free).  Lane l
+// holds tokens 32 j + l.
 template <bool REV>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32)
 k_linear_tables(const float *__restrict__ beta, const float *__restrict__ gate, float *__restrict__ tab,
-                int BH, int N, int T, float scale, float log2_min) {
+                int N, int T, float scale, float log2_min) {
     // once what came before is done, the pass after this one may begin: it reads that at once
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const long long c = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (c >= (long long)BH * N) return;
-    const int bh = (int)(c / N), n = (int)(c - (long long)bh * N), t0 = n * kLtC + lane;
+    const int lane = threadIdx.x;
+    const unsigned c = blockIdx.x;
+    const int bh = (int)(c / (unsigned)N), n = (int)(c - (unsigned)bh * (unsigned)N), t0 = n * kLtC + lane;
     const Log2Sum zero = {0.f, 0.f};
     float g[4];
     Log2Sum l[4], e[4], end = zero;   // e[b]: cumulative log at the end of block b
@@ -261,11 +266,11 @@ k_linear_tables(const float *__restrict__ beta, const float *__restrict__ gate, 
             if (lane >= o) l[j] = l[j] + y;
         }
     }
-    float lb[4];   // from the block's start
+    Log2Sum lb[4];   // from the block's start
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const Log2Sum c2 = end + l[j];
-        lb[j] = l[j].hi + l[j].lo;
+        lb[j] = l[j];
         end = end + shfl(l[j], 31);
         l[j] = c2;
         e[j] = end;
@@ -274,21 +279,25 @@ k_linear_tables(const float *__restrict__ beta, const float *__restrict__ gate, 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float to = exp2_diff(l[j], zero), from = exp2_diff(end, l[j]);
-        const float v[8] = {
+        Log2Sum m = lb[j];
+        if (!REV && gate)   // a closed gate's m, +inf, weighs 0
+            m = g[j] == 0.f ? Log2Sum{INFINITY, 0.f} : m + Log2Sum{-log2f(g[j]), 0.f};
+        const float v[10] = {
             REV ? from : scale * to,                       // a
             REV ? scale * to : g[j] * from,                // u
-            lb[j],                                         // l
-            REV ? exp2_diff(e[j], l[j]) : ex2(lb[j]),      // ta
+            lb[j].hi,                                      // l
+            REV ? exp2_diff(e[j], l[j]) : exp2_diff(lb[j], zero),   // ta
             // c: forward, c[b] serves block row b + 1, the blocks before it; backward, block row
             // b, the blocks after it (0 elsewhere, where it is not read)
             (REV ? j > 0 : j <= 0) ? (REV ? exp2_diff(l[j], e[0]) : g[j] * exp2_diff(e[0], l[j])) : 0.f,
             (REV ? j > 1 : j <= 1) ? (REV ? exp2_diff(l[j], e[1]) : g[j] * exp2_diff(e[1], l[j])) : 0.f,
             (REV ? j > 2 : j <= 2) ? (REV ? exp2_diff(l[j], e[2]) : g[j] * exp2_diff(e[2], l[j])) : 0.f,
-            REV ? g[j] : lb[j] - log2f(g[j])};             // g, or m: a closed gate's +inf weighs 0
+            REV ? g[j] : m.hi,                             // g, or m
+            lb[j].lo, m.lo};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ta[i * kLtC + 32 * j] = v[i];
+        for (int i = 0; i < (REV ? 9 : 10); ++i) ta[i * kLtC + 32 * j] = v[i];
     }
-    if (lane < 4) ta[8 * kLtC] = lane ? 0.f : ex2(end.hi + end.lo);   // b
+    if (lane < 4) ta[kLtTabB] = lane ? 0.f : ex2(end.hi + end.lo);   // b
 }
 
 // (u z) of item i (16 bytes of a row) in three bf16 parts: the first two stored 16 KB apart, the
@@ -642,21 +651,27 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                         tc::tmem_ld16(tl + kP + c0, v);
                         if (cb == quarter) {
                             const float4 *w4 = reinterpret_cast<const float4 *>(tab + (REV ? 2 : 7) * C + c0);
-                            const float lt = tab[2 * C + row];
+                            const float4 *x4 = reinterpret_cast<const float4 *>(tab + (REV ? 8 : 9) * C + c0);
+                            // 2^(l_t - l_i) up to and including the token itself
+                            const float sgn = REV ? 1.f : -1.f, lt = -sgn * tab[2 * C + row], xt = -sgn * tab[8 * C + row];
                             const int first = lane - (h & 1) * 16;   // column of the token itself
                             tc::tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 16; j += 4) {
-                                const float4 c4 = w4[j / 4];
-                                float w[4] = {lt - c4.x, lt - c4.y, lt - c4.z, lt - c4.w};
+                                const float4 c4 = w4[j / 4], d4 = x4[j / 4];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    // 2^(l_t - l_i) up to and including the token itself
-                                    w[e] = ex2(REV ? -w[e] : w[e]) * v[j + e];
-                                    w[e] = (REV ? j + e >= first : j + e <= first) ? w[e] : 0.f;
+                                for (int e = 0; e < 4; e += 2) {
+                                    const float2 c = e ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
+                                    const float2 d = e ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y);
+                                    const float2 s2 = make_float2(sgn, sgn);
+                                    const float2 l2 = __fadd2_rn(__ffma2_rn(c, s2, make_float2(lt, lt)),
+                                                                 __ffma2_rn(d, s2, make_float2(xt, xt)));
+                                    float2 w = __fmul2_rn(make_float2(ex2(l2.x), ex2(l2.y)),
+                                                          make_float2(v[j + e], v[j + e + 1]));
+                                    w.x = (REV ? j + e >= first : j + e <= first) ? w.x : 0.f;
+                                    w.y = (REV ? j + e + 1 >= first : j + e + 1 <= first) ? w.y : 0.f;
+                                    put((j + e) / 2, w);
                                 }
-                                put(j / 2, make_float2(w[0], w[1]));
-                                put(j / 2 + 1, make_float2(w[2], w[3]));
                             }
                         } else {
                             const float4 *w4 = reinterpret_cast<const float4 *>(
@@ -795,7 +810,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                 fence_proxy_async_smem();
                 arrive(b_lo);
             }
-            const float b = tab[8 * C];
+            const float b = tab[kLtTabB];
             if (GRAD && p.states && owns) {
                 float *dst = p.states + ((size_t)bh * p.N + n) * D * D + (size_t)z0 * D + row;
 #pragma unroll
@@ -946,7 +961,7 @@ k_linear_agg_tc(const __grid_constant__ LinTcPass A, int *__restrict__ timeout_f
                 if (it == 0) griddep_wait();   // the tables' kernel is done
                 const float *tab = A.tab + ((size_t)bh * p.N + chunk(it)) * kLtTabF;
                 lt_bulk_load(sb + L::U + st * (4 * kLtC + 16), tab + kLtC, 4 * kLtC, b_yz + 8 * st);
-                lt_bulk_load(sb + L::U + st * (4 * kLtC + 16) + 4 * kLtC, tab + 8 * kLtC, 16, b_yz + 8 * st);
+                lt_bulk_load(sb + L::U + st * (4 * kLtC + 16) + 4 * kLtC, tab + kLtTabB, 16, b_yz + 8 * st);
                 ++loads;
             }
             if (!ok)
