@@ -3,7 +3,7 @@ are sums of are as near as their own rounding, like those of fp32 arithmetic on 
 import pytest
 import torch
 
-from linear_ref import linear, linear_grad
+from linear_ref import linear, linear_grad, linear_inputs
 from test_ridge_regression_b200 import build, gka
 
 pytestmark = pytest.mark.gpu
@@ -101,3 +101,25 @@ def test_decays_keep_their_bits_behind_resets(D, T, resets):
     """A reset is the largest decay that is told apart: sums of decays behind it still hold those
     between two tokens to fp32's bits."""
     check_erased(D, T, resets)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("T,gate,state", [(1, False, True), (37, True, False), (129, False, False), (400, True, True)])
+def test_every_element(D, T, gate, state):
+    """Random inputs, packed documents.  Share: two exponentials (2^-21), three parts (2^-25), 24
+    steps of the tensor cores' sum, each off by at most 2^-23 of the terms (2^-18.4), the state's
+    sum over four chunks (2^-21): below 2^-17."""
+    a, kw, gen = linear_inputs(2, 3, T, D, torch.bfloat16, 71 + T, gate=gate, state=state, resets=(5, 64, 300))
+    share, sc, g, S = 2.0 ** -17, kw["scale"], kw.get("gate"), kw.get("state")
+    o = gka.gka_linear_forward(*a.values(), gate=g, scale=sc, initial_state=S)
+    sizes = [x.abs() for x in a.values()]
+    up = None if S is None else S.abs()
+    assert near(o, linear(*a.values(), g, sc, S)[0], linear(*sizes, g, sc, up)[0], share)
+    do = torch.randn(a["q"].shape, generator=gen).bfloat16().cuda()
+    got = gka.gka_linear_backward(*a.values(), do, gate=g, scale=sc, initial_state=S, dfinal_state=S)
+    want = linear_grad(*a.values(), do, g, sc, S, S)
+    terms = linear_grad(*sizes, do.abs(), g, sc, up, up)
+    # 2^-60 of what was written passes a reset
+    written = 2.0 ** -60 * sum(float(x.double().abs().sum()) for x in (*a.values(), do))
+    for n in ("dq", "dk", "dv"):
+        assert near(got[n], want[n], terms[n] + written / share, share), n
