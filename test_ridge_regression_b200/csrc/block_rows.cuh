@@ -18,11 +18,12 @@
 // many), so that it touches kilobytes in a run on either side, and finds the tile with
 // one division.  A lane group's rows (RPT) are all loaded before the first is used; more
 // of them, or fewer, were slower (block_out and block_in's gradient: 1, 2, 4 rows 27, 25,
-// 30 us and 70, 55, 68).  bf16 B8 T2048 H8 D128, with gate, z and skip:
-//   block_in       32 us, 203 MB, 96 % of the copy rate (a division a row: 88)
-//   its gradient   55 us, 271 MB, 76 %: issue slots 75 % used
-//   block_out      25 us, 134 MB, 83 % (row by row: 43)
-//   its gradient   50 us, 235 MB, 73 %: 117 registers for dw and the next rows, two CTAs an SM
+// 30 us and 70, 55, 68).  bf16 B8 T2048 H8 D128, with gate, z and skip (fp32: 62, 90, 44, 84 us,
+// 87 % of the copy rate and more):
+//   block_in       32 us, 203 MB, 98 % of the copy rate (a division a row: 88)
+//   its gradient   54 us, 271 MB, 77 %: issue slots 75 % used
+//   block_out      25 us, 134 MB, 84 % (row by row: 43)
+//   its gradient   51 us, 235 MB, 71 %: 115 registers for dw and the next rows, two CTAs an SM
 // All sums are fp32; the gradients of what is shared by many rows (biases, w, skip) are
 // summed per block and then over the blocks in a fixed order, so results do not
 // depend on scheduling.

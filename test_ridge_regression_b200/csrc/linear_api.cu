@@ -54,8 +54,8 @@ struct LinLayout {
 
 // Segments per sequence: enough CTAs for every SM, whole chunks each.  A few chunks in a row are
 // faster than the two launches more: 4 heads of D = 128, device time without and with segments, on
-// the tensor cores 4 chunks 13.9 and 16.4 us (gradients 42 and 53), 6 chunks 18.4 and 16.7 (57
-// and 54); on CUDA cores 2 chunks 18.0 and 20.7, 4 chunks 35 and 21.
+// the tensor cores 5 chunks 18.2 and 17.2 us (gradients 49 and 54), 6 chunks 20.9 and 17.3 (56
+// and 54); on CUDA cores 2 chunks 21.2 and 24.4 (47 and 48), 3 chunks 29 and 24.5 (66 and 49).
 static int lin_segments(int ctas, int N, int D, bool tc) {
     const int S = ctas > 0 ? kSms * (tc ? 1 : lin_per_sm(D)) / ctas : 1;
     return N <= (tc ? 5 : 2) ? 1 : std::max(1, std::min(S, N));

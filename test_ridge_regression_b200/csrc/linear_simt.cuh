@@ -192,7 +192,9 @@ struct LinPasses {
     LinPass pass[2];
 };
 
-// CTAs of k_linear_pass an SM holds.
+// CTAs of k_linear_pass an SM holds.  With these D = 128 spills 20 bytes (forward), 64 88 to 100, 32
+// 20 to 28, and all are faster than the smaller tiles that spilled less (B8 H8 T2048 624 -> 546,
+// 203 -> 176, 110 -> 98 us).  Without spills, three CTAs of D = 32 take 105 us, two of 64 171.
 __host__ __device__ constexpr int lin_per_sm(int D) { return D > 64 ? 2 : D > 32 ? 3 : 4; }
 
 // grid (passes * D / ZN, B*H, S), block kLinThreads.  OUT = false: the segments' aggregates
@@ -202,10 +204,11 @@ __host__ __device__ constexpr int lin_per_sm(int D) { return D > 64 ? 2 : D > 32
 // columns): a thread has SR x 4 of the state and, for the scores and the state's part of the
 // outputs, a 4 x 4 tile over a part of the sum, which shuffles join, since a 16-byte load is four
 // passes of shared memory whatever its lanes share.  Chunk n + 1's tiles and decays come from
-// memory, and its decay table is formed, while chunk n is worked on.  What bounds it: shared
-// memory (70 % of the cycles before those tiles, issue slots 50 %).  B2 H1 T88769 D128: 638 us with
-// the aggregates (whole sums a thread, 2 x 2 and 2 x 4: 730; 32 columns a CTA and tables between
-// the chunks: 1276), against 194 of FMAs at 60 TFLOP/s.
+// memory, and its decay table is formed, while chunk n is worked on.  What bounds it (D = 128):
+// shared memory 68 % of the cycles, issue slots 63 %, the fp32 pipe 47 %.  B2 H1 T88769 D128:
+// 635 us with the aggregates (whole sums a thread, 2 x 2 and 2 x 4: 730; 32 columns a CTA and
+// tables between the chunks: 1276), of which the recurrence's own 4 D^2 a token would be 194 at
+// 60 TFLOP/s; the aggregates and the chunks' scores are as much again.
 // Where few chunks are left a launch (T of some hundreds), the launches' latency.
 template <int D, bool REV, bool OUT>
 __global__ void __launch_bounds__(kLinThreads, lin_per_sm(D))

@@ -12,7 +12,7 @@
 // the heads alone fill the SMs); with D = 128 the two CTAs of a head read the same x
 // and y, the second time from L2.  Heads of 32 and 64 columns take the same tiles:
 // their boxes' missing columns read as zeros, the K steps and column halves beyond D
-// are not issued.  (On CUDA cores B8 H8 T2048 D64 took 345 us, here 46.)
+// are not issued.  (B8 H8 T2048 D64 took 345 us on CUDA cores, here 52.)
 //
 // Roundings.  bf16 inputs enter the products exactly.  The increments' weighted
 // rows u z are split into three bf16 parts (24 bits: the state is an fp32 one, and
@@ -24,7 +24,8 @@
 // difference of weights, which two parts hold to 2^-17 of either (one part is a rounding as large
 // as the output's own).  What is left of the difference from fp32 arithmetic is the hardware's
 // exponential (2^-22).  B8 H8 T2048 D128, kernel: state and scores in two parts 50 us, the
-// state in three 54, both in three 57.
+// state in three 54, both in three 56.  Rounded parts, not cut ones: cut, three hold an fp32
+// number to the bit, but the aggregates took 152 us, not 136, and the passes as long.
 //
 // Roles (640 threads, one CTA an SM).  What follows at -> is a barrier and who waits:
 //   warp 18      loads x (one stage), y (two) -> 17;  z (two) -> 17, 8-15;  decay tables (three)
@@ -55,15 +56,16 @@
 //   registers, are a pass of the memory pipe per row.
 // - Loops stay rolled: unrolled, the roles' code no longer fits the instruction caches
 //   together (no variant of it was faster).
-// - Sixteen warps for the outputs (registers split by role) were 7 % slower.
-// - Rows formed one chunk late, under the next chunk's OI and P: 6 % slower (two accumulators
-//   of OI and OS leave DS 64 columns, its parts one product each).
-// What bounds it: several chains from chunk to chunk of nearly one length, 4500 against 2900
-// of tensor work.  The outputs' warps: scores (1400), OI (700), rows (1000), hand-offs
-// (130 a satisfied wait); the state's: its operand, parts, DS, sum; loads, stores and hand-offs
-// alone: 29 us of the kernel's 49 (the bytes 21.5 at the copy rate).  No unit is full: tensor
-// pipe 47 % active, issue slots 50 %, the warps' shared memory accesses 26 %, its banks 16 %
-// reading and 13 % writing.
+// - With scores in two parts, sixteen warps for the outputs (registers split by role) were 7 %
+//   slower, and rows formed one chunk late, under the next chunk's OI and P, 6 %.
+// - OI begun on the first half of the scores while the second is formed: 5 % slower.
+// What bounds it: several chains from chunk to chunk of one length, 4800 against 3500 of tensor
+// work.  The outputs' warps: P (300 left to wait), scores (2200), OI (1500 with its hand-offs and
+// the products queued before it), rows (650); the state's: its operand (650), OS with its
+// hand-offs (2250, u z's first parts formed under it), the third part and DS (1700), sum (240).
+// Loads, stores and hand-offs alone: 29 us of the kernel's 56 (the bytes 21.5 at the copy rate).
+// No unit is full: tensor pipe 53 % active, issue slots 52 %, the warps' shared memory accesses
+// 27 %, its banks 18 % reading and 12 % writing.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -320,8 +322,7 @@ __device__ __forceinline__ uint4 lt_parts(const uint8_t *z, uint8_t *dst, float 
 }
 
 // GRAD: the passes of the backward, which also keep the states and form dbeta's dots.
-// B8 H8 T2048 D128: dq's pass 62 us, dv's and dk's 124 (256 CTAs, two waves on 148 SMs).
-// The state's third part over x's stage instead held back the next x: 14 and 6 % more.
+// B8 H8 T2048 D128: dq's pass 68 us, dv's and dk's 139 (256 CTAs, two waves on 148 SMs).
 // grid (lt_splits(D) * passes, B*H, S), block kLtThreads.
 template <bool REV, bool GRAD>
 __global__ void __launch_bounds__(kLtThreads, 1)
@@ -865,7 +866,7 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
 // over the segment (a chunk's u times the decay of the chunks between it and that end): one
 // product per chunk into the same accumulators, with nothing of the state in between.  Warps
 // 0-15 form the weighted rows (as in k_linear_tc), warp 16 issues, warp 18 loads.  B1 H8
-// T131072 D128: 145 us for 538 MB (58 % of the copy rate); the parts (48 KB of shared
+// T131072 D128: 136 us for 538 MB (61 % of the copy rate); the parts (48 KB of shared
 // memory written a chunk) and the product follow one another, 2400 cycles a chunk.
 struct LaSmem {
     static constexpr int ST = 3;                                 // stages of loads
