@@ -309,7 +309,8 @@ int gka_solver_study(const void *q, const void *k, const float *beta, const floa
  *               (0 bytes for some sizes: then NULL will do)
  * B*H is at most 65535.  The state is carried in fp32.  With bf16 inputs the products
  * run on the tensor cores (fp32 accumulation): inputs enter exactly, the state, its
- * increments and the decayed scores in three bf16 parts (24 bits).  fp32 inputs run on CUDA cores in fp32.
+ * increments and the decayed scores in three bf16 parts (24 bits).  fp32 inputs run on
+ * CUDA cores in fp32.
  */
 size_t gka_linear_forward_workspace_bytes(int B, int H, int T, int D, gka_dtype dt);
 int gka_linear_forward(const void *q, const void *k, const void *v, const float *beta,

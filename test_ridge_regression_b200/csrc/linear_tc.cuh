@@ -340,7 +340,8 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
     const uint32_t b_xy = bars + 64, b_z = bars + 80, b_o = bars + 96, b_out = bars + 112,
                    b_fin = bars + 128;                                                        // [2]
     const uint32_t b_zfree = bars + 144;                                                      // [2]
-    const uint32_t b_lo = bars + 160, b_w = bars + 168, b_tfree = b_w + 8 * kLtTabs;                             // [kLtTabs]
+    const uint32_t b_lo = bars + 160;
+    const uint32_t b_w = bars + 168, b_tfree = b_w + 8 * kLtTabs;                             // [kLtTabs]
     uint32_t *tbase = reinterpret_cast<uint32_t *>(sm + L::TBASE);
     const uint32_t abort = sb + L::TBASE + 4;
     float *s_tab = reinterpret_cast<float *>(sm + L::TAB);
@@ -653,8 +654,10 @@ k_linear_tc(const __grid_constant__ LinTcArgs args, int *__restrict__ timeout_fl
                         if (cb == quarter) {
                             const float4 *w4 = reinterpret_cast<const float4 *>(tab + (REV ? 2 : 7) * C + c0);
                             const float4 *x4 = reinterpret_cast<const float4 *>(tab + (REV ? 8 : 9) * C + c0);
-                            // 2^(l_t - l_i) up to and including the token itself
-                            const float sgn = REV ? 1.f : -1.f, lt = -sgn * tab[2 * C + row], xt = -sgn * tab[8 * C + row];
+                            // 2^(l_t - l_i) (backward: its inverse) up to and including the token
+                            // itself; l and what it is short of apart, so that differences keep their bits
+                            const float sgn = REV ? 1.f : -1.f;
+                            const float lt = -sgn * tab[2 * C + row], xt = -sgn * tab[8 * C + row];
                             const int first = lane - (h & 1) * 16;   // column of the token itself
                             tc::tmem_wait_ld();
 #pragma unroll
